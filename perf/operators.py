@@ -338,8 +338,8 @@ def nearest(x, fmt, rule):
     emax = {"e2m1": 2, "e4m3": 8, "e5m2": 15}[fmt]
     b = x.view(rows, cols // 32, 32)
     amax = b.abs().amax(-1)
-    bound = (grid[-1] * 2.0 ** torch.arange(-127, 128, dtype=torch.float64, device=x.device) if rule == "ceil"
-             else 2.0 ** torch.arange(-126 + emax, 129 + emax, dtype=torch.float64, device=x.device))
+    power = torch.arange(-127, 128, device=x.device)
+    bound = times_pow2(grid[-1], power) if rule == "ceil" else times_pow2(grid.new_ones(()), power[1:] + emax)
     # ceil: the first exponent whose largest value is not below amax; floor: the first whose next binade is above it
     e = torch.searchsorted(bound, amax, right=rule == "floor").clamp(max=254) - 127
     v = times_pow2(b, -e.unsqueeze(-1))
