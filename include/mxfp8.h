@@ -75,7 +75,9 @@ typedef enum {
   MXFP8_ERR_DEVICE = 7  /* the HIP runtime reported an error at launch */
 } mxfp8_status;
 
-typedef enum { MXFP8_E4M3 = 0, MXFP8_E5M2 = 1 } mxfp8_fmt; /* OCP encodings [FP8F] */
+/* OCP encodings [FP8F]; E2M1 (4 bits: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives) where an entry point says so. */
+typedef enum { MXFP8_E4M3 = 0, MXFP8_E5M2 = 1, MXFP8_E2M1 = 2 } mxfp8_fmt;
 typedef enum { MXFP8_F32 = 0, MXFP8_BF16 = 1 } mxfp8_dtype;
 typedef enum { MXFP8_GROUP_ROW = 0, MXFP8_GROUP_COL_T = 1 } mxfp8_axis;
 typedef enum { MXFP8_RULE_CEIL = 0, MXFP8_RULE_FLOOR = 1 } mxfp8_rule;
@@ -305,6 +307,137 @@ int mx_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, int 
 int gaussws_sample(const void* w, int w_dtype, int64_t rows, int64_t cols, int64_t ldw,
                    const int8_t* bitwidths, uint64_t seed, uint64_t stream_id, uint16_t* w_hat,
                    int64_t ldo, void* stream);
+
+/*
+ * The MX operators below work on 32-element blocks with one E8M0 scale byte
+ * (as mx_quantize) and add to its formats E2M1: two codes to a byte, the even
+ * element in the low four bits; a row of n elements takes n / 2 bytes, and the
+ * leading dimension of an E2M1 matrix counts BYTES (a multiple of 16).
+ *
+ * Non-finite values: a block that holds an infinity or a NaN gets the scale
+ * byte 255 (the E8M0 NaN) and zero codes; mx_dequantize, mx_requantize_t, the
+ * backward passes and the matrix products read every element of such a block
+ * as NaN.
+ *
+ * `rule` is as for mx_quantize: MXFP8_RULE_CEIL (the smallest e with
+ * amax <= fmax * 2^e; nothing saturates) or MXFP8_RULE_FLOOR (floor(log2
+ * amax) - emax, emax = 2 for E2M1, 8 for E4M3, 15 for E5M2; saturating).
+ */
+
+/*
+ * mxfp4_quantize -- MX blocks of 32 along rows, E2M1 codes.
+ *   x:      [rows][ldx >= cols] fp32 or bf16.
+ *   q:      [rows][ldq >= cols / 2 bytes] codes.
+ *   scales: [rows][cols / 32].
+ * Requires cols % 32 == 0.
+ */
+int mxfp4_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, int rule, uint8_t* q,
+                   int64_t ldq, uint8_t* scales, void* stream);
+
+/*
+ * mx_dequantize -- the values that MX codes stand for: y = dec(q) * 2^(s - 127),
+ * as fp32 (exact within fp32's range) or rounded to bf16.
+ *   q: [rows][ldq] codes of fmt (E4M3, E5M2 or E2M1); scales [rows][cols / 32].
+ *   y: [rows][ldy >= cols] fp32 or bf16.
+ * Requires cols % 32 == 0.
+ */
+int mx_dequantize(const uint8_t* q, int64_t ldq, int fmt, const uint8_t* scales, int64_t rows, int64_t cols,
+                  void* y, int y_dtype, int64_t ldy, void* stream);
+
+/*
+ * mx_quantize_t -- MX blocks of 32 consecutive rows (tokens) down each column,
+ * codes written transposed: the operand of a product whose K axis is the row
+ * axis (the weight gradient; a weight [out][in] for the data gradient).
+ *   x:        [rows][ldx >= cols] fp32 or bf16.
+ *   qt:       [cols][ldqt] codes of fmt (E4M3, E5M2 or E2M1), rows_out of them
+ *             per column: rows beyond `rows` are zeros, so that a token count
+ *             can be filled up to the K that a product takes.
+ *   scales_t: [cols][rows_out / 32].
+ * Requires cols % 16 == 0, rows_out % 32 == 0, rows_out >= rows, and at most
+ * 2^23 - 1 tiles of 128 x 128.
+ */
+int mx_quantize_t(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, int fmt, int rule,
+                  uint8_t* qt, int64_t ldqt, int64_t rows_out, uint8_t* scales_t, void* stream);
+
+/*
+ * mx_requantize_t -- mx_quantize_t of a matrix held as FP8 MX codes (blocks
+ * along rows), such as an activation kept for the backward pass: the values
+ * are decoded, put into blocks of 32 rows and rounded once more.
+ *   q: [rows][ldq >= cols] codes of q_fmt (E4M3 or E5M2); scales [rows][cols / 32].
+ * Requires cols % 32 == 0 and otherwise what mx_quantize_t requires.
+ */
+int mx_requantize_t(const uint8_t* q, int64_t ldq, int q_fmt, const uint8_t* scales, int64_t rows, int64_t cols,
+                    int fmt, int rule, uint8_t* qt, int64_t ldqt, int64_t rows_out, uint8_t* scales_t, void* stream);
+
+/*
+ * mxfp4_gemm -- C = A * B^T with B in E2M1 and A in E2M1, E4M3 or E5M2, one
+ * E8M0 scale per 32 consecutive elements along K for both, fp32 accumulation:
+ *
+ *   C[m][n] = sum over 32-wide K blocks j of
+ *             2^(sa[m][j] - 127) * 2^(sb[n][j] - 127) *
+ *             sum_{k in j} dec(A[m][k]) * dec(B[n][k]).
+ *
+ * a: [M][lda] codes (a_fmt), a_scales [M][K / 32].
+ * b: [N][ldb >= K / 2 bytes] E2M1 codes, b_scales [N][K / 32].
+ * c: [M][ldc >= N], fp32 or bf16 (c_dtype), overwritten.
+ * Requires K % 128 == 0, 4-byte aligned scale pointers, lda and ldb <= 2^24;
+ * M and N are arbitrary.  Accuracy as for mx_gemm.
+ */
+int mxfp4_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, int a_fmt, const uint8_t* a_scales,
+               const uint8_t* b, int64_t ldb, const uint8_t* b_scales, void* c, int64_t ldc, int c_dtype,
+               void* stream);
+
+/*
+ * mx_swiglu_forward -- h = silu(g) * u, silu(g) = g / (1 + exp(-g)), of
+ * x = (g, u): [rows][ldx >= 2 cols] fp32 or bf16, g the first cols columns.
+ * Computed in fp32 and written as MX codes along rows:
+ *   h:    [rows][ldh >= cols] codes of fmt (E4M3 or E5M2), h_scales [rows][cols / 32].
+ *   kept: [rows][ldk >= 2 cols] codes of x itself, kept_scales [rows][2 cols / 32],
+ *         for mx_swiglu_backward.  Both NULL: nothing is kept (inference).
+ * Requires cols % 32 == 0.
+ */
+int mx_swiglu_forward(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, int fmt, int rule,
+                      uint8_t* h, int64_t ldh, uint8_t* h_scales, uint8_t* kept, int64_t ldk, uint8_t* kept_scales,
+                      void* stream);
+
+/*
+ * mx_swiglu_backward -- the gradient of h at the kept values (g, u):
+ *   s = 1 / (1 + exp(-g)),  dg = dh * u * s * (1 + g * (1 - s)),  du = dh * g * s.
+ *   dh: [rows][lddh >= cols], dx: [rows][lddx >= 2 cols] = (dg, du), both of `dtype`.
+ */
+int mx_swiglu_backward(const uint8_t* kept, int64_t ldk, const uint8_t* kept_scales, int fmt, const void* dh,
+                       int dtype, int64_t lddh, int64_t rows, int64_t cols, void* dx, int64_t lddx, void* stream);
+
+/*
+ * mx_rmsnorm_forward -- y = x * r * w, r = 1 / sqrt(mean over the row of x^2 + eps),
+ * computed in fp32 and written as MX codes along rows.
+ *   x: [rows][ldx >= cols] fp32 or bf16;  w: [cols] fp32, 16-byte aligned;  eps >= 0 and finite.
+ *   y: [rows][ldy >= cols] codes of fmt (E4M3 or E5M2), y_scales [rows][cols / 32].
+ *   kept: [rows][ldk >= cols] codes of x, kept_scales [rows][cols / 32], and
+ *         rstd: [rows] fp32 = r, for mx_rmsnorm_backward.  All three NULL:
+ *         nothing is kept (inference).
+ * Requires cols % 32 == 0 and cols <= 32768 (a row stays in registers).
+ */
+int mx_rmsnorm_forward(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const float* w,
+                       float eps, int fmt, int rule, uint8_t* y, int64_t ldy, uint8_t* y_scales, uint8_t* kept,
+                       int64_t ldk, uint8_t* kept_scales, float* rstd, void* stream);
+
+/*
+ * mx_rmsnorm_backward -- the gradients of y at the kept values x~, r the one
+ * of the forward pass:
+ *   xh = x~ * r,  c = dy * w,  dx = r * (c - xh * mean over the row of c * xh),
+ *   dw = sum over rows of dy * xh.
+ *   dy: [rows][lddy >= cols], dx: [rows][lddx >= cols], both of `dtype`;  dw: [cols] fp32.
+ *   workspace: mx_rmsnorm_backward_workspace(rows, cols) bytes, 16-byte
+ *   aligned, used only during the call.
+ * dw is summed in a fixed order: the same inputs give the same bits.  With
+ * rows == 0, dw is set to zero.
+ */
+int mx_rmsnorm_backward(const uint8_t* kept, int64_t ldk, const uint8_t* kept_scales, const float* rstd, int fmt,
+                        const float* w, const void* dy, int dtype, int64_t lddy, int64_t rows, int64_t cols,
+                        void* dx, int64_t lddx, float* dw, void* workspace, void* stream);
+/* Bytes of workspace; 0 for extents that mx_rmsnorm_backward refuses or that need none. */
+int64_t mx_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
 
 /* Static description of a status code (never NULL). */
 const char* mxfp8_status_string(int status);

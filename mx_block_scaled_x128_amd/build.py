@@ -18,7 +18,9 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmxfp8.so")
 ARCH = "gfx950"
 # (source, extra flags, object name)
-UNITS = [("api.cpp", [], "api"), ("quant.hip", [], "quant"), ("gaussws.hip", [], "gaussws"),
+UNITS = [("api.cpp", [], "api"), ("mx_api.cpp", [], "mx_api"), ("mx_quant.hip", [], "mx_quant"),
+         ("mx_act.hip", [], "mx_act"), ("mxfp4_gemm.hip", [], "mxfp4_gemm"),
+         ("quant.hip", [], "quant"), ("gaussws.hip", [], "gaussws"),
          ("gemm.hip", ["-DMXFP8_GEMM_FMT=-1"], "gemm_dispatch")] + \
         [("gemm.hip", ["-DMXFP8_GEMM_FMT=%d" % k], "gemm_fmt%d" % k) for k in range(4)]
 

@@ -1,0 +1,495 @@
+// mx_act.hip -- SwiGLU and RMSNorm that keep their input in 8 bits for the
+// backward pass (gfx950).
+//
+// Forward, per row of x:
+//   SwiGLU   x = (g, u),  h = g * sigma(g) * u,  sigma(g) = 1 / (1 + 2^(-g log2 e))
+//   RMSNorm  r = 1 / sqrt(mean(x^2) + eps),  y = x * r * w
+// h and y leave as MX codes (32-element blocks, one E8M0 scale), the operand
+// of the product that follows; x itself is kept as MX codes (RMSNorm: and r)
+// in place of the 16- or 32-bit tensor.
+//
+// Backward, on the kept values x~ (codes times scales):
+//   SwiGLU   dg = dh * u~ * sigma * (1 + g~ * (1 - sigma)),  du = dh * g~ * sigma
+//   RMSNorm  c = dy * w,  xh = x~ * r,  dx = r * (c - xh * mean(c * xh)),
+//            dw = sum over rows of dy * xh
+// All arithmetic is in fp32; the codes and the gradients' own type are the
+// only roundings.  Each tensor is read and written once: HBM bounds all four.
+#include "mx_common.hpp"
+#include "mx_launch.hpp"
+
+namespace mxfp8 {
+
+namespace mx_act_detail {
+
+constexpr int kThreads = 256;
+constexpr uint32_t kMaxBlocks = 256 * 8;
+
+// sigma(g).  exp2 and rcp are the hardware's (1 ulp each); the argument's own
+// rounding puts a relative error of |g| * 2^-24 on top.  2^(-g log2 e) = inf
+// for very negative g gives 0.
+__device__ __forceinline__ float sigmoid(float g) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896341f));
+}
+
+template <typename InT, int FMT, bool CEIL, bool KEEP, int U, bool NT>
+__global__ __launch_bounds__(kThreads) void swiglu_forward_kernel(
+    const InT* __restrict__ x, int64_t ldx, int64_t rows, uint32_t upr, uint8_t* __restrict__ h, int64_t ldh,
+    uint8_t* __restrict__ hs, uint8_t* __restrict__ kept, int64_t ldk, uint8_t* __restrict__ ks) {
+  const uint32_t lane = threadIdx.x & 63;
+  const uint32_t wave = blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t nwaves = gridDim.x * (kThreads / 64);
+  const uint32_t cols = upr * 8, nb = upr >> 2;
+  // items of 64 U units of one row; a wave's item is uniform
+  const uint32_t ipr = (upr + 64 * U - 1) / (64 * U);
+  const int64_t items = rows * ipr;
+  for (int64_t it = wave; it < items; it += nwaves) {
+    const int64_t row = it <= (int64_t)UINT32_MAX ? (int64_t)((uint32_t)it / ipr) : it / ipr;
+    const uint32_t unit0 = (uint32_t)(it - row * ipr) * (64 * U) + lane;
+    const InT* xr = x + row * ldx;
+    MxRaw<InT> rg[U], ru[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const uint32_t unit = unit0 + i * 64;
+      if (unit < upr) {
+        mx_load_raw<NT>(xr + unit * 8, rg[i]);
+        mx_load_raw<NT>(xr + cols + unit * 8, ru[i]);
+      } else {
+        mx_zero_raw(rg[i]);
+        mx_zero_raw(ru[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const uint32_t unit = unit0 + i * 64;
+      float g[8], u[8], v[8];
+      mx_unpack(rg[i], g);
+      mx_unpack(ru[i], u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = g[j] * sigmoid(g[j]) * u[j];
+      const MxScale sv = mx_scale<FMT, CEIL>(max_quad(absmax8(v)));
+      if constexpr (KEEP) {
+        const MxScale sg = mx_scale<FMT, CEIL>(max_quad(absmax8(g)));
+        const MxScale su = mx_scale<FMT, CEIL>(max_quad(absmax8(u)));
+        if (unit < upr) {
+          uint8_t* kr = kept + row * ldk;
+          mx_store_codes8<FMT>(kr + unit * 8, mx_codes8<FMT, CEIL>(g, sg));
+          mx_store_codes8<FMT>(kr + cols + unit * 8, mx_codes8<FMT, CEIL>(u, su));
+          if ((lane & 3) == 0) {
+            ks[row * (2 * nb) + (unit >> 2)] = (uint8_t)sg.byte;
+            ks[row * (2 * nb) + nb + (unit >> 2)] = (uint8_t)su.byte;
+          }
+        }
+      }
+      if (unit < upr) {
+        mx_store_codes8<FMT>(h + row * ldh + unit * 8, mx_codes8<FMT, CEIL>(v, sv));
+        if ((lane & 3) == 0) hs[row * nb + (unit >> 2)] = (uint8_t)sv.byte;
+      }
+    }
+  }
+}
+
+template <typename T, int FMT, int U, bool NT>
+__global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(
+    const uint8_t* __restrict__ kept, int64_t ldk, const uint8_t* __restrict__ ks, const T* __restrict__ dh,
+    int64_t lddh, int64_t rows, uint32_t upr, T* __restrict__ dx, int64_t lddx) {
+  const uint32_t lane = threadIdx.x & 63;
+  const uint32_t wave = blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t nwaves = gridDim.x * (kThreads / 64);
+  const uint32_t cols = upr * 8, nb = upr >> 2;
+  const uint32_t ipr = (upr + 64 * U - 1) / (64 * U);
+  const int64_t items = rows * ipr;
+  for (int64_t it = wave; it < items; it += nwaves) {
+    const int64_t row = it <= (int64_t)UINT32_MAX ? (int64_t)((uint32_t)it / ipr) : it / ipr;
+    const uint32_t unit0 = (uint32_t)(it - row * ipr) * (64 * U) + lane;
+    uint2 wg[U], wu[U];
+    uint32_t bg[U], bu[U];
+    MxRaw<T> rd[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const uint32_t unit = unit0 + i * 64;
+      wg[i] = wu[i] = make_uint2(0u, 0u);
+      bg[i] = bu[i] = 0;
+      mx_zero_raw(rd[i]);
+      if (unit < upr) {
+        wg[i] = mx_load_codes8<FMT>(kept + row * ldk + unit * 8);
+        wu[i] = mx_load_codes8<FMT>(kept + row * ldk + cols + unit * 8);
+        bg[i] = ks[row * (2 * nb) + (unit >> 2)];
+        bu[i] = ks[row * (2 * nb) + nb + (unit >> 2)];
+        mx_load_raw<NT>(dh + row * lddh + unit * 8, rd[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const uint32_t unit = unit0 + i * 64;
+      float g[8], u[8], d[8], dg[8], du[8];
+      mx_decode8<FMT>(wg[i], mx_factor(bg[i]), g);
+      mx_decode8<FMT>(wu[i], mx_factor(bu[i]), u);
+      mx_unpack(rd[i], d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float s = sigmoid(g[j]);
+        const float a = d[j] * s;
+        du[j] = a * g[j];
+        dg[j] = a * u[j] * __builtin_fmaf(g[j], 1.0f - s, 1.0f);
+      }
+      if (unit < upr) {
+        mx_store8(dx + row * lddx + unit * 8, dg);
+        mx_store8(dx + row * lddx + cols + unit * 8, du);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// RMSNorm.  wpr waves share a row (1 up to 4096 columns, 4 up to 16384, then
+// 16), each lane holding NU units of 8 elements, 64 wpr units apart: the row stays
+// in registers between its sum and its output, and the lane's columns of w
+// (and of dw) stay the same for every row, so they are read (and written) once
+// per wave.  Workgroups walk rows with a fixed stride.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+  return v;
+}
+// Sum over the waves of one row, the same order in each of them.
+__device__ __forceinline__ float row_sum(float v, uint32_t wpr, uint32_t wave, float* red) {
+  v = wave_sum(v);
+  if (wpr > 1) {
+    __syncthreads();  // red of the row before has been read
+    if ((threadIdx.x & 63) == 0) red[wave] = v;
+    __syncthreads();
+    const uint32_t first = wave / wpr * wpr;
+    v = 0.0f;
+    for (uint32_t i = 0; i < wpr; ++i) v += red[first + i];
+  }
+  return v;
+}
+
+__device__ __forceinline__ void load_w(const float* __restrict__ w, uint32_t unit, uint32_t upr, float (&f)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+  if (unit < upr) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = w[unit * 8 + j];
+  }
+}
+
+template <typename InT, int FMT, bool CEIL, int NU, int THREADS>
+__global__ __launch_bounds__(THREADS) void rmsnorm_forward_kernel(
+    const InT* __restrict__ x, int64_t ldx, int64_t rows, uint32_t upr, uint32_t wpr, const float* __restrict__ w,
+    float eps, uint8_t* __restrict__ y, int64_t ldy, uint8_t* __restrict__ ys, uint8_t* __restrict__ kept, int64_t ldk,
+    uint8_t* __restrict__ ks, float* __restrict__ rstd) {
+  __shared__ float red[16];
+  const uint32_t lane = threadIdx.x & 63;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t rpw = (THREADS / 64) / wpr;  // rows per workgroup and round
+  const uint32_t unit0 = (wave % wpr) * 64 + lane, ustep = wpr * 64;
+  const uint32_t nb = upr >> 2;
+  const float inv_cols = 1.0f / (float)(upr * 8);
+  float wf[NU][8];
+#pragma unroll
+  for (int i = 0; i < NU; ++i) load_w(w, unit0 + i * ustep, upr, wf[i]);
+  for (int64_t r0 = (int64_t)blockIdx.x * rpw; r0 < rows; r0 += (int64_t)gridDim.x * rpw) {
+    const int64_t row = r0 + wave / wpr;
+    const bool ract = row < rows;
+    MxRaw<InT> raw[NU];
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const uint32_t unit = unit0 + i * ustep;
+      if (ract && unit < upr) mx_load_raw<false>(x + row * ldx + unit * 8, raw[i]);
+      else mx_zero_raw(raw[i]);
+    }
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      float f[8];
+      mx_unpack(raw[i], f);
+      float part = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) part = __builtin_fmaf(f[j], f[j], part);
+      ss += part;
+    }
+    ss = row_sum(ss, wpr, wave, red);
+    const float r = 1.0f / __builtin_sqrtf(ss * inv_cols + eps);
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const uint32_t unit = unit0 + i * ustep;
+      const bool act = ract && unit < upr;
+      float f[8], v[8];
+      mx_unpack(raw[i], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = f[j] * r * wf[i][j];
+      const MxScale sv = mx_scale<FMT, CEIL>(max_quad(absmax8(v)));
+      if (act) {
+        mx_store_codes8<FMT>(y + row * ldy + unit * 8, mx_codes8<FMT, CEIL>(v, sv));
+        if ((lane & 3) == 0) ys[row * nb + (unit >> 2)] = (uint8_t)sv.byte;
+      }
+      if (kept) {
+        const MxScale sk = mx_scale<FMT, CEIL>(max_quad(absmax8(f)));
+        if (act) {
+          mx_store_codes8<FMT>(kept + row * ldk + unit * 8, mx_codes8<FMT, CEIL>(f, sk));
+          if ((lane & 3) == 0) ks[row * nb + (unit >> 2)] = (uint8_t)sk.byte;
+        }
+      }
+    }
+    if (kept && ract && unit0 == 0) rstd[row] = r;
+  }
+}
+
+// part: [gridDim.x][8 upr] partial sums of dw, one row per workgroup.
+template <typename T, int FMT, int NU, int THREADS>
+__global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(
+    const uint8_t* __restrict__ kept, int64_t ldk, const uint8_t* __restrict__ ks, const float* __restrict__ rstd,
+    const float* __restrict__ w, const T* __restrict__ dy, int64_t lddy, int64_t rows, uint32_t upr, uint32_t wpr,
+    T* __restrict__ dx, int64_t lddx, float* __restrict__ part) {
+  __shared__ float red[16];
+  const uint32_t lane = threadIdx.x & 63;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t rpw = (THREADS / 64) / wpr;
+  const uint32_t unit0 = (wave % wpr) * 64 + lane, ustep = wpr * 64;
+  const uint32_t nb = upr >> 2;
+  const float inv_cols = 1.0f / (float)(upr * 8);
+  float wf[NU][8], dw[NU][8];
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    load_w(w, unit0 + i * ustep, upr, wf[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+  }
+  for (int64_t r0 = (int64_t)blockIdx.x * rpw; r0 < rows; r0 += (int64_t)gridDim.x * rpw) {
+    const int64_t row = r0 + wave / wpr;
+    const bool ract = row < rows;
+    uint2 code[NU];
+    uint32_t b[NU];
+    MxRaw<T> raw[NU];
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const uint32_t unit = unit0 + i * ustep;
+      code[i] = make_uint2(0u, 0u);
+      b[i] = 0;
+      mx_zero_raw(raw[i]);
+      if (ract && unit < upr) {
+        code[i] = mx_load_codes8<FMT>(kept + row * ldk + unit * 8);
+        b[i] = ks[row * nb + (unit >> 2)];
+        mx_load_raw<false>(dy + row * lddy + unit * 8, raw[i]);
+      }
+    }
+    const float r = ract ? rstd[row] : 0.0f;
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      float xh[8], d[8];
+      mx_decode8<FMT>(code[i], mx_factor(b[i]), xh);
+      mx_unpack(raw[i], d);
+      float p = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float t = d[j] * (xh[j] * r);
+        dw[i][j] += t;
+        p = __builtin_fmaf(t, wf[i][j], p);
+      }
+      dot += p;
+    }
+    const float k = row_sum(dot, wpr, wave, red) * inv_cols;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const uint32_t unit = unit0 + i * ustep;
+      float xh[8], d[8];
+      mx_decode8<FMT>(code[i], mx_factor(b[i]), xh);
+      mx_unpack(raw[i], d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] = r * (d[j] * wf[i][j] - xh[j] * r * k);
+      if (ract && unit < upr) mx_store8(dx + row * lddx + unit * 8, d);
+    }
+  }
+  // The workgroup's rows, wave after wave in order, into its row of partials:
+  // the same sum on every run.  A workgroup's own stores are seen by its
+  // later loads after the barrier.
+  float* out = part + (int64_t)blockIdx.x * (upr * 8);
+  for (uint32_t turn = 0; turn < rpw; ++turn) {
+    if (wave / wpr == turn) {
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        const uint32_t unit = unit0 + i * ustep;
+        if (unit < upr) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) out[unit * 8 + j] = (turn ? out[unit * 8 + j] : 0.0f) + dw[i][j];
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// dw[c] = sum of part[p][c] in order of p, 4 interleaved runs joined at the end.
+__global__ __launch_bounds__(256) void rmsnorm_dw_kernel(const float* __restrict__ part, uint32_t parts, uint32_t cols,
+                                                         float* __restrict__ dw) {
+  __shared__ float sum[4][64];
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t c = blockIdx.x * 64 + lane;
+  float s = 0.0f;
+  if (c < cols)
+    for (uint32_t p = wave; p < parts; p += 4) s += part[(int64_t)p * cols + c];
+  sum[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < cols) dw[c] = (sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]);
+}
+
+// Waves per row and units per lane for a row of upr units.
+struct NormShape {
+  uint32_t wpr, threads;
+  int nu;
+};
+NormShape norm_shape(int64_t cols) {
+  const uint32_t upr = (uint32_t)(cols / kLaneElems);
+  NormShape n;
+  n.wpr = upr <= 512 ? 1 : upr <= 2048 ? 4 : 16;
+  n.nu = (int)((upr + 64 * n.wpr - 1) / (64 * n.wpr));
+  n.threads = n.wpr <= 4 ? 256 : 1024;  // 1024 threads leave 128 registers: 4 units per lane at most
+  return n;
+}
+uint32_t norm_blocks(int64_t rows, const NormShape& n, int64_t cap) {
+  const int64_t rpw = n.threads / 64 / n.wpr;
+  const int64_t b = (rows + rpw - 1) / rpw;
+  return (uint32_t)(b < cap ? b : cap);
+}
+
+template <typename InT, int FMT, bool CEIL, bool KEEP>
+void swiglu_forward(const void* x, int64_t rows, int64_t cols, int64_t ldx, uint8_t* h, int64_t ldh, uint8_t* hs,
+                    uint8_t* kept, int64_t ldk, uint8_t* ks, hipStream_t stream) {
+  const uint32_t upr = (uint32_t)(cols / kLaneElems);
+  const bool deep = rows * upr >= (int64_t)kThreads * 2 * 4 * device_cus();
+  const int u = deep ? 2 : 1;
+  const int64_t items = rows * ((upr + 64 * u - 1) / (64 * u)), need = (items + 3) / 4;
+  const uint32_t blocks = (uint32_t)(need < kMaxBlocks ? need : kMaxBlocks);
+#define MXFP8_SF(U, NT)                                                                                          \
+  hipLaunchKernelGGL((swiglu_forward_kernel<InT, FMT, CEIL, KEEP, U, NT>), dim3(blocks), dim3(kThreads), 0, stream, \
+                     static_cast<const InT*>(x), ldx, rows, upr, h, ldh, hs, kept, ldk, ks)
+  if (!deep) MXFP8_SF(1, false);
+  else if (stream_loads(rows, 2 * cols, sizeof(InT))) MXFP8_SF(2, true);
+  else MXFP8_SF(2, false);
+#undef MXFP8_SF
+}
+
+template <typename T, int FMT>
+void swiglu_backward(const uint8_t* kept, int64_t ldk, const uint8_t* ks, const void* dh, int64_t lddh, int64_t rows,
+                     int64_t cols, void* dx, int64_t lddx, hipStream_t stream) {
+  const uint32_t upr = (uint32_t)(cols / kLaneElems);
+  const bool deep = rows * upr >= (int64_t)kThreads * 2 * 4 * device_cus();
+  const int u = deep ? 2 : 1;
+  const int64_t items = rows * ((upr + 64 * u - 1) / (64 * u)), need = (items + 3) / 4;
+  const uint32_t blocks = (uint32_t)(need < kMaxBlocks ? need : kMaxBlocks);
+#define MXFP8_SB(U, NT)                                                                                             \
+  hipLaunchKernelGGL((swiglu_backward_kernel<T, FMT, U, NT>), dim3(blocks), dim3(kThreads), 0, stream, kept, ldk, ks, \
+                     static_cast<const T*>(dh), lddh, rows, upr, static_cast<T*>(dx), lddx)
+  if (!deep) MXFP8_SB(1, false);
+  else if (stream_loads(rows, cols, sizeof(T))) MXFP8_SB(2, true);
+  else MXFP8_SB(2, false);
+#undef MXFP8_SB
+}
+
+template <typename InT, int FMT, bool CEIL>
+void rmsnorm_forward(const void* x, int64_t rows, int64_t cols, int64_t ldx, const float* w, float eps, uint8_t* y,
+                     int64_t ldy, uint8_t* ys, uint8_t* kept, int64_t ldk, uint8_t* ks, float* rstd,
+                     hipStream_t stream) {
+  const NormShape n = norm_shape(cols);
+  const uint32_t upr = (uint32_t)(cols / kLaneElems);
+  const dim3 grid(norm_blocks(rows, n, 256 * 4));
+#define MXFP8_NF(NU, THREADS)                                                                                               \
+  case NU:                                                                                                         \
+    hipLaunchKernelGGL((rmsnorm_forward_kernel<InT, FMT, CEIL, NU, THREADS>), grid, dim3(n.threads), 0, stream,             \
+                       static_cast<const InT*>(x), ldx, rows, upr, n.wpr, w, eps, y, ldy, ys, kept, ldk, ks, rstd); \
+    break;
+  if (n.threads > 256) {
+    switch (n.nu) { MXFP8_NF(3, 1024) MXFP8_NF(4, 1024) }
+  } else {
+    switch (n.nu) {
+      MXFP8_NF(1, 256) MXFP8_NF(2, 256) MXFP8_NF(3, 256) MXFP8_NF(4, 256)
+      MXFP8_NF(5, 256) MXFP8_NF(6, 256) MXFP8_NF(7, 256) MXFP8_NF(8, 256)
+    }
+  }
+#undef MXFP8_NF
+}
+
+template <typename T, int FMT>
+void rmsnorm_backward(const uint8_t* kept, int64_t ldk, const uint8_t* ks, const float* rstd, const float* w,
+                      const void* dy, int64_t lddy, int64_t rows, int64_t cols, void* dx, int64_t lddx, float* part,
+                      int64_t parts, hipStream_t stream) {
+  const NormShape n = norm_shape(cols);
+  const uint32_t upr = (uint32_t)(cols / kLaneElems);
+  const dim3 grid((uint32_t)parts);
+#define MXFP8_NB(NU, THREADS)                                                                                              \
+  case NU:                                                                                                        \
+    hipLaunchKernelGGL((rmsnorm_backward_kernel<T, FMT, NU, THREADS>), grid, dim3(n.threads), 0, stream, kept, ldk, ks, rstd, \
+                       w, static_cast<const T*>(dy), lddy, rows, upr, n.wpr, static_cast<T*>(dx), lddx, part);    \
+    break;
+  if (n.threads > 256) {
+    switch (n.nu) { MXFP8_NB(3, 1024) MXFP8_NB(4, 1024) }
+  } else {
+    switch (n.nu) {
+      MXFP8_NB(1, 256) MXFP8_NB(2, 256) MXFP8_NB(3, 256) MXFP8_NB(4, 256)
+      MXFP8_NB(5, 256) MXFP8_NB(6, 256) MXFP8_NB(7, 256) MXFP8_NB(8, 256)
+    }
+  }
+#undef MXFP8_NB
+}
+
+}  // namespace mx_act_detail
+
+using namespace mx_act_detail;
+
+void launch_mx_swiglu_forward(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ldx, int fmt, int rule,
+                              uint8_t* h, int64_t ldh, uint8_t* hs, uint8_t* kept, int64_t ldk, uint8_t* ks,
+                              hipStream_t stream) {
+#define MXFP8_K(T, FMT, CEIL)                                                                             \
+  (kept ? swiglu_forward<T, FMT, CEIL, true>(x, rows, cols, ldx, h, ldh, hs, kept, ldk, ks, stream)       \
+        : swiglu_forward<T, FMT, CEIL, false>(x, rows, cols, ldx, h, ldh, hs, nullptr, 0, nullptr, stream))
+#define MXFP8_R(T, FMT) (rule == 0 ? MXFP8_K(T, FMT, true) : MXFP8_K(T, FMT, false))
+  if (dtype == 0) fmt == 0 ? MXFP8_R(float, 0) : MXFP8_R(float, 1);
+  else fmt == 0 ? MXFP8_R(uint16_t, 0) : MXFP8_R(uint16_t, 1);
+#undef MXFP8_R
+#undef MXFP8_K
+}
+
+void launch_mx_swiglu_backward(const uint8_t* kept, int64_t ldk, const uint8_t* ks, int fmt, const void* dh, int dtype,
+                               int64_t lddh, int64_t rows, int64_t cols, void* dx, int64_t lddx, hipStream_t stream) {
+#define MXFP8_B(T, FMT) swiglu_backward<T, FMT>(kept, ldk, ks, dh, lddh, rows, cols, dx, lddx, stream)
+  if (dtype == 0) fmt == 0 ? MXFP8_B(float, 0) : MXFP8_B(float, 1);
+  else fmt == 0 ? MXFP8_B(uint16_t, 0) : MXFP8_B(uint16_t, 1);
+#undef MXFP8_B
+}
+
+void launch_mx_rmsnorm_forward(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ldx, const float* w,
+                               float eps, int fmt, int rule, uint8_t* y, int64_t ldy, uint8_t* ys, uint8_t* kept,
+                               int64_t ldk, uint8_t* ks, float* rstd, hipStream_t stream) {
+#define MXFP8_R(T, FMT)                                                                                          \
+  (rule == 0                                                                                                     \
+       ? rmsnorm_forward<T, FMT, true>(x, rows, cols, ldx, w, eps, y, ldy, ys, kept, ldk, ks, rstd, stream)      \
+       : rmsnorm_forward<T, FMT, false>(x, rows, cols, ldx, w, eps, y, ldy, ys, kept, ldk, ks, rstd, stream))
+  if (dtype == 0) fmt == 0 ? MXFP8_R(float, 0) : MXFP8_R(float, 1);
+  else fmt == 0 ? MXFP8_R(uint16_t, 0) : MXFP8_R(uint16_t, 1);
+#undef MXFP8_R
+}
+
+int64_t rmsnorm_backward_parts(int64_t rows, int64_t cols) {
+  const NormShape n = norm_shape(cols);
+  return norm_blocks(rows, n, 256 * 2);
+}
+
+void launch_mx_rmsnorm_backward(const uint8_t* kept, int64_t ldk, const uint8_t* ks, const float* rstd, int fmt,
+                                const float* w, const void* dy, int dtype, int64_t lddy, int64_t rows, int64_t cols,
+                                void* dx, int64_t lddx, float* dw, float* workspace, int64_t parts,
+                                hipStream_t stream) {
+  if (rows > 0) {
+#define MXFP8_B(T, FMT) \
+  rmsnorm_backward<T, FMT>(kept, ldk, ks, rstd, w, dy, lddy, rows, cols, dx, lddx, workspace, parts, stream)
+  if (dtype == 0) fmt == 0 ? MXFP8_B(float, 0) : MXFP8_B(float, 1);
+  else fmt == 0 ? MXFP8_B(uint16_t, 0) : MXFP8_B(uint16_t, 1);
+#undef MXFP8_B
+  }
+  hipLaunchKernelGGL(rmsnorm_dw_kernel, dim3((uint32_t)((cols + 63) / 64)), dim3(256), 0, stream, workspace,
+                     (uint32_t)parts, (uint32_t)cols, dw);
+}
+
+}  // namespace mxfp8

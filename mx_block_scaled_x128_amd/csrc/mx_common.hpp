@@ -1,0 +1,208 @@
+// mx_common.hpp -- device helpers of the MX operators (32-element blocks with
+// one E8M0 scale): the E2M1 format next to E4M3 and E5M2, block exponents
+// under both rules, the casts with the scale already divided out, and the way
+// back from codes to values.
+//
+// E2M1 [OCP MX element format]: bias 1, no infinities or NaN, magnitudes
+// 0, 0.5, 1, 1.5, 2, 3, 4, 6; largest finite value 6 = 1.5 * 2^2.  Two codes
+// to a byte, the even element in the low four bits.
+//
+// Non-finite input.  A block that holds an infinity or a NaN gets the scale
+// byte 255 (E8M0's NaN) and zero codes; every reader (mx_unscale here, the
+// matrix cores in the products) turns its elements into NaN.  The largest
+// |x| as an integer finds both: the patterns of inf and NaN are above every
+// finite one.
+#pragma once
+
+#include "device_common.hpp"
+
+namespace mxfp8 {
+
+constexpr int kE2M1 = 2;
+constexpr uint32_t kInfBits = 0x7F800000u;
+
+// Elements per lane of the row-wise kernels: 8 (16 bytes of bf16, 8 of FP8
+// codes, 4 of E2M1 codes); 4 lanes, a DPP quad, share one MX block.
+constexpr int kLaneElems = 8;
+
+template <int FMT> struct MxFmt {
+  static constexpr int q = FmtInfo<FMT>::q;
+  static constexpr float fmax = FmtInfo<FMT>::fmax;
+  static constexpr uint32_t frac_max = 0x600000u;  // fmax = 1.75 * 2^q
+  static constexpr int code_bits = 8;
+};
+template <> struct MxFmt<kE2M1> {
+  static constexpr int q = 2;
+  static constexpr float fmax = 6.0f;
+  static constexpr uint32_t frac_max = 0x400000u;  // fmax = 1.5 * 2^q
+  static constexpr int code_bits = 4;
+};
+
+// Exponent of a finite block maximum (its fp32 bits).  ceil: the smallest e
+// with amax <= fmax * 2^e; otherwise floor(log2 amax) - q; both clamped to
+// [-127, 127].  A subnormal amax gives -127 under both rules.
+template <int FMT, bool CEIL>
+__device__ __forceinline__ int mx_exp(uint32_t amax_bits) {
+  const int E = (int)(amax_bits >> 23);
+  int e = E - 127 - MxFmt<FMT>::q;
+  if (CEIL && (amax_bits & 0x7FFFFFu) > MxFmt<FMT>::frac_max) ++e;
+  return E == 0 || e < -127 ? -127 : e;  // e <= 127 - q + 1 for finite amax
+}
+
+// Scale byte and the factor 2^-e of a block.  A block with a non-finite
+// element: byte 255 and factor 0 (mx_cast then gives zero codes, see there).
+struct MxScale {
+  uint32_t byte;
+  float inv;
+};
+template <int FMT, bool CEIL>
+__device__ __forceinline__ MxScale mx_scale(uint32_t amax_bits) {
+  const int e = mx_exp<FMT, CEIL>(amax_bits);
+  const bool ok = amax_bits < kInfBits;
+  return MxScale{ok ? (uint32_t)(e + 127) : 255u, ok ? pow2_neg(e) : 0.0f};
+}
+
+// x * 2^-e for the cast.  The floor rule leaves values up to 2^(q+1), which
+// are held to +-fmax here; the ceil rule leaves none above fmax.  A block with
+// factor 0 may give NaN (inf * 0): its codes are dropped after the cast.
+template <int FMT, bool CEIL>
+__device__ __forceinline__ float mx_fit(float x, float inv) {
+  if constexpr (CEIL) return x * inv;
+  return __builtin_amdgcn_fmed3f(x * inv, -MxFmt<FMT>::fmax, MxFmt<FMT>::fmax);
+}
+
+// Four values in range -> four codes: FP8 in 32 bits, E2M1 in the low 16.
+// v_cvt_scalef32_pk_fp4_f32 with scale 1 rounds to nearest even.
+template <int FMT>
+__device__ __forceinline__ uint32_t mx_cvt4(float a, float b, float c, float d) {
+  if constexpr (FMT == kE2M1) {
+    uint32_t w = 0;
+#if defined(__HIP_DEVICE_COMPILE__)
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, a, b, 1.0f, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, c, d, 1.0f, 1);
+#endif
+    return w;
+  } else {
+    return cvt4<FMT>(a, b, c, d);
+  }
+}
+
+// Eight codes: FP8 in both words, E2M1 in the first.
+template <int FMT, bool CEIL>
+__device__ __forceinline__ uint2 mx_codes8(const float (&f)[8], const MxScale& s) {
+  uint2 o = make_uint2(0u, 0u);
+#if defined(__HIP_DEVICE_COMPILE__)
+  if constexpr (FMT == kE2M1) {
+    uint32_t w = 0;
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, mx_fit<FMT, CEIL>(f[0], s.inv), mx_fit<FMT, CEIL>(f[1], s.inv), 1.0f, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, mx_fit<FMT, CEIL>(f[2], s.inv), mx_fit<FMT, CEIL>(f[3], s.inv), 1.0f, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, mx_fit<FMT, CEIL>(f[4], s.inv), mx_fit<FMT, CEIL>(f[5], s.inv), 1.0f, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, mx_fit<FMT, CEIL>(f[6], s.inv), mx_fit<FMT, CEIL>(f[7], s.inv), 1.0f, 3);
+    o.x = w;
+  } else {
+    o.x = cvt4<FMT>(mx_fit<FMT, CEIL>(f[0], s.inv), mx_fit<FMT, CEIL>(f[1], s.inv), mx_fit<FMT, CEIL>(f[2], s.inv),
+                    mx_fit<FMT, CEIL>(f[3], s.inv));
+    o.y = cvt4<FMT>(mx_fit<FMT, CEIL>(f[4], s.inv), mx_fit<FMT, CEIL>(f[5], s.inv), mx_fit<FMT, CEIL>(f[6], s.inv),
+                    mx_fit<FMT, CEIL>(f[7], s.inv));
+  }
+#endif
+  if (s.byte == 255u) o = make_uint2(0u, 0u);
+  return o;
+}
+
+__device__ __forceinline__ uint32_t absmax8(const float (&f)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, abs_bits(f[j]));
+  return m;
+}
+
+// 2^(b - 127) of a scale byte: NaN for 255, the subnormal 2^-127 for 0.
+__device__ __forceinline__ float mx_factor(uint32_t b) {
+  return __uint_as_float(b == 255u ? 0x7FC00000u : b == 0u ? 0x00400000u : b << 23);
+}
+
+typedef float mx_f2 __attribute__((ext_vector_type(2)));
+
+// Eight codes -> the values they stand for (exact but for fp32's own range).
+template <int FMT>
+__device__ __forceinline__ void mx_decode8(uint2 w, float factor, float (&f)[8]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  mx_f2 v[4];
+  if constexpr (FMT == kE2M1) {
+    v[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w.x, 1.0f, 0);
+    v[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w.x, 1.0f, 1);
+    v[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w.x, 1.0f, 2);
+    v[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w.x, 1.0f, 3);
+  } else if constexpr (FMT == 0) {
+    v[0] = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.x, false);
+    v[1] = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.x, true);
+    v[2] = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.y, false);
+    v[3] = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.y, true);
+  } else {
+    v[0] = __builtin_amdgcn_cvt_pk_f32_bf8((int)w.x, false);
+    v[1] = __builtin_amdgcn_cvt_pk_f32_bf8((int)w.x, true);
+    v[2] = __builtin_amdgcn_cvt_pk_f32_bf8((int)w.y, false);
+    v[3] = __builtin_amdgcn_cvt_pk_f32_bf8((int)w.y, true);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = v[j].x * factor;
+    f[2 * j + 1] = v[j].y * factor;
+  }
+#endif
+}
+
+// Eight codes of one lane from memory: 8 bytes of FP8, 4 of E2M1.
+template <int FMT>
+__device__ __forceinline__ uint2 mx_load_codes8(const uint8_t* p) {
+  if constexpr (FMT == kE2M1) return make_uint2(*reinterpret_cast<const uint32_t*>(p), 0u);
+  const nt_u32x2 v = *reinterpret_cast<const nt_u32x2*>(p);
+  return make_uint2(v.x, v.y);
+}
+template <int FMT>
+__device__ __forceinline__ void mx_store_codes8(uint8_t* p, uint2 v) {
+  if constexpr (FMT == kE2M1) *reinterpret_cast<uint32_t*>(p) = v.x;
+  else store_codes(p, v);
+}
+
+// Eight fp32 values out, as fp32 or rounded (nearest even) to bf16.
+typedef __bf16 mx_bf2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t mx_bf16x2(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((mx_f2{lo, hi}), mx_bf2));
+}
+__device__ __forceinline__ void mx_store8(float* p, const float (&f)[8]) {
+  *reinterpret_cast<nt_f32x4*>(p) = nt_f32x4{f[0], f[1], f[2], f[3]};
+  *reinterpret_cast<nt_f32x4*>(p + 4) = nt_f32x4{f[4], f[5], f[6], f[7]};
+}
+__device__ __forceinline__ void mx_store8(uint16_t* p, const float (&f)[8]) {
+  *reinterpret_cast<nt_u32x4*>(p) = nt_u32x4{mx_bf16x2(f[0], f[1]), mx_bf16x2(f[2], f[3]), mx_bf16x2(f[4], f[5]),
+                                             mx_bf16x2(f[6], f[7])};
+}
+
+// Raw words of eight input elements, converted where they are used.
+template <typename T> struct MxRaw;
+template <> struct MxRaw<uint16_t> { nt_u32x4 v; };
+template <> struct MxRaw<float> { nt_f32x4 a, b; };
+template <bool NT>
+__device__ __forceinline__ void mx_load_raw(const uint16_t* p, MxRaw<uint16_t>& r) {
+  r.v = NT ? __builtin_nontemporal_load(reinterpret_cast<const nt_u32x4*>(p)) : *reinterpret_cast<const nt_u32x4*>(p);
+}
+template <bool NT>
+__device__ __forceinline__ void mx_load_raw(const float* p, MxRaw<float>& r) {
+  r.a = NT ? __builtin_nontemporal_load(reinterpret_cast<const nt_f32x4*>(p)) : *reinterpret_cast<const nt_f32x4*>(p);
+  r.b = NT ? __builtin_nontemporal_load(reinterpret_cast<const nt_f32x4*>(p + 4))
+           : *reinterpret_cast<const nt_f32x4*>(p + 4);
+}
+__device__ __forceinline__ void mx_zero_raw(MxRaw<uint16_t>& r) { r.v = nt_u32x4{0, 0, 0, 0}; }
+__device__ __forceinline__ void mx_zero_raw(MxRaw<float>& r) { r.a = nt_f32x4{0, 0, 0, 0}; r.b = r.a; }
+__device__ __forceinline__ void mx_unpack(const MxRaw<uint16_t>& r, float (&f)[8]) {
+  f[0] = bf16_lo(r.v.x); f[1] = bf16_hi(r.v.x); f[2] = bf16_lo(r.v.y); f[3] = bf16_hi(r.v.y);
+  f[4] = bf16_lo(r.v.z); f[5] = bf16_hi(r.v.z); f[6] = bf16_lo(r.v.w); f[7] = bf16_hi(r.v.w);
+}
+__device__ __forceinline__ void mx_unpack(const MxRaw<float>& r, float (&f)[8]) {
+  f[0] = r.a.x; f[1] = r.a.y; f[2] = r.a.z; f[3] = r.a.w;
+  f[4] = r.b.x; f[5] = r.b.y; f[6] = r.b.z; f[7] = r.b.w;
+}
+
+}  // namespace mxfp8

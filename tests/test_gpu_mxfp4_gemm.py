@@ -1,0 +1,144 @@
+"""mxfp4_gemm against fp64 products over the same codes (E2M1 on the right; E2M1, E4M3 or
+E5M2 on the left).
+
+Tolerance: 2^-12 * sum |a b| per element, as for the other products, and for bf16 output one
+rounding (2^-8) more.  E2M1 products span 6 binades and are exact in the matrix cores; what is
+left for two E2M1 operands is the fp32 accumulation."""
+import numpy as np
+import pytest
+import torch
+
+import mx_block_scaled_x128_amd as mx
+import mxref
+from gpu_helpers import assert_gemm_close, dev, dev_ld16, host
+
+pytestmark = pytest.mark.gpu
+FMTS = [mx.E2M1, mx.E4M3, mx.E5M2]
+
+
+def operand(rows, K, fmt, seed, spread=6):
+    rng = np.random.default_rng(seed)
+    x = rng.normal(0, 1, (rows, K)) * mxref.pow2(rng.integers(-spread, spread + 1, (rows, K // 32)).repeat(32, axis=1))
+    return mxref.quantize(x, fmt, mxref.CEIL)
+
+
+def product(a, sa, a_fmt, b, sb):
+    A, B = mxref.dequantize(a, sa, a_fmt), mxref.dequantize(b, sb, mxref.E2M1)
+    return A @ B.T, np.abs(A) @ np.abs(B).T
+
+
+def run(a, sa, a_fmt, b, sb, dtype, pad=0):
+    a_d = dev(a, pitch=a.shape[1] + pad) if a.shape[1] else dev(a)
+    b_d = dev(b, pitch=b.shape[1] + pad) if b.shape[1] else dev(b)
+    out = mx.mxfp4_scaled_gemm(a_d, dev(sa), a_fmt, b_d, dev(sb), out_dtype=dtype)
+    torch.cuda.synchronize()
+    return host(out)
+
+
+SHAPES = [(1, 1, 128), (1, 16, 256), (1, 300, 3584), (2, 100, 384), (15, 17, 640), (16, 256, 1152), (17, 33, 256),
+          (33, 520, 128), (37, 1536, 1280), (64, 64, 512), (65, 70, 896), (100, 258, 384), (128, 128, 256),
+          (129, 300, 640), (200, 515, 1024), (256, 256, 512), (300, 260, 128), (520, 1030, 1664)]
+
+
+@pytest.mark.parametrize("a_fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_shapes(M, N, K, a_fmt):
+    a, sa = operand(M, K, a_fmt, M)
+    b, sb = operand(N, K, mx.E2M1, N + 7)
+    y, t = product(a, sa, a_fmt, b, sb)
+    assert_gemm_close(run(a, sa, a_fmt, b, sb, torch.float32, pad=16), y, t, False)
+    assert_gemm_close(run(a, sa, a_fmt, b, sb, torch.bfloat16), y, t, True)
+
+
+@pytest.mark.parametrize("a_fmt", FMTS)
+@pytest.mark.parametrize("M,N", [(3, 40), (40, 40), (140, 150), (300, 600)])
+def test_each_element_meets_its_partner_and_scales(M, N, a_fmt):
+    """One nonzero element per row of A, random everything in B: the product is a single
+    term, exact in fp32, so a wrong k, row or scale anywhere shows."""
+    K = 768
+    rng = np.random.default_rng(M)
+    a = np.zeros((M, K), dtype=np.uint8)
+    at = (np.arange(M) * 131) % K
+    a[np.arange(M), at] = mxref.cast(np.array([1.5]), a_fmt)[0]
+    a = mxref.pack(a) if a_fmt == mx.E2M1 else a
+    sa = rng.integers(117, 138, (M, K // 32)).astype(np.uint8)
+    b = rng.integers(0, 256, (N, K // 2)).astype(np.uint8)
+    sb = rng.integers(117, 138, (N, K // 32)).astype(np.uint8)
+    y, _ = product(a, sa, a_fmt, b, sb)
+    assert np.array_equal(run(a, sa, a_fmt, b, sb, torch.float32).astype(np.float64), y)
+
+
+@pytest.mark.parametrize("M,N", [(5, 64), (70, 96), (260, 300)])
+def test_whole_sums_are_exact(M, N):
+    """E2M1 codes under scales of 1: every partial sum is a multiple of 1/4 below 2^22, exact in fp32."""
+    K = 2048
+    rng = np.random.default_rng(N)
+    a = rng.integers(0, 256, (M, K // 2)).astype(np.uint8)
+    b = rng.integers(0, 256, (N, K // 2)).astype(np.uint8)
+    sa, sb = np.full((M, K // 32), 127, np.uint8), np.full((N, K // 32), 127, np.uint8)
+    y, _ = product(a, sa, mx.E2M1, b, sb)
+    assert np.array_equal(run(a, sa, mx.E2M1, b, sb, torch.float32).astype(np.float64), y)
+
+
+@pytest.mark.parametrize("a_fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [(8, 512, 512), (512, 512, 512)])
+def test_nan_blocks_reach_their_outputs_only(M, N, K, a_fmt):
+    a, sa = operand(M, K, a_fmt, 1)
+    b, sb = operand(N, K, mx.E2M1, 2)
+    sa[3, 2] = 255
+    sb[40, K // 32 - 1] = 255
+    y = run(a, sa, a_fmt, b, sb, torch.float32)
+    want = np.zeros((M, N), bool)
+    want[3, :] = want[:, 40] = True
+    assert np.array_equal(np.isnan(y), want)
+
+
+@pytest.mark.parametrize("a_fmt", FMTS)
+def test_k_zero_and_padding(a_fmt):
+    e = torch.empty((5, 0), dtype=torch.uint8, device="cuda")
+    y = mx.mxfp4_scaled_gemm(e, e, a_fmt, torch.empty((40, 0), dtype=torch.uint8, device="cuda"),
+                             torch.empty((40, 0), dtype=torch.uint8, device="cuda"))
+    assert y.shape == (5, 40) and not host(y).any()
+    for M in (5, 300):
+        a, sa = operand(M, 256, a_fmt, 1)
+        b, sb = operand(50, 256, mx.E2M1, 2)
+        buf = torch.full((M, 64), 7.0, device="cuda")
+        mx.mxfp4_scaled_gemm(dev_ld16(a), dev(sa), a_fmt, dev_ld16(b), dev(sb), out=buf[:, :50])
+        ref, t = product(a, sa, a_fmt, b, sb)
+        assert_gemm_close(host(buf)[:, :50], ref, t, False)
+        assert (host(buf)[:, 50:] == 7.0).all()
+
+
+@pytest.mark.parametrize("a_fmt", FMTS)
+def test_same_bits_every_time(a_fmt):
+    for M in (4, 48, 400):
+        a, sa = operand(M, 1024, a_fmt, 1)
+        b, sb = operand(700, 1024, mx.E2M1, 2)
+        first = run(a, sa, a_fmt, b, sb, torch.float32)
+        for _ in range(3):
+            assert np.array_equal(run(a, sa, a_fmt, b, sb, torch.float32), first)
+
+
+def test_quantize_then_product():
+    """The library's own codes through the product: forward, and the data gradient on the transposed weight."""
+    rng = np.random.default_rng(0)
+    x, w = rng.normal(0, 1, (200, 256)).astype(np.float32), rng.normal(0, 0.02, (384, 256)).astype(np.float32)
+    dy = rng.normal(0, 1e-3, (200, 384)).astype(np.float32)
+    wq, ws = mx.quantize_mxfp4(torch.from_numpy(w).cuda())
+    wt, wts = mx.quantize_mx_t(torch.from_numpy(w).cuda(), mx.E2M1, mx.RULE_FLOOR)
+    xq, xs, _ = mx.quantize_mx(torch.from_numpy(x).cuda(), mx.E4M3, mx.RULE_CEIL)
+    gq, gs, _ = mx.quantize_mx(torch.from_numpy(dy).cuda(), mx.E5M2, mx.RULE_CEIL)
+    y = mx.mxfp4_scaled_gemm(xq, xs, mx.E4M3, wq, ws)
+    dx = mx.mxfp4_scaled_gemm(gq, gs, mx.E5M2, wt, wts)
+    assert_gemm_close(host(y), *product(host(xq), host(xs), 0, host(wq), host(ws)), False)
+    assert_gemm_close(host(dx), *product(host(gq), host(gs), 1, host(wt), host(wts)), False)
+
+
+def test_full_k_and_large_extents():
+    """Long K at every few-row width, and a wide N: sums over 18944."""
+    for M, N, K, fmt in ((1, 512, 18944, mx.E4M3), (24, 512, 18944, mx.E2M1), (512, 512, 18944, mx.E5M2),
+                         (2, 40000, 128, mx.E2M1), (3000, 64, 256, mx.E4M3)):
+        a, sa = operand(M, K, fmt, 1, spread=0)
+        b, sb = operand(N, K, mx.E2M1, 2, spread=0)
+        y, t = product(a, sa, fmt, b, sb)
+        assert_gemm_close(run(a, sa, fmt, b, sb, torch.float32), y, t, False, what=str((M, N, K)))
