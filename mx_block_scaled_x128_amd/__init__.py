@@ -600,227 +600,87 @@ def gaussws(w, bitwidths, seed, stream_id=0, out=None, stream=None):
 
 # ------------------------------------------------------------------ MX operators
 #
-# E2M1 codes are uint8 tensors with two elements to a byte: [rows][cols / 2].
+# Their checks, allocations and calls are in the extension _tensors (built from
+# csrc/tensors.cpp next to the library): the same in Python takes longer than
+# the small kernels.  ValueError for a tensor that does not fit, before any
+# call.  E2M1 codes are uint8 tensors with two elements to a byte:
+# [rows][cols / 2].
 
 SwigluKept = collections.namedtuple("SwigluKept", "codes scales fmt")
 SwigluKept.__doc__ = "What swiglu_mx keeps of its input: codes [rows][2 cols], scales [rows][2 cols / 32], their format."
 RmsnormKept = collections.namedtuple("RmsnormKept", "codes scales rstd fmt")
 RmsnormKept.__doc__ = "What rmsnorm_mx keeps: the input's codes and scales, 1 / rms of each row (fp32), the codes' format."
 
-
-def _fmt(fmt, name, allowed):
-    _require(fmt in allowed, "%s must be one of %s, got %r", name, allowed, fmt)
+_tensors = None
 
 
-def _packed_cols(fmt, cols):
-    return cols // 2 if fmt == E2M1 else cols
-
-
-def _code_matrix(t, fmt, name):
-    """A 2-D code tensor of fmt; returns (rows, elements per row)."""
-    _require(_is_tensor(t) and t.dim() == 2, "%s must be a 2-D torch tensor", name)
-    _matrix(t, name, (_torch().uint8,) if fmt == E2M1 else _code_dtypes(), t.shape)
-    rows, cols = t.shape
-    return rows, cols * 2 if fmt == E2M1 else cols
-
-
-def _blocks(cols, name):
-    _require(cols % 32 == 0, "%s must have a multiple of 32 columns, got %d", name, cols)
-
-
-def _new(rows, cols, dtype, device):
-    """Uninitialized [rows][cols] view with a 16-element row pitch."""
-    torch = _torch()
-    if cols % 16 == 0:
-        return torch.empty((rows, cols), dtype=dtype, device=device)
-    return torch.empty((rows, _pad16(max(cols, 1))), dtype=dtype, device=device)[:, :cols]
-
-
-def _real_dtype(dtype):
-    torch = _torch()
-    _require(dtype in (torch.float32, torch.bfloat16), "dtype must be torch.float32 or torch.bfloat16, got %s", dtype)
-    return F32 if dtype == torch.float32 else BF16
+def _ops():
+    """The extension, its calls bound to the library."""
+    global _tensors
+    if _tensors is None:
+        import importlib
+        load_library()
+        _torch()
+        try:
+            ops = importlib.import_module(__name__ + "._tensors")
+        except ImportError as e:
+            raise ImportError("the extension _tensors is not built (%s); run python -m mx_block_scaled_x128_amd.build"
+                              % e) from e
+        ops.bind(_LIB_PATH)
+        _tensors = ops
+    return _tensors
 
 
 def quantize_mxfp4(x, rule=RULE_FLOOR, stream=None):
     """MXFP4 quantization along rows: (E2M1 codes [rows][cols / 2] uint8, scales [rows][cols / 32])."""
-    torch = _torch()
-    rows, cols = _input(x, "x")
-    _blocks(cols, "x")
-    dev = _device_of([("x", x)])
-    q = _new(rows, cols // 2, torch.uint8, dev)
-    s = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
-    _check(mxfp4_quantize(x.data_ptr(), _in_dtype(x), rows, cols, _ld(x), rule, q.data_ptr(), _ld(q), s.data_ptr(),
-                          _stream(stream, dev)), "mxfp4_quantize")
-    return q, s
+    return (_tensors or _ops()).quantize_mxfp4(x, rule, stream)
 
 
 def dequantize_mx(q, scales, fmt, dtype=None, stream=None):
     """The values that MX codes (E4M3, E5M2 or packed E2M1) stand for, as float32 (the
     default) or bfloat16 [rows][cols]."""
-    torch = _torch()
-    _fmt(fmt, "fmt", (E4M3, E5M2, E2M1))
-    rows, cols = _code_matrix(q, fmt, "q")
-    _blocks(cols, "q")
-    _dense(scales, "scales", _scale_dtypes(), (rows, cols // 32))
-    dtype = dtype or torch.float32
-    y_dtype = _real_dtype(dtype)
-    dev = _device_of([("q", q), ("scales", scales)])
-    y = torch.empty((rows, cols), dtype=dtype, device=dev)
-    _check(mx_dequantize(q.data_ptr(), _ld(q), fmt, scales.data_ptr(), rows, cols, y.data_ptr(), y_dtype, _ld(y),
-                         _stream(stream, dev)), "mx_dequantize")
-    return y
-
-
-def _rows_out(rows, rows_out):
-    if rows_out is None:
-        return (rows + 127) // 128 * 128
-    _require(rows_out % 32 == 0 and rows_out >= rows, "rows_out must be a multiple of 32 and at least %d, got %d", rows,
-             rows_out)
-    return rows_out
+    return (_tensors or _ops()).dequantize_mx(q, scales, fmt, dtype or _torch().float32, stream)
 
 
 def quantize_mx_t(x, fmt=E4M3, rule=RULE_CEIL, rows_out=None, stream=None):
     """MX quantization in blocks of 32 rows, transposed: (codes [cols][rows_out] -- [cols][rows_out / 2]
     for E2M1 -- and scales [cols][rows_out / 32]).  rows_out: at least rows, filled with zeros; by
     default rows rounded up to 128, the K multiple of the products."""
-    torch = _torch()
-    _fmt(fmt, "fmt", (E4M3, E5M2, E2M1))
-    rows, cols = _input(x, "x")
-    _require(cols % 16 == 0, "x must have a multiple of 16 columns, got %d", cols)
-    rows_out = _rows_out(rows, rows_out)
-    dev = _device_of([("x", x)])
-    qt = _new(cols, _packed_cols(fmt, rows_out), torch.uint8, dev)
-    st = torch.empty((cols, rows_out // 32), dtype=torch.uint8, device=dev)
-    _check(mx_quantize_t(x.data_ptr(), _in_dtype(x), rows, cols, _ld(x), fmt, rule, qt.data_ptr(), _ld(qt), rows_out,
-                         st.data_ptr(), _stream(stream, dev)), "mx_quantize_t")
-    return qt, st
+    return (_tensors or _ops()).quantize_mx_t(x, fmt, rule, rows_out, stream)
 
 
 def requantize_mx_t(q, scales, q_fmt, fmt=E4M3, rule=RULE_CEIL, rows_out=None, stream=None):
     """quantize_mx_t of a matrix held as FP8 MX codes along rows (q_fmt E4M3 or E5M2), such
     as an activation kept for the backward pass."""
-    torch = _torch()
-    _fmt(q_fmt, "q_fmt", (E4M3, E5M2))
-    _fmt(fmt, "fmt", (E4M3, E5M2, E2M1))
-    rows, cols = _code_matrix(q, q_fmt, "q")
-    _blocks(cols, "q")
-    _dense(scales, "scales", _scale_dtypes(), (rows, cols // 32))
-    rows_out = _rows_out(rows, rows_out)
-    dev = _device_of([("q", q), ("scales", scales)])
-    qt = _new(cols, _packed_cols(fmt, rows_out), torch.uint8, dev)
-    st = torch.empty((cols, rows_out // 32), dtype=torch.uint8, device=dev)
-    _check(mx_requantize_t(q.data_ptr(), _ld(q), q_fmt, scales.data_ptr(), rows, cols, fmt, rule, qt.data_ptr(),
-                           _ld(qt), rows_out, st.data_ptr(), _stream(stream, dev)), "mx_requantize_t")
-    return qt, st
+    return (_tensors or _ops()).requantize_mx_t(q, scales, q_fmt, fmt, rule, rows_out, stream)
 
 
 def mxfp4_scaled_gemm(a, a_scales, a_fmt, b, b_scales, out_dtype=None, out=None, stream=None):
     """C = A * B^T with B in E2M1 (codes [N][K / 2]) and A in E2M1 ([M][K / 2]), E4M3 or E5M2
     ([M][K]); scales [M][K / 32] and [N][K / 32].  K a multiple of 128."""
-    _fmt(a_fmt, "a_fmt", (E4M3, E5M2, E2M1))
-    M, K = _code_matrix(a, a_fmt, "a")
-    N, kb = _code_matrix(b, E2M1, "b")
-    _require(kb == K, "a has K = %d but b has K = %d", K, kb)
-    _require(K % 128 == 0, "mxfp4_scaled_gemm: K must be a multiple of 128, got %d", K)
-    _dense(a_scales, "a_scales", _scale_dtypes(), (M, K // 32))
-    _dense(b_scales, "b_scales", _scale_dtypes(), (N, K // 32))
-    _check_out(out, out_dtype, M, N)
-    dev = _device_of([("a", a), ("a_scales", a_scales), ("b", b), ("b_scales", b_scales)]
-                     + ([("out", out)] if out is not None else []))
-    out = _out_matrix(out, out_dtype, M, N, dev)
-    c_dtype = F32 if out.dtype == _torch().float32 else BF16
-    _check(mxfp4_gemm(M, N, K, a.data_ptr(), _ld(a), a_fmt, a_scales.data_ptr(), b.data_ptr(), _ld(b),
-                      b_scales.data_ptr(), out.data_ptr(), _ld(out), c_dtype, _stream(stream, dev)), "mxfp4_gemm")
-    return out
+    return (_tensors or _ops()).mxfp4_scaled_gemm(a, a_scales, a_fmt, b, b_scales, out_dtype, out, stream)
 
 
 def swiglu_mx(x, fmt=E4M3, rule=RULE_CEIL, keep=True, stream=None):
     """h = silu(g) * u of x = (g, u) [rows][2 cols] as MX codes: (h [rows][cols], scales
     [rows][cols / 32], SwigluKept for swiglu_mx_backward, or None with keep=False)."""
-    torch = _torch()
-    _fmt(fmt, "fmt", (E4M3, E5M2))
-    rows, wide = _input(x, "x")
-    _require(wide % 64 == 0, "x must have twice a multiple of 32 columns, got %d", wide)
-    cols = wide // 2
-    dev = _device_of([("x", x)])
-    h = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
-    hs = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
-    kept, k, ldk, ks = None, None, 0, None
-    if keep:
-        kept = SwigluKept(torch.empty((rows, wide), dtype=torch.uint8, device=dev),
-                          torch.empty((rows, wide // 32), dtype=torch.uint8, device=dev), fmt)
-        k, ldk, ks = kept.codes.data_ptr(), wide, kept.scales.data_ptr()
-    _check(mx_swiglu_forward(x.data_ptr(), _in_dtype(x), rows, cols, _ld(x), fmt, rule, h.data_ptr(), cols,
-                             hs.data_ptr(), k, ldk, ks, _stream(stream, dev)), "mx_swiglu_forward")
-    return h, hs, kept
+    r = (_tensors or _ops()).swiglu_mx(x, fmt, rule, keep, stream)
+    return r[0], r[1], SwigluKept(r[2], r[3], fmt) if keep else None
 
 
 def swiglu_mx_backward(kept, dh, stream=None):
     """The gradient (dg, du) [rows][2 cols] at the kept values; dh [rows][cols] and the
     result are float32 or bfloat16."""
-    torch = _torch()
-    _fmt(kept.fmt, "kept.fmt", (E4M3, E5M2))
-    rows, wide = _code_matrix(kept.codes, kept.fmt, "kept.codes")
-    _require(wide % 64 == 0, "kept.codes must have twice a multiple of 32 columns, got %d", wide)
-    _dense(kept.scales, "kept.scales", _scale_dtypes(), (rows, wide // 32))
-    _matrix(dh, "dh", (torch.float32, torch.bfloat16), (rows, wide // 2))
-    dev = _device_of([("kept.codes", kept.codes), ("kept.scales", kept.scales), ("dh", dh)])
-    dx = torch.empty((rows, wide), dtype=dh.dtype, device=dev)
-    _check(mx_swiglu_backward(kept.codes.data_ptr(), _ld(kept.codes), kept.scales.data_ptr(), kept.fmt, dh.data_ptr(),
-                              _in_dtype(dh), _ld(dh), rows, wide // 2, dx.data_ptr(), wide, _stream(stream, dev)),
-           "mx_swiglu_backward")
-    return dx
-
-
-def _norm_weight(w, cols):
-    _require(_is_tensor(w) and w.dim() == 1 and w.shape[0] == cols and w.dtype == _torch().float32
-             and w.is_contiguous(), "w must be a contiguous float32 vector of %d", cols)
+    return (_tensors or _ops()).swiglu_mx_backward(kept.codes, kept.scales, kept.fmt, dh, stream)
 
 
 def rmsnorm_mx(x, w, eps, fmt=E4M3, rule=RULE_CEIL, keep=True, stream=None):
     """y = x / sqrt(mean(x^2) + eps) * w along rows as MX codes: (y [rows][cols], scales
     [rows][cols / 32], RmsnormKept for rmsnorm_mx_backward, or None with keep=False)."""
-    torch = _torch()
-    _fmt(fmt, "fmt", (E4M3, E5M2))
-    rows, cols = _input(x, "x")
-    _blocks(cols, "x")
-    _norm_weight(w, cols)
-    dev = _device_of([("x", x), ("w", w)])
-    y = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
-    ys = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
-    kept, k, ks, r = None, None, None, None
-    if keep:
-        kept = RmsnormKept(torch.empty((rows, cols), dtype=torch.uint8, device=dev),
-                           torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev),
-                           torch.empty((rows,), dtype=torch.float32, device=dev), fmt)
-        k, ks, r = kept.codes.data_ptr(), kept.scales.data_ptr(), kept.rstd.data_ptr()
-    _check(mx_rmsnorm_forward(x.data_ptr(), _in_dtype(x), rows, cols, _ld(x), w.data_ptr(), eps, fmt, rule,
-                              y.data_ptr(), cols, ys.data_ptr(), k, cols if keep else 0, ks, r, _stream(stream, dev)),
-           "mx_rmsnorm_forward")
-    return y, ys, kept
+    r = (_tensors or _ops()).rmsnorm_mx(x, w, eps, fmt, rule, keep, stream)
+    return r[0], r[1], RmsnormKept(r[2], r[3], r[4], fmt) if keep else None
 
 
 def rmsnorm_mx_backward(kept, w, dy, stream=None):
     """(dx [rows][cols] of dy's dtype, dw [cols] float32) at the kept values."""
-    torch = _torch()
-    _fmt(kept.fmt, "kept.fmt", (E4M3, E5M2))
-    rows, cols = _code_matrix(kept.codes, kept.fmt, "kept.codes")
-    _blocks(cols, "kept.codes")
-    _dense(kept.scales, "kept.scales", _scale_dtypes(), (rows, cols // 32))
-    _require(_is_tensor(kept.rstd) and kept.rstd.dtype == torch.float32 and tuple(kept.rstd.shape) == (rows,)
-             and kept.rstd.is_contiguous(), "kept.rstd must be a contiguous float32 vector of %d", rows)
-    _norm_weight(w, cols)
-    _matrix(dy, "dy", (torch.float32, torch.bfloat16), (rows, cols))
-    dev = _device_of([("kept.codes", kept.codes), ("kept.scales", kept.scales), ("kept.rstd", kept.rstd), ("w", w),
-                      ("dy", dy)])
-    handle = _stream(stream, dev)
-    dx = torch.empty((rows, cols), dtype=dy.dtype, device=dev)
-    dw = torch.empty((cols,), dtype=torch.float32, device=dev)
-    work = torch.empty((mx_rmsnorm_backward_workspace(rows, cols),), dtype=torch.uint8, device=dev)
-    if stream is not None:
-        work.record_stream(stream)  # freed here, used there
-    _check(mx_rmsnorm_backward(kept.codes.data_ptr(), _ld(kept.codes), kept.scales.data_ptr(), kept.rstd.data_ptr(),
-                               kept.fmt, w.data_ptr(), dy.data_ptr(), _in_dtype(dy), _ld(dy), rows, cols,
-                               dx.data_ptr(), cols, dw.data_ptr(), work.data_ptr(), handle), "mx_rmsnorm_backward")
-    return dx, dw
+    return (_tensors or _ops()).rmsnorm_mx_backward(kept.codes, kept.scales, kept.rstd, kept.fmt, w, dy, stream)

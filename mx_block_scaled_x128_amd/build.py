@@ -1,7 +1,9 @@
-"""Build libmxfp8.so (HIP kernels + C ABI) for gfx950 with hipcc, in-tree.
+"""Build libmxfp8.so (HIP kernels + C ABI) for gfx950 with hipcc, in-tree, and
+_tensors.so, the Python extension with the MX operators' tensor functions.
 
 The sources compile to objects in parallel (the GEMM once per pair of operand
-formats, plus its host dispatch), which hipcc then links into the library.
+formats, plus its host dispatch; the MXFP4 product once per format of its left
+operand), which hipcc then links into the library.
 
 Usage: python -m mx_block_scaled_x128_amd.build   (always recompiles)
 """
@@ -10,19 +12,23 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmxfp8.so")
+TENSORS = os.path.join(HERE, "_tensors.so")
 ARCH = "gfx950"
 # (source, extra flags, object name)
 UNITS = [("api.cpp", [], "api"), ("mx_api.cpp", [], "mx_api"), ("mx_quant.hip", [], "mx_quant"),
-         ("mx_act.hip", [], "mx_act"), ("mxfp4_gemm.hip", [], "mxfp4_gemm"),
+         ("mx_act.hip", [], "mx_act"), 
+         ("mxfp4_gemm.hip", ["-DMXFP4_GEMM_FMT=-1"], "mxfp4_gemm_dispatch"),
          ("quant.hip", [], "quant"), ("gaussws.hip", [], "gaussws"),
          ("gemm.hip", ["-DMXFP8_GEMM_FMT=-1"], "gemm_dispatch")] + \
-        [("gemm.hip", ["-DMXFP8_GEMM_FMT=%d" % k], "gemm_fmt%d" % k) for k in range(4)]
+        [("gemm.hip", ["-DMXFP8_GEMM_FMT=%d" % k], "gemm_fmt%d" % k) for k in range(4)] + \
+        [("mxfp4_gemm.hip", ["-DMXFP4_GEMM_FMT=%d" % k], "mxfp4_gemm_fmt%d" % k) for k in range(3)]
 
 FLAGS = [
     "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC",
@@ -49,12 +55,25 @@ def _run(cmd):
     return err
 
 
+def tensors_command(cc, out):
+    """The extension: host code against torch's headers and libraries."""
+    import torch
+    base = os.path.dirname(torch.__file__)
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"]]
+    return [cc, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-DTORCH_EXTENSION_NAME=_tensors",
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI] + \
+        [a for d in inc for a in ("-isystem", d)] + [os.path.join(CSRC, "tensors.cpp"), "-L" + os.path.join(base, "lib")] + \
+        ["-l" + n for n in ("c10", "c10_hip", "torch_cpu", "torch", "torch_python")] + ["-o", out]
+
+
 def build(verbose=False, jobs=None):
     cc = hipcc()
     tmpdir = tempfile.mkdtemp(prefix="mxfp8_build_")
     try:
         cmds = [[cc] + FLAGS + extra + ["-c", os.path.join(CSRC, src), "-o", os.path.join(tmpdir, name + ".o")]
                 for src, extra, name in UNITS]
+        cmds.insert(0, tensors_command(cc, TENSORS + ".tmp"))  # the longest first
         if verbose:
             for c in cmds:
                 print(" ".join(c), flush=True)
@@ -72,6 +91,7 @@ def build(verbose=False, jobs=None):
                 if e.strip():
                     print(e, file=sys.stderr)
         os.replace(tmp, LIB)
+        os.replace(TENSORS + ".tmp", TENSORS)
     finally:
         shutil.rmtree(tmpdir, ignore_errors=True)
     return LIB

@@ -10,9 +10,22 @@
 #include "mx_common.hpp"
 #include "mx_launch.hpp"
 
+// One translation unit can hold everything (MXFP4_GEMM_FMT undefined), or the
+// build compiles this file once per format of A in parallel (0, 1, 2) and once
+// with -1 for the host dispatch alone.
+#ifndef MXFP4_GEMM_FMT
+#define MXFP4_GEMM_FMT 3
+#endif
+
 namespace mxfp8 {
 
 namespace mxfp4_detail {
+
+template <int AFMT>
+void gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const uint8_t* sa, const uint8_t* b,
+          int64_t ldb, const uint8_t* sb, void* c, int64_t ldc, int c_dtype, hipStream_t stream);
+
+#if MXFP4_GEMM_FMT >= 0
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
@@ -636,8 +649,23 @@ void gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const 
   }
 }
 
+#define MXFP4_GEMM(FMT)                                                                                      \
+  template void gemm<FMT>(int64_t, int64_t, int64_t, const uint8_t*, int64_t, const uint8_t*, const uint8_t*, \
+                          int64_t, const uint8_t*, void*, int64_t, int, hipStream_t);
+#if MXFP4_GEMM_FMT == 3
+MXFP4_GEMM(0)
+MXFP4_GEMM(1)
+MXFP4_GEMM(2)
+#else
+MXFP4_GEMM(MXFP4_GEMM_FMT)
+#endif
+#undef MXFP4_GEMM
+
+#endif  // MXFP4_GEMM_FMT >= 0
+
 }  // namespace mxfp4_detail
 
+#if MXFP4_GEMM_FMT == 3 || MXFP4_GEMM_FMT < 0
 void launch_mxfp4_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, int a_fmt, const uint8_t* sa,
                        const uint8_t* b, int64_t ldb, const uint8_t* sb, void* c, int64_t ldc, int c_dtype,
                        hipStream_t stream) {
@@ -646,5 +674,7 @@ void launch_mxfp4_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_
   else if (a_fmt == 1) gemm<1>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, stream);
   else gemm<kE2M1>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, stream);
 }
+
+#endif
 
 }  // namespace mxfp8

@@ -1,0 +1,329 @@
+// tensors.cpp -- the tensor functions of the MX operators as a Python
+// extension (_tensors): checks of the tensors, allocation of the outputs and
+// one call of the C ABI each.  The same checks in Python cost about 9 us a
+// call, several times what the small kernels take; here they cost under one.
+// Nothing computes here, and the C functions are those of the library that
+// mx_block_scaled_x128_amd loads (bind).
+#include <ATen/ATen.h>
+#include <c10/hip/HIPFunctions.h>
+#include <c10/hip/HIPStream.h>
+#include <dlfcn.h>
+#include <torch/extension.h>
+
+#include <string>
+
+#include "../../include/mxfp8.h"
+
+namespace {
+
+struct Library {
+  decltype(&::mxfp4_quantize) mxfp4_quantize;
+  decltype(&::mx_dequantize) mx_dequantize;
+  decltype(&::mx_quantize_t) mx_quantize_t;
+  decltype(&::mx_requantize_t) mx_requantize_t;
+  decltype(&::mxfp4_gemm) mxfp4_gemm;
+  decltype(&::mx_swiglu_forward) mx_swiglu_forward;
+  decltype(&::mx_swiglu_backward) mx_swiglu_backward;
+  decltype(&::mx_rmsnorm_forward) mx_rmsnorm_forward;
+  decltype(&::mx_rmsnorm_backward) mx_rmsnorm_backward;
+  decltype(&::mx_rmsnorm_backward_workspace) mx_rmsnorm_backward_workspace;
+} lib;
+
+void bind(const std::string& path) {
+  void* h = dlopen(path.c_str(), RTLD_NOW);
+  if (!h) throw py::import_error(dlerror());
+  auto find = [&](auto& f, const char* name) {
+    f = reinterpret_cast<std::decay_t<decltype(f)>>(dlsym(h, name));
+    if (!f) throw py::import_error(std::string(name) + " is missing from " + path);
+  };
+#define MXFP8_FIND(name) find(lib.name, #name)
+  MXFP8_FIND(mxfp4_quantize);
+  MXFP8_FIND(mx_dequantize);
+  MXFP8_FIND(mx_quantize_t);
+  MXFP8_FIND(mx_requantize_t);
+  MXFP8_FIND(mxfp4_gemm);
+  MXFP8_FIND(mx_swiglu_forward);
+  MXFP8_FIND(mx_swiglu_backward);
+  MXFP8_FIND(mx_rmsnorm_forward);
+  MXFP8_FIND(mx_rmsnorm_backward);
+  MXFP8_FIND(mx_rmsnorm_backward_workspace);
+#undef MXFP8_FIND
+}
+
+// ---- checks.  The text is put together only when a check fails.
+
+template <typename... Part>
+[[noreturn]] void refuse(const Part&... part) {
+  std::ostringstream s;
+  (s << ... << part);
+  throw py::value_error(s.str());
+}
+#define REQUIRE(cond, ...)             \
+  do {                                 \
+    if (!(cond)) refuse(__VA_ARGS__);  \
+  } while (0)
+
+void status(int st, const char* where) {
+  if (st == MXFP8_OK) return;
+  py::object error = py::module_::import("mx_block_scaled_x128_amd").attr("MxFp8Error");
+  PyErr_SetObject(error.ptr(), error(st, where).ptr());
+  throw py::error_already_set();
+}
+
+bool is_real(const at::Tensor& t) { return t.scalar_type() == at::kFloat || t.scalar_type() == at::kBFloat16; }
+int real_type(const at::Tensor& t) { return t.scalar_type() == at::kFloat ? MXFP8_F32 : MXFP8_BF16; }
+int64_t ld(const at::Tensor& t) { return t.size(0) > 1 ? t.stride(0) : std::max(t.stride(0), t.size(1)); }
+void* ptr(const at::Tensor& t) { return t.data_ptr(); }
+uint8_t* bytes(const at::Tensor& t) { return static_cast<uint8_t*>(t.data_ptr()); }
+
+// A 2-D tensor with unit column stride whose rows do not overlap.
+void layout(const at::Tensor& t, const char* name) {
+  REQUIRE(t.dim() == 2, name, " must be 2-D, got ", t.dim(), "-D");
+  REQUIRE(t.size(1) <= 1 || t.stride(1) == 1, name, " must have unit column stride");
+  REQUIRE(t.size(0) <= 1 || t.stride(0) >= t.size(1), name, " rows must not overlap");
+}
+void shape(const at::Tensor& t, const char* name, int64_t rows, int64_t cols) {
+  REQUIRE(t.dim() == 2 && t.size(0) == rows && t.size(1) == cols, name, " must have shape (", rows, ", ", cols,
+          "), got ", t.sizes());
+}
+void real_matrix(const at::Tensor& t, const char* name) {
+  layout(t, name);
+  REQUIRE(is_real(t), name, " must be float32 or bfloat16, got ", t.scalar_type());
+}
+bool one_byte(const at::Tensor& t, bool codes) {
+  const auto s = t.scalar_type();
+  return s == at::kByte || (codes ? s == at::kFloat8_e4m3fn || s == at::kFloat8_e5m2 : s == at::kFloat8_e8m0fnu);
+}
+// A matrix of codes; the elements of a row.
+int64_t codes(const at::Tensor& t, int fmt, const char* name) {
+  layout(t, name);
+  REQUIRE(fmt == MXFP8_E2M1 ? t.scalar_type() == at::kByte : one_byte(t, true), name, " must hold codes (uint8",
+          fmt == MXFP8_E2M1 ? "" : " or float8", "), got ", t.scalar_type());
+  return fmt == MXFP8_E2M1 ? t.size(1) * 2 : t.size(1);
+}
+void scales(const at::Tensor& t, const char* name, int64_t rows, int64_t blocks) {
+  REQUIRE(one_byte(t, false), name, " must be uint8 or float8_e8m0fnu, got ", t.scalar_type());
+  shape(t, name, rows, blocks);
+  REQUIRE(t.is_contiguous(), name, " must be contiguous");
+}
+void vector(const at::Tensor& t, const char* name, int64_t n) {
+  REQUIRE(t.dim() == 1 && t.size(0) == n && t.scalar_type() == at::kFloat && t.is_contiguous(), name,
+          " must be a contiguous float32 vector of ", n);
+}
+void blocks32(int64_t cols, const char* name) {
+  REQUIRE(cols % 32 == 0, name, " must have a multiple of 32 columns, got ", cols);
+}
+void format(int fmt, const char* name, bool with_e2m1) {
+  REQUIRE(fmt == MXFP8_E4M3 || fmt == MXFP8_E5M2 || (with_e2m1 && fmt == MXFP8_E2M1), name, " must be E4M3",
+          with_e2m1 ? ", E5M2 or E2M1" : " or E5M2", ", got ", fmt);
+}
+
+// All tensors on the current device; its index.
+int device_of(std::initializer_list<const at::Tensor*> all) {
+  int dev = -1;
+  for (const at::Tensor* t : all) {
+    REQUIRE(t->is_cuda(), "expected a CUDA tensor, got device ", t->device());
+    const int i = t->get_device();
+    REQUIRE(dev < 0 || i == dev, "tensors are on cuda:", dev, " and cuda:", i);
+    dev = i;
+  }
+  const int cur = c10::hip::current_device();
+  REQUIRE(dev == cur, "tensors are on cuda:", dev, " but the current device is cuda:", cur);
+  return dev;
+}
+void* stream_of(const py::object& stream, int dev) {
+  if (stream.is_none()) return c10::hip::getCurrentHIPStream(dev).stream();
+  const int i = stream.attr("device").attr("index").cast<int>();
+  REQUIRE(i == dev, "stream is on cuda:", i, " but the tensors are on cuda:", dev);
+  return reinterpret_cast<void*>(stream.attr("cuda_stream").cast<uintptr_t>());
+}
+
+at::Tensor fresh(at::IntArrayRef size, at::ScalarType type, int dev) {
+  return at::empty(size, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, (c10::DeviceIndex)dev)));
+}
+// Uninitialized [rows][cols] with rows of a multiple of 16 elements.
+at::Tensor pitched(int64_t rows, int64_t cols, at::ScalarType type, int dev) {
+  const int64_t pitch = std::max<int64_t>((cols + 15) / 16 * 16, 16);
+  at::Tensor t = fresh({rows, pitch}, type, dev);
+  return pitch == cols ? t : t.narrow(1, 0, cols);
+}
+int64_t filled_rows(int64_t rows, const c10::optional<int64_t>& rows_out) {
+  if (!rows_out.has_value()) return (rows + 127) / 128 * 128;
+  REQUIRE(*rows_out % 32 == 0 && *rows_out >= rows, "rows_out must be a multiple of 32 and at least ", rows, ", got ",
+          *rows_out);
+  return *rows_out;
+}
+
+// ---- the functions
+
+py::tuple quantize_mxfp4(const at::Tensor& x, int rule, const py::object& stream) {
+  real_matrix(x, "x");
+  const int64_t rows = x.size(0), cols = x.size(1);
+  blocks32(cols, "x");
+  const int dev = device_of({&x});
+  at::Tensor q = pitched(rows, cols / 2, at::kByte, dev), s = fresh({rows, cols / 32}, at::kByte, dev);
+  status(lib.mxfp4_quantize(ptr(x), real_type(x), rows, cols, ld(x), rule, bytes(q), ld(q), bytes(s),
+                            stream_of(stream, dev)), "mxfp4_quantize");
+  return py::make_tuple(q, s);
+}
+
+at::Tensor dequantize_mx(const at::Tensor& q, const at::Tensor& s, int fmt, at::ScalarType dtype,
+                         const py::object& stream) {
+  format(fmt, "fmt", true);
+  const int64_t rows = q.size(0), cols = codes(q, fmt, "q");
+  blocks32(cols, "q");
+  scales(s, "scales", rows, cols / 32);
+  REQUIRE(dtype == at::kFloat || dtype == at::kBFloat16, "dtype must be float32 or bfloat16, got ", dtype);
+  const int dev = device_of({&q, &s});
+  at::Tensor y = fresh({rows, cols}, dtype, dev);
+  status(lib.mx_dequantize(bytes(q), ld(q), fmt, bytes(s), rows, cols, ptr(y), real_type(y), ld(y),
+                           stream_of(stream, dev)), "mx_dequantize");
+  return y;
+}
+
+py::tuple quantize_mx_t(const at::Tensor& x, int fmt, int rule, const c10::optional<int64_t>& rows_out,
+                        const py::object& stream) {
+  format(fmt, "fmt", true);
+  real_matrix(x, "x");
+  const int64_t rows = x.size(0), cols = x.size(1), out = filled_rows(rows, rows_out);
+  REQUIRE(cols % 16 == 0, "x must have a multiple of 16 columns, got ", cols);
+  const int dev = device_of({&x});
+  at::Tensor qt = pitched(cols, fmt == MXFP8_E2M1 ? out / 2 : out, at::kByte, dev);
+  at::Tensor st = fresh({cols, out / 32}, at::kByte, dev);
+  status(lib.mx_quantize_t(ptr(x), real_type(x), rows, cols, ld(x), fmt, rule, bytes(qt), ld(qt), out, bytes(st),
+                           stream_of(stream, dev)), "mx_quantize_t");
+  return py::make_tuple(qt, st);
+}
+
+py::tuple requantize_mx_t(const at::Tensor& q, const at::Tensor& s, int q_fmt, int fmt, int rule,
+                          const c10::optional<int64_t>& rows_out, const py::object& stream) {
+  format(q_fmt, "q_fmt", false);
+  format(fmt, "fmt", true);
+  const int64_t rows = q.size(0), cols = codes(q, q_fmt, "q"), out = filled_rows(rows, rows_out);
+  blocks32(cols, "q");
+  scales(s, "scales", rows, cols / 32);
+  const int dev = device_of({&q, &s});
+  at::Tensor qt = pitched(cols, fmt == MXFP8_E2M1 ? out / 2 : out, at::kByte, dev);
+  at::Tensor st = fresh({cols, out / 32}, at::kByte, dev);
+  status(lib.mx_requantize_t(bytes(q), ld(q), q_fmt, bytes(s), rows, cols, fmt, rule, bytes(qt), ld(qt), out,
+                             bytes(st), stream_of(stream, dev)), "mx_requantize_t");
+  return py::make_tuple(qt, st);
+}
+
+at::Tensor mxfp4_scaled_gemm(const at::Tensor& a, const at::Tensor& sa, int a_fmt, const at::Tensor& b,
+                             const at::Tensor& sb, const c10::optional<at::ScalarType>& out_dtype,
+                             const c10::optional<at::Tensor>& out, const py::object& stream) {
+  format(a_fmt, "a_fmt", true);
+  const int64_t K = codes(a, a_fmt, "a"), kb = codes(b, MXFP8_E2M1, "b"), M = a.size(0), N = b.size(0);
+  REQUIRE(kb == K, "a has K = ", K, " but b has K = ", kb);
+  REQUIRE(K % 128 == 0, "mxfp4_scaled_gemm: K must be a multiple of 128, got ", K);
+  scales(sa, "a_scales", M, K / 32);
+  scales(sb, "b_scales", N, K / 32);
+  at::Tensor c;
+  int dev;
+  if (out.has_value()) {
+    c = *out;
+    real_matrix(c, "out");
+    shape(c, "out", M, N);
+    dev = device_of({&a, &sa, &b, &sb, &c});
+  } else {
+    const at::ScalarType type = out_dtype.value_or(at::kFloat);
+    REQUIRE(type == at::kFloat || type == at::kBFloat16, "out_dtype must be float32 or bfloat16, got ", type);
+    dev = device_of({&a, &sa, &b, &sb});
+    c = pitched(M, N, type, dev);
+  }
+  status(lib.mxfp4_gemm(M, N, K, bytes(a), ld(a), a_fmt, bytes(sa), bytes(b), ld(b), bytes(sb), ptr(c), ld(c),
+                        real_type(c), stream_of(stream, dev)), "mxfp4_gemm");
+  return c;
+}
+
+py::tuple swiglu_mx(const at::Tensor& x, int fmt, int rule, bool keep, const py::object& stream) {
+  format(fmt, "fmt", false);
+  real_matrix(x, "x");
+  const int64_t rows = x.size(0), wide = x.size(1), cols = wide / 2;
+  REQUIRE(wide % 64 == 0, "x must have twice a multiple of 32 columns, got ", wide);
+  const int dev = device_of({&x});
+  at::Tensor h = fresh({rows, cols}, at::kByte, dev), hs = fresh({rows, cols / 32}, at::kByte, dev), k, ks;
+  if (keep) {
+    k = fresh({rows, wide}, at::kByte, dev);
+    ks = fresh({rows, wide / 32}, at::kByte, dev);
+  }
+  status(lib.mx_swiglu_forward(ptr(x), real_type(x), rows, cols, ld(x), fmt, rule, bytes(h), cols, bytes(hs),
+                               keep ? bytes(k) : nullptr, wide, keep ? bytes(ks) : nullptr, stream_of(stream, dev)),
+         "mx_swiglu_forward");
+  if (!keep) return py::make_tuple(h, hs);
+  return py::make_tuple(h, hs, k, ks);
+}
+
+at::Tensor swiglu_mx_backward(const at::Tensor& k, const at::Tensor& ks, int fmt, const at::Tensor& dh,
+                              const py::object& stream) {
+  format(fmt, "kept.fmt", false);
+  const int64_t rows = k.size(0), wide = codes(k, fmt, "kept.codes");
+  REQUIRE(wide % 64 == 0, "kept.codes must have twice a multiple of 32 columns, got ", wide);
+  scales(ks, "kept.scales", rows, wide / 32);
+  real_matrix(dh, "dh");
+  shape(dh, "dh", rows, wide / 2);
+  const int dev = device_of({&k, &ks, &dh});
+  at::Tensor dx = fresh({rows, wide}, dh.scalar_type(), dev);
+  status(lib.mx_swiglu_backward(bytes(k), ld(k), bytes(ks), fmt, ptr(dh), real_type(dh), ld(dh), rows, wide / 2,
+                                ptr(dx), wide, stream_of(stream, dev)), "mx_swiglu_backward");
+  return dx;
+}
+
+py::tuple rmsnorm_mx(const at::Tensor& x, const at::Tensor& w, double eps, int fmt, int rule, bool keep,
+                     const py::object& stream) {
+  format(fmt, "fmt", false);
+  real_matrix(x, "x");
+  const int64_t rows = x.size(0), cols = x.size(1);
+  blocks32(cols, "x");
+  vector(w, "w", cols);
+  const int dev = device_of({&x, &w});
+  at::Tensor y = fresh({rows, cols}, at::kByte, dev), ys = fresh({rows, cols / 32}, at::kByte, dev), k, ks, r;
+  if (keep) {
+    k = fresh({rows, cols}, at::kByte, dev);
+    ks = fresh({rows, cols / 32}, at::kByte, dev);
+    r = fresh({rows}, at::kFloat, dev);
+  }
+  status(lib.mx_rmsnorm_forward(ptr(x), real_type(x), rows, cols, ld(x), static_cast<float*>(ptr(w)), (float)eps, fmt,
+                                rule, bytes(y), cols, bytes(ys), keep ? bytes(k) : nullptr, cols,
+                                keep ? bytes(ks) : nullptr, keep ? static_cast<float*>(ptr(r)) : nullptr,
+                                stream_of(stream, dev)), "mx_rmsnorm_forward");
+  if (!keep) return py::make_tuple(y, ys);
+  return py::make_tuple(y, ys, k, ks, r);
+}
+
+py::tuple rmsnorm_mx_backward(const at::Tensor& k, const at::Tensor& ks, const at::Tensor& r, int fmt,
+                              const at::Tensor& w, const at::Tensor& dy, const py::object& stream) {
+  format(fmt, "kept.fmt", false);
+  const int64_t rows = k.size(0), cols = codes(k, fmt, "kept.codes");
+  blocks32(cols, "kept.codes");
+  scales(ks, "kept.scales", rows, cols / 32);
+  vector(r, "kept.rstd", rows);
+  vector(w, "w", cols);
+  real_matrix(dy, "dy");
+  shape(dy, "dy", rows, cols);
+  const int dev = device_of({&k, &ks, &r, &w, &dy});
+  void* on = stream_of(stream, dev);
+  at::Tensor dx = fresh({rows, cols}, dy.scalar_type(), dev), dw = fresh({cols}, at::kFloat, dev);
+  at::Tensor work = fresh({lib.mx_rmsnorm_backward_workspace(rows, cols)}, at::kByte, dev);
+  if (!stream.is_none()) py::cast(work).attr("record_stream")(stream);  // freed here, used there
+  status(lib.mx_rmsnorm_backward(bytes(k), ld(k), bytes(ks), static_cast<float*>(ptr(r)), fmt,
+                                 static_cast<float*>(ptr(w)), ptr(dy), real_type(dy), ld(dy), rows, cols, ptr(dx),
+                                 cols, static_cast<float*>(ptr(dw)), ptr(work), on), "mx_rmsnorm_backward");
+  return py::make_tuple(dx, dw);
+}
+
+}  // namespace
+
+PYBIND11_MODULE(_tensors, m) {
+  m.def("bind", &bind);
+  m.def("quantize_mxfp4", &quantize_mxfp4);
+  m.def("dequantize_mx", &dequantize_mx);
+  m.def("quantize_mx_t", &quantize_mx_t);
+  m.def("requantize_mx_t", &requantize_mx_t);
+  m.def("mxfp4_scaled_gemm", &mxfp4_scaled_gemm);
+  m.def("swiglu_mx", &swiglu_mx);
+  m.def("swiglu_mx_backward", &swiglu_mx_backward);
+  m.def("rmsnorm_mx", &rmsnorm_mx);
+  m.def("rmsnorm_mx_backward", &rmsnorm_mx_backward);
+}
