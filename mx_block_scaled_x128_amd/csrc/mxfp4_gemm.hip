@@ -65,117 +65,259 @@ __device__ __forceinline__ void store4(uint16_t* p, v4f v, int64_t left) {
   }
 }
 
+// Operands are read through buffer descriptors whose range check returns
+// zeros for lanes whose offset is set to kOutside: rows past M or N, K past
+// its end, scales past a row's end.  Zero codes under a zero scale byte
+// (2^-127) add nothing, so no edge needs a branch.
+[[maybe_unused]] constexpr uint32_t kRange = 0xF0000000u;    // bytes behind a descriptor; valid offsets stay below 2^31
+[[maybe_unused]] constexpr uint32_t kOutside = 0xF8000000u;
+
+#if defined(__HIP_DEVICE_COMPILE__)
+typedef __attribute__((address_space(3))) void lds_void;
+template <int BYTES>
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t rsrc, uint8_t* to, uint32_t lane_off, uint32_t off) {
+  if constexpr (BYTES == 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)to, 16, lane_off, off, 0, 0);
+  else __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)to, 4, lane_off, off, 0, 0);
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t descriptor(const uint8_t* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, (int)kRange, 0x00020000);
+}
+#endif
+
+// Wait for this wave's loads and LDS reads, then meet the others: a bare
+// s_barrier, since __syncthreads() would add a release fence.
+template <int N>
+__device__ __forceinline__ void wait_loads_and_meet() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  static_assert(N >= 0 && N <= 63, "vmcnt");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+  asm volatile("s_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+#endif
+}
+
 // ---------------------------------------------------------------------------
 // Few rows of A.  A workgroup owns 16 MT rows of A x 16 NT rows of B; its
 // waves split K in contiguous runs of 128-wide chunks and add up their
 // accumulators through LDS at the end, in a fixed order.  B goes from memory
-// to the matrix cores' registers without LDS: each of its bytes is used by
-// one wave only.  v_mfma_scale_f32_16x16x128: lane l holds row l & 15 of both
+// to registers without LDS (each of its bytes is used by one wave only), U
+// chunks at a time, the next U on their way while these multiply; the scales
+// of the workgroup's rows, and A itself where it fits (ALDS), are copied to
+// LDS first.  v_mfma_scale_f32_16x16x128: lane l holds row l & 15 of both
 // operands and, with g = l >> 4, the 32 E2M1 elements 32 g .. +31 of the
 // chunk (16 bytes), or of FP8 the bytes 16 g .. +15 and 64 + 16 g .. +15; the
 // scale of the chunk's 32-wide block g is taken from the lanes of group g.
 // Operands are swapped (B first), so a lane's four results are four
 // consecutive columns of C.
+//
+// What bounds it: the load path of a CU takes about 40 cycles for an
+// instruction that gathers 16 rows x 64 bytes, whatever it brings, so the
+// count of those is what matters: one per 16 rows and chunk of B, and of A
+// unless it is in LDS; then latency, and about 1 us per 1000 waves started.
 // ---------------------------------------------------------------------------
-template <int AFMT, int MT, int NT, int WAVES, typename OutT>
+#if defined(__HIP_DEVICE_COMPILE__)
+__device__ __forceinline__ v4i load16(__amdgpu_buffer_rsrc_t rsrc, uint32_t lane_off, uint32_t off) {
+  return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rsrc, lane_off, off, 0));
+}
+// n bytes (a multiple of 4) from p to LDS, by the waves of a workgroup in turn.
+template <int WAVES>
+__device__ __forceinline__ void copy_to_lds(const uint8_t* p, int n, uint8_t* to, int wave, int lane) {
+  const __amdgpu_buffer_rsrc_t rsrc = descriptor(p);
+  if (((uintptr_t)p & 15) == 0 && (n & 15) == 0) {
+    for (int at = wave * 1024; at < n; at += WAVES * 1024)
+      load_lds<16>(rsrc, to + at, at + lane * 16 < n ? lane * 16 : kOutside, at);
+  } else {
+    for (int at = wave * 256; at < n; at += WAVES * 256)
+      load_lds<4>(rsrc, to + at, at + lane * 4 < n ? lane * 4 : kOutside, at);
+  }
+}
+#endif
+
+// LDS of the few-row kernel, in bytes: A's scales, B's scales, A, each in
+// whole kilobytes (a copy fills whole ones); the partial sums of the waves
+// take their place at the end.
+__host__ __device__ constexpr int kilo(int n) { return (n + 1023) & ~1023; }
+template <int AFMT, int MT, int NT, int WAVES, bool ALDS>
+__host__ __device__ inline int few_rows_lds(int rows, int K) {
+  const int a = AFMT == kE2M1 ? K / 2 : K;
+  const int in = kilo(16 * MT * (K / 32)) + kilo(16 * NT * (K / 32)) + (ALDS ? kilo(rows * a) : 0);
+  const int out = WAVES > 1 ? WAVES * MT * NT * 1024 : 0;
+  return in > out ? in : out;
+}
+
+template <int AFMT, int MT, int NT, int WAVES, int U, bool ALDS, typename OutT>
 __global__ __launch_bounds__(WAVES * 64) void few_rows_kernel(int M, int N, int K, const uint8_t* __restrict__ A,
                                                               int64_t lda, const uint8_t* __restrict__ SA,
                                                               const uint8_t* __restrict__ B, int64_t ldb,
                                                               const uint8_t* __restrict__ SB, OutT* __restrict__ C,
                                                               int64_t ldc) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  __shared__ v4f red[WAVES > 1 ? (WAVES - 1) * MT * NT * 64 : 1];
+  constexpr int PARTS = AFMT == kE2M1 ? 1 : 2;  // 16-byte parts of A per lane and chunk
+  constexpr int AB = 64 * PARTS;                // bytes of a chunk of a row of A
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * (16 * NT), m0 = blockIdx.y * (16 * MT);
+  const int tiles_n = (N + 16 * NT - 1) / (16 * NT);
+  const int n0 = (int)(blockIdx.x % tiles_n) * (16 * NT), m0 = (int)(blockIdx.x / tiles_n) * (16 * MT);
+  const int rows_a = min(16 * MT, M - m0), rows_b = min(16 * NT, N - n0);
   const int chunks = K >> 7, sk = K >> 5;
   const int c0 = (int)((int64_t)chunks * wave / WAVES), c1 = (int)((int64_t)chunks * (wave + 1) / WAVES);
-  const uint8_t *bp[NT], *sbp[NT], *ap[MT], *sap[MT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int64_t row = min(n0 + 16 * t + r, N - 1);  // rows past the end: results dropped
-    bp[t] = B + row * ldb + 16 * g;
-    sbp[t] = SB + row * sk;
+  uint8_t *lsa = lds, *lsb = lsa + kilo(16 * MT * sk), *la = lsb + kilo(16 * NT * sk);
+
+  copy_to_lds<WAVES>(SA + (int64_t)m0 * sk, rows_a * sk, lsa, wave, lane);
+  copy_to_lds<WAVES>(SB + (int64_t)n0 * sk, rows_b * sk, lsb, wave, lane);
+  const __amdgpu_buffer_rsrc_t ra = descriptor(A + (int64_t)m0 * lda), rb = descriptor(B + (int64_t)n0 * ldb);
+  const int apr = chunks * AB;  // bytes of a row of A
+  if constexpr (ALDS) {
+    const int n = rows_a * apr;
+    for (int at = wave * 1024; at < n; at += WAVES * 1024) {
+      const int i = at + lane * 16, row = i / apr;
+      load_lds<16>(ra, la + at, i < n ? (uint32_t)(row * lda + (i - row * apr)) : kOutside, 0);
+    }
   }
+  // Rows past M or N repeat the last one's: what they give is dropped.
+  uint32_t ao[MT], bo[NT];
+  int sao[MT], sbo[NT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
-    const int64_t row = min(m0 + 16 * t + r, M - 1);
-    ap[t] = A + row * lda + 16 * g;
-    sap[t] = SA + row * sk;
+    const int row = min(16 * t + r, rows_a - 1);
+    ao[t] = (uint32_t)(ALDS ? row * apr : row * lda) + 16 * g;
+    sao[t] = row * sk + g;
   }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int row = min(16 * t + r, rows_b - 1);
+    bo[t] = (uint32_t)(row * ldb) + 16 * g;
+    sbo[t] = row * sk + g;
+  }
+  constexpr int AREGS = ALDS ? 1 : U;  // chunks of A held in registers
+  struct Batch {
+    v4i b[U][NT], a[AREGS][MT][PARTS];
+  };
+  auto load = [&](int c, Batch& x) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool in = c + u < c1;  // past the wave's run: no traffic
+#pragma unroll
+      for (int t = 0; t < NT; ++t) x.b[u][t] = load16(rb, in ? bo[t] : kOutside, (c + u) * 64);
+      if constexpr (!ALDS) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int part = 0; part < PARTS; ++part)
+            x.a[u][t][part] = load16(ra, in ? ao[t] : kOutside, (c + u) * AB + part * 64);
+      }
+    }
+  };
   v4f acc[MT][NT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int c = c0; c < c1; ++c) {
-    v8i bf[NT], af[MT];
-    int bs[NT], as[MT];
+  auto multiply = [&](int c, Batch& x) __attribute__((always_inline)) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const v4i v = *reinterpret_cast<const v4i*>(bp[t] + c * 64);
-      bf[t] = v8i{v[0], v[1], v[2], v[3], 0, 0, 0, 0};
-      bs[t] = *reinterpret_cast<const int*>(sbp[t] + c * 4) >> (8 * g);
-    }
+    for (int u = 0; u < U; ++u) {
+      if (c + u >= c1) break;
+      int as[MT], bs[NT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      if constexpr (AFMT == kE2M1) {
-        const v4i v = *reinterpret_cast<const v4i*>(ap[t] + c * 64);
-        af[t] = v8i{v[0], v[1], v[2], v[3], 0, 0, 0, 0};
-      } else {
-        const v4i v = *reinterpret_cast<const v4i*>(ap[t] + c * 128);
-        const v4i u = *reinterpret_cast<const v4i*>(ap[t] + c * 128 + 64);
-        af[t] = v8i{v[0], v[1], v[2], v[3], u[0], u[1], u[2], u[3]};
+      for (int t = 0; t < NT; ++t) bs[t] = lsb[sbo[t] + (c + u) * 4];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) as[t] = lsa[sao[t] + (c + u) * 4];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        v4i lo, hi = v4i{0, 0, 0, 0};
+        if constexpr (ALDS) {
+          lo = *reinterpret_cast<const v4i*>(la + ao[i] + (c + u) * AB);
+          if constexpr (PARTS == 2) hi = *reinterpret_cast<const v4i*>(la + ao[i] + (c + u) * AB + 64);
+        } else {
+          lo = x.a[u][i][0];
+          if constexpr (PARTS == 2) hi = x.a[u][i][PARTS - 1];
+        }
+        const v8i af = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const v8i bf = v8i{x.b[u][j][0], x.b[u][j][1], x.b[u][j][2], x.b[u][j][3], 0, 0, 0, 0};
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf, af, acc[i][j], kMfmaFmt<kE2M1>,
+                                                                      kMfmaFmt<AFMT>, 0, bs[j], 0, as[i]);
+        }
       }
-      as[t] = *reinterpret_cast<const int*>(sap[t] + c * 4) >> (8 * g);
     }
+  };
+  // The first two batches travel with the copies; everything has landed, in
+  // every wave, before the first product.  (The empty asm uses their
+  // registers: the loads cannot be moved past the wait.)
+  Batch x, y;
+  load(c0, x);
+  load(c0 + U, y);
+  auto pin = [](Batch& v) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) asm volatile("" : "+v"(v.b[u][t]));
+    if constexpr (!ALDS) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int part = 0; part < PARTS; ++part) asm volatile("" : "+v"(v.a[u][t][part]));
+    }
+  };
+  pin(x);
+  pin(y);
+  wait_loads_and_meet<0>();
+  for (int c = c0; c < c1; c += 2 * U) {
+    multiply(c, x);
+    __builtin_amdgcn_sched_barrier(0);  // each load is issued a batch ahead of its use
+    load(c + 2 * U, x);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(c + U, y);
+    __builtin_amdgcn_sched_barrier(0);
+    load(c + 3 * U, y);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  mfma_retire_pad();
+  auto store = [&](int i, int j, v4f v) __attribute__((always_inline)) {
+    const int m = m0 + 16 * i + r, n = n0 + 16 * j + 4 * g;
+    if (m < M) store4(C + (int64_t)m * ldc + n, v, N - n);
+  };
+  if constexpr (WAVES == 1) {
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af[i], acc[i][j], kMfmaFmt<kE2M1>,
-                                                                    kMfmaFmt<AFMT>, 0, bs[j], 0, as[i]);
-  }
-  mfma_retire_pad();
-  if constexpr (WAVES > 1) {
-    if (wave > 0) {
+      for (int j = 0; j < NT; ++j) store(i, j, acc[i][j]);
+  } else {
+    __syncthreads();  // the scales and A have been read
+    v4f* red = reinterpret_cast<v4f*>(lds);
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) red[(((wave - 1) * MT + i) * NT + j) * 64 + lane] = acc[i][j];
-    }
+      for (int j = 0; j < NT; ++j) red[((wave * MT + i) * NT + j) * 64 + lane] = acc[i][j];
     __syncthreads();
-    if (wave > 0) return;
-    for (int w = 0; w < WAVES - 1; ++w) {
+    for (int f = wave; f < MT * NT; f += WAVES) {  // a fragment per wave
+      v4f sum = red[f * 64 + lane];
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] += red[((w * MT + i) * NT + j) * 64 + lane];
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int m = m0 + 16 * i + r;
-    if (m >= M) continue;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int n = n0 + 16 * j + 4 * g;
-      store4(C + (int64_t)m * ldc + n, acc[i][j], N - n);
+      for (int w = 1; w < WAVES; ++w) sum += red[(w * MT * NT + f) * 64 + lane];
+      store(f / NT, f % NT, sum);
     }
   }
 #endif
 }
 
-template <int AFMT, int MT, int NT, int WAVES>
+constexpr int kFewRowsLds = 150 * 1024;
+
+template <int AFMT, int MT, int NT, int WAVES, int U, bool ALDS>
 void few_rows(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const uint8_t* sa, const uint8_t* b,
               int64_t ldb, const uint8_t* sb, void* c, int64_t ldc, int c_dtype, hipStream_t stream) {
-  const dim3 grid((uint32_t)((N + 16 * NT - 1) / (16 * NT)), (uint32_t)((M + 16 * MT - 1) / (16 * MT)));
+  const dim3 grid((uint32_t)(((N + 16 * NT - 1) / (16 * NT)) * ((M + 16 * MT - 1) / (16 * MT))));
+  const int lds = few_rows_lds<AFMT, MT, NT, WAVES, ALDS>((int)(M < 16 * MT ? M : 16 * MT), (int)K);
   if (c_dtype == 0)
-    hipLaunchKernelGGL((few_rows_kernel<AFMT, MT, NT, WAVES, float>), grid, dim3(WAVES * 64), 0, stream, (int)M,
-                       (int)N, (int)K, a, lda, sa, b, ldb, sb, static_cast<float*>(c), ldc);
+    hipLaunchKernelGGL((few_rows_kernel<AFMT, MT, NT, WAVES, U, ALDS, float>), grid, dim3(WAVES * 64), lds, stream,
+                       (int)M, (int)N, (int)K, a, lda, sa, b, ldb, sb, static_cast<float*>(c), ldc);
   else
-    hipLaunchKernelGGL((few_rows_kernel<AFMT, MT, NT, WAVES, uint16_t>), grid, dim3(WAVES * 64), 0, stream, (int)M,
-                       (int)N, (int)K, a, lda, sa, b, ldb, sb, static_cast<uint16_t*>(c), ldc);
+    hipLaunchKernelGGL((few_rows_kernel<AFMT, MT, NT, WAVES, U, ALDS, uint16_t>), grid, dim3(WAVES * 64), lds, stream,
+                       (int)M, (int)N, (int)K, a, lda, sa, b, ldb, sb, static_cast<uint16_t*>(c), ldc);
 }
 
 // ---------------------------------------------------------------------------
@@ -200,9 +342,6 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kTileThreads = 256;
-[[maybe_unused]] constexpr uint32_t kRange = 0xF0000000u;    // bytes behind a descriptor; valid offsets stay below 2^31
-[[maybe_unused]] constexpr uint32_t kOutside = 0xF8000000u;
-
 template <int BM, int BN, int AFMT>
 struct Tile {
   static constexpr bool A4 = AFMT == kE2M1;
@@ -217,19 +356,6 @@ struct Tile {
   static constexpr int SGRP = 2 * SG;
 };
 
-// Wait for this wave's loads and LDS reads, then meet the others: a bare
-// s_barrier, since __syncthreads() would add a release fence.
-template <int N>
-__device__ __forceinline__ void wait_loads_and_meet() {
-#if defined(__HIP_DEVICE_COMPILE__)
-  static_assert(N >= 0 && N <= 63, "vmcnt");
-  __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
-  asm volatile("s_barrier" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-#endif
-}
-
 // Keeps an address offset out of the optimiser's sight, so that LDS accesses
 // stay "named array + offset" and their waits are per array.
 __device__ __forceinline__ uint32_t opaque(uint32_t x) {
@@ -238,18 +364,6 @@ __device__ __forceinline__ uint32_t opaque(uint32_t x) {
 #endif
   return x;
 }
-
-#if defined(__HIP_DEVICE_COMPILE__)
-typedef __attribute__((address_space(3))) void lds_void;
-template <int BYTES>
-__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t rsrc, uint8_t* to, uint32_t lane_off, uint32_t off) {
-  if constexpr (BYTES == 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)to, 16, lane_off, off, 0, 0);
-  else __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)to, 4, lane_off, off, 0, 0);
-}
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t descriptor(const uint8_t* p) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, (int)kRange, 0x00020000);
-}
-#endif
 
 // SW: scale rows that start on 16-byte boundaries are loaded 16 bytes a lane,
 // others 4.
@@ -632,10 +746,39 @@ void tiles(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const
 template <int AFMT>
 void gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const uint8_t* sa, const uint8_t* b,
           int64_t ldb, const uint8_t* sb, void* c, int64_t ldc, int c_dtype, hipStream_t stream) {
-  if (M <= 16) {
-    few_rows<AFMT, 1, 1, 4>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, stream);
-  } else if (M <= 64 || K <= Tile<256, 256, AFMT>::KB) {
-    few_rows<AFMT, 4, 4, 4>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, stream);
+  // Few rows or tiles.  Up to 16 rows B crosses a CU's load path once however
+  // wide it is.  Beyond, the few-row kernel's time goes with M N K, that of
+  // the tile kernel with K alone while its tiles fit on the CUs; they meet near
+  // M N = 700000 (us, few rows / tiles, E5M2-or-E4M3 x E2M1: 64x8960x1536
+  // 7.7 / 8.5, 96x8960x1536 10.0 / 8.6, 128x3584x3584 13.6 / 18.3, 256x3584x3584
+  // 25.5 / 19.0, 512x1536x8960 42 / 44; E2M1 pairs: 128x3584x3584 7.7 / 11.3,
+  // 256x3584x3584 14.0 / 12.4).  The tile kernel takes two K blocks at least,
+  // the few-row kernel as many scales as fit in LDS.
+  const int chunks = (int)(K / 128);
+  const int64_t n16 = (N + 15) / 16, pairs = ((N + 31) / 32) * ((M + 31) / 32);
+  const bool one_block = K <= Tile<256, 256, AFMT>::KB;
+  const bool few = (M <= 16 || M * N <= 700000) && few_rows_lds<AFMT, 2, 2, 4, false>(0, (int)K) <= kFewRowsLds;
+#define MXFP4_FEW(MT, NT, WAVES, U)                                                                           \
+  (few_rows_lds<AFMT, MT, NT, WAVES, true>((int)(M < 16 * MT ? M : 16 * MT), (int)K) <= kFewRowsLds           \
+       ? few_rows<AFMT, MT, NT, WAVES, U, true>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, stream)     \
+       : few_rows<AFMT, MT, NT, WAVES, U, false>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, stream))
+  if (few || one_block) {
+    if (M <= 16) {
+      // Waves of a workgroup: they cost to start (1 us per 1000), so two where
+      // a run of K is short (1x8960x1536: two 3.5 us, four 4.0; 1x18944x3584:
+      // 8.3 and 8.2).  Where many workgroups would hold much of A each, wider
+      // ones (16x18944x3584, E4M3: 11.2 us against 14.0).
+      const bool wide_a = M * (AFMT == kE2M1 ? K / 2 : K) > 32 * 1024 && n16 >= 512;
+      if (wide_a) MXFP4_FEW(1, 2, 8, 2);
+      else if (chunks <= 16) MXFP4_FEW(1, 1, 2, 4);
+      else MXFP4_FEW(1, 1, 4, 4);
+    } else if (pairs < 128 && !one_block) {
+      // Few workgroups of 32 x 32: smaller ones with K over eight waves
+      // (37x1536x8960: 7.5 us against 8.2-11.4, E4M3 10.9 against 12.6-16.0).
+      MXFP4_FEW(1, 2, 8, 2);
+    } else {
+      MXFP4_FEW(2, 2, 4, 4);
+    }
   } else {
     const bool sw = K % 512 == 0 && (((uintptr_t)sa | (uintptr_t)sb) & 15) == 0;
     float* cf = static_cast<float*>(c);
@@ -647,6 +790,7 @@ void gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const 
       sw ? tiles<AFMT, true>(M, N, K, a, lda, sa, b, ldb, sb, cb, ldc, stream)
          : tiles<AFMT, false>(M, N, K, a, lda, sa, b, ldb, sb, cb, ldc, stream);
   }
+#undef MXFP4_FEW
 }
 
 #define MXFP4_GEMM(FMT)                                                                                      \
