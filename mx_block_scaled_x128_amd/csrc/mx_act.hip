@@ -141,11 +141,12 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(
 }
 
 // ---------------------------------------------------------------------------
-// RMSNorm.  wpr waves share a row (1 up to 4096 columns, 4 up to 16384, then
-// 16), each lane holding NU units of 8 elements, 64 wpr units apart: the row stays
-// in registers between its sum and its output, and the lane's columns of w
-// (and of dw) stay the same for every row, so they are read (and written) once
-// per wave.  Workgroups walk rows with a fixed stride.
+// RMSNorm.  WPR waves share a row (1 up to 4096 columns, 4 up to 16384, then
+// 16), each lane holding NU units of 8 elements, 64 WPR units apart (only the
+// last may lie past the row's end): the row stays in registers between its sum
+// and its output, and the next row is on its way meanwhile.  With WPR = 1 each
+// wave walks rows of its own, else the whole workgroup one row at a time.  w
+// is copied to LDS once per workgroup, dw stays in registers until the end.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
@@ -153,53 +154,92 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 // Sum over the waves of one row, the same order in each of them.
-__device__ __forceinline__ float row_sum(float v, uint32_t wpr, uint32_t wave, float* red) {
+template <int WPR>
+__device__ __forceinline__ float row_sum(float v, uint32_t wave, float* red) {
   v = wave_sum(v);
-  if (wpr > 1) {
+  if constexpr (WPR > 1) {
     __syncthreads();  // red of the row before has been read
     if ((threadIdx.x & 63) == 0) red[wave] = v;
     __syncthreads();
-    const uint32_t first = wave / wpr * wpr;
     v = 0.0f;
-    for (uint32_t i = 0; i < wpr; ++i) v += red[first + i];
+#pragma unroll
+    for (int i = 0; i < WPR; ++i) v += red[i];
   }
   return v;
 }
 
-__device__ __forceinline__ void load_w(const float* __restrict__ w, uint32_t unit, uint32_t upr, float (&f)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] = 0.0f;
-  if (unit < upr) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = w[unit * 8 + j];
-  }
+// The row as read, once more: without this the compiler keeps the converted
+// values of the first pass for the second, twice the registers.
+__device__ __forceinline__ void again(MxRaw<uint16_t>& r) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" : "+v"(r.v));
+#endif
+}
+__device__ __forceinline__ void again(MxRaw<float>&) {}
+__device__ __forceinline__ void again(uint2& c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" : "+v"(c.x), "+v"(c.y));
+#endif
 }
 
-template <typename InT, int FMT, bool CEIL, int NU, int THREADS>
+// w in LDS as two planes, the first and the last four elements of each unit:
+// a wave's reads of a plane are 1 KB without a gap.
+struct WeightLds {
+  nt_f32x4 *lo, *hi;
+  __device__ __forceinline__ WeightLds(nt_f32x4* lds, uint32_t upr) : lo(lds), hi(lds + upr) {}
+  __device__ __forceinline__ void fill(const float* __restrict__ w, uint32_t upr, uint32_t threads) const {
+    for (uint32_t u = threadIdx.x; u < upr; u += threads) {
+      lo[u] = reinterpret_cast<const nt_f32x4*>(w)[2 * u];
+      hi[u] = reinterpret_cast<const nt_f32x4*>(w)[2 * u + 1];
+    }
+    __syncthreads();
+  }
+  __device__ __forceinline__ void get(uint32_t unit, uint32_t upr, float (&f)[8]) const {
+    uint32_t u = unit < upr ? unit : 0;
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" : "+v"(u));  // read again each time: kept across rows, w would cost 8 registers a unit
+#endif
+    const nt_f32x4 a = lo[u], b = hi[u];
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+};
+
+template <typename InT, int FMT, bool CEIL, int NU, int WPR, int THREADS>
 __global__ __launch_bounds__(THREADS) void rmsnorm_forward_kernel(
-    const InT* __restrict__ x, int64_t ldx, int64_t rows, uint32_t upr, uint32_t wpr, const float* __restrict__ w,
+    const InT* __restrict__ x, int64_t ldx, int64_t rows, uint32_t upr, const float* __restrict__ w,
     float eps, uint8_t* __restrict__ y, int64_t ldy, uint8_t* __restrict__ ys, uint8_t* __restrict__ kept, int64_t ldk,
     uint8_t* __restrict__ ks, float* __restrict__ rstd) {
+  extern __shared__ nt_f32x4 lds[];
   __shared__ float red[16];
   const uint32_t lane = threadIdx.x & 63;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t rpw = (THREADS / 64) / wpr;  // rows per workgroup and round
-  const uint32_t unit0 = (wave % wpr) * 64 + lane, ustep = wpr * 64;
+  constexpr uint32_t RPW = WPR == 1 ? THREADS / 64 : 1;  // rows per workgroup and round
+  static_assert(WPR == 1 || THREADS == 64 * WPR, "one row per workgroup");
+  const uint32_t unit0 = (WPR == 1 ? 0 : wave * 64) + lane;
+  constexpr uint32_t USTEP = WPR * 64;
   const uint32_t nb = upr >> 2;
   const float inv_cols = 1.0f / (float)(upr * 8);
-  float wf[NU][8];
-#pragma unroll
-  for (int i = 0; i < NU; ++i) load_w(w, unit0 + i * ustep, upr, wf[i]);
-  for (int64_t r0 = (int64_t)blockIdx.x * rpw; r0 < rows; r0 += (int64_t)gridDim.x * rpw) {
-    const int64_t row = r0 + wave / wpr;
-    const bool ract = row < rows;
-    MxRaw<InT> raw[NU];
+  auto load = [&](int64_t row, MxRaw<InT> (&raw)[NU]) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const uint32_t unit = unit0 + i * ustep;
-      if (ract && unit < upr) mx_load_raw<false>(x + row * ldx + unit * 8, raw[i]);
+      const uint32_t unit = unit0 + i * USTEP;
+      if (i < NU - 1 || unit < upr) mx_load_raw<false>(x + row * ldx + unit * 8, raw[i]);
       else mx_zero_raw(raw[i]);
     }
+  };
+  const WeightLds wl(lds, upr);
+  MxRaw<InT> next[NU];
+  const int64_t step = (int64_t)gridDim.x * RPW;
+  int64_t row = (int64_t)blockIdx.x * RPW + (WPR == 1 ? wave : 0);
+  load(row < rows ? row : rows - 1, next);
+  wl.fill(w, upr, THREADS);
+  for (; row < rows; row += step) {
+    const int64_t ahead = row + step < rows ? row + step : row;  // the last row's own again
+    MxRaw<InT> raw[NU];
+#pragma unroll
+    for (int i = 0; i < NU; ++i) raw[i] = next[i];
+    load(ahead, next);
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
@@ -210,16 +250,19 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_forward_kernel(
       for (int j = 0; j < 8; ++j) part = __builtin_fmaf(f[j], f[j], part);
       ss += part;
     }
-    ss = row_sum(ss, wpr, wave, red);
+    ss = row_sum<WPR>(ss, wave, red);
+#pragma unroll
+    for (int i = 0; i < NU; ++i) again(raw[i]);
     const float r = 1.0f / __builtin_sqrtf(ss * inv_cols + eps);
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const uint32_t unit = unit0 + i * ustep;
-      const bool act = ract && unit < upr;
-      float f[8], v[8];
+      const uint32_t unit = unit0 + i * USTEP;
+      const bool act = i < NU - 1 || unit < upr;
+      float f[8], v[8], wf[8];
+      wl.get(unit, upr, wf);
       mx_unpack(raw[i], f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = f[j] * r * wf[i][j];
+      for (int j = 0; j < 8; ++j) v[j] = f[j] * r * wf[j];
       const MxScale sv = mx_scale<FMT, CEIL>(max_quad(absmax8(v)));
       if (act) {
         mx_store_codes8<FMT>(y + row * ldy + unit * 8, mx_codes8<FMT, CEIL>(v, sv));
@@ -233,127 +276,171 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_forward_kernel(
         }
       }
     }
-    if (kept && ract && unit0 == 0) rstd[row] = r;
+    if (kept && unit0 == 0) rstd[row] = r;
   }
 }
 
+// One row's share of a lane, as read.
+template <typename T, int NU>
+struct BackwardIn {
+  uint2 code[NU];
+  uint32_t b[NU];
+  MxRaw<T> dy[NU];
+  float r;
+};
+
 // part: [gridDim.x][8 upr] partial sums of dw, one row per workgroup.
-template <typename T, int FMT, int NU, int THREADS>
+template <typename T, int FMT, int NU, int WPR, int THREADS>
 __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(
     const uint8_t* __restrict__ kept, int64_t ldk, const uint8_t* __restrict__ ks, const float* __restrict__ rstd,
-    const float* __restrict__ w, const T* __restrict__ dy, int64_t lddy, int64_t rows, uint32_t upr, uint32_t wpr,
+    const float* __restrict__ w, const T* __restrict__ dy, int64_t lddy, int64_t rows, uint32_t upr,
     T* __restrict__ dx, int64_t lddx, float* __restrict__ part) {
+  extern __shared__ nt_f32x4 lds[];
   __shared__ float red[16];
   const uint32_t lane = threadIdx.x & 63;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t rpw = (THREADS / 64) / wpr;
-  const uint32_t unit0 = (wave % wpr) * 64 + lane, ustep = wpr * 64;
+  constexpr uint32_t RPW = WPR == 1 ? THREADS / 64 : 1;
+  static_assert(WPR == 1 || THREADS == 64 * WPR, "one row per workgroup");
+  const uint32_t unit0 = (WPR == 1 ? 0 : wave * 64) + lane;
+  constexpr uint32_t USTEP = WPR * 64;
   const uint32_t nb = upr >> 2;
   const float inv_cols = 1.0f / (float)(upr * 8);
-  float wf[NU][8], dw[NU][8];
-#pragma unroll
-  for (int i = 0; i < NU; ++i) {
-    load_w(w, unit0 + i * ustep, upr, wf[i]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
-  }
-  for (int64_t r0 = (int64_t)blockIdx.x * rpw; r0 < rows; r0 += (int64_t)gridDim.x * rpw) {
-    const int64_t row = r0 + wave / wpr;
-    const bool ract = row < rows;
-    uint2 code[NU];
-    uint32_t b[NU];
-    MxRaw<T> raw[NU];
+  typedef BackwardIn<T, NU> In;
+  auto load = [&](int64_t row, In& in) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const uint32_t unit = unit0 + i * ustep;
-      code[i] = make_uint2(0u, 0u);
-      b[i] = 0;
-      mx_zero_raw(raw[i]);
-      if (ract && unit < upr) {
-        code[i] = mx_load_codes8<FMT>(kept + row * ldk + unit * 8);
-        b[i] = ks[row * nb + (unit >> 2)];
-        mx_load_raw<false>(dy + row * lddy + unit * 8, raw[i]);
+      const uint32_t unit = unit0 + i * USTEP;
+      in.code[i] = make_uint2(0u, 0u);
+      in.b[i] = 0;
+      mx_zero_raw(in.dy[i]);
+      if (i < NU - 1 || unit < upr) {
+        in.code[i] = mx_load_codes8<FMT>(kept + row * ldk + unit * 8);
+        in.b[i] = ks[row * nb + (unit >> 2)];
+        mx_load_raw<false>(dy + row * lddy + unit * 8, in.dy[i]);
       }
     }
-    const float r = ract ? rstd[row] : 0.0f;
+    in.r = rstd[row];
+  };
+  // A row ahead where two rows fit in the registers (16-bit dy).
+  constexpr bool AHEAD = sizeof(T) == 2;
+  const WeightLds wl(lds, upr);
+  float dw[NU][8];
+#pragma unroll
+  for (int i = 0; i < NU; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+  In next;
+  const int64_t step = (int64_t)gridDim.x * RPW;
+  int64_t row = (int64_t)blockIdx.x * RPW + (WPR == 1 ? wave : 0);
+  load(row < rows ? row : rows - 1, next);
+  wl.fill(w, upr, THREADS);
+  for (; row < rows; row += step) {
+    const int64_t ahead = row + step < rows ? row + step : row;  // the last row's own again
+    In in = next;
+    if constexpr (AHEAD) load(ahead, next);
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      float xh[8], d[8];
-      mx_decode8<FMT>(code[i], mx_factor(b[i]), xh);
-      mx_unpack(raw[i], d);
+      float xh[8], d[8], wf[8];
+      wl.get(unit0 + i * USTEP, upr, wf);
+      mx_decode8<FMT>(in.code[i], mx_factor(in.b[i]) * in.r, xh);
+      mx_unpack(in.dy[i], d);
       float p = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float t = d[j] * (xh[j] * r);
+        const float t = d[j] * xh[j];
         dw[i][j] += t;
-        p = __builtin_fmaf(t, wf[i][j], p);
+        p = __builtin_fmaf(t, wf[j], p);
       }
       dot += p;
+      __builtin_amdgcn_sched_barrier(0);  // unit after unit: side by side they need every register
     }
-    const float k = row_sum(dot, wpr, wave, red) * inv_cols;
+    const float k = row_sum<WPR>(dot, wave, red) * inv_cols;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const uint32_t unit = unit0 + i * ustep;
-      float xh[8], d[8];
-      mx_decode8<FMT>(code[i], mx_factor(b[i]), xh);
-      mx_unpack(raw[i], d);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = r * (d[j] * wf[i][j] - xh[j] * r * k);
-      if (ract && unit < upr) mx_store8(dx + row * lddx + unit * 8, d);
+      again(in.code[i]);
+      again(in.dy[i]);
     }
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const uint32_t unit = unit0 + i * USTEP;
+      float xh[8], d[8], wf[8];
+      wl.get(unit, upr, wf);
+      mx_decode8<FMT>(in.code[i], mx_factor(in.b[i]) * in.r, xh);
+      mx_unpack(in.dy[i], d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] = in.r * __builtin_fmaf(xh[j], -k, d[j] * wf[j]);
+      if (i < NU - 1 || unit < upr) mx_store8(dx + row * lddx + unit * 8, d);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (!AHEAD) load(ahead, next);
   }
-  // The workgroup's rows, wave after wave in order, into its row of partials:
-  // the same sum on every run.  A workgroup's own stores are seen by its
-  // later loads after the barrier.
-  float* out = part + (int64_t)blockIdx.x * (upr * 8);
-  for (uint32_t turn = 0; turn < rpw; ++turn) {
-    if (wave / wpr == turn) {
+  // The workgroup's rows, one group of waves after the other, into LDS (w is
+  // not needed any more) and out: the same sum on every run.
+  __syncthreads();
+  for (uint32_t turn = 0; turn < RPW; ++turn) {
+    if (WPR > 1 || wave == turn) {
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
-        const uint32_t unit = unit0 + i * ustep;
+        const uint32_t unit = unit0 + i * USTEP;
         if (unit < upr) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) out[unit * 8 + j] = (turn ? out[unit * 8 + j] : 0.0f) + dw[i][j];
+          const nt_f32x4 a = {dw[i][0], dw[i][1], dw[i][2], dw[i][3]}, b = {dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+          wl.lo[unit] = turn ? wl.lo[unit] + a : a;
+          wl.hi[unit] = turn ? wl.hi[unit] + b : b;
         }
       }
     }
     __syncthreads();
   }
+  nt_f32x4* out = reinterpret_cast<nt_f32x4*>(part + (int64_t)blockIdx.x * (upr * 8));
+  for (uint32_t u = threadIdx.x; u < upr; u += THREADS) {
+    out[2 * u] = wl.lo[u];
+    out[2 * u + 1] = wl.hi[u];
+  }
 }
 
-// dw[c] = sum of part[p][c] in order of p, 4 interleaved runs joined at the end.
-__global__ __launch_bounds__(256) void rmsnorm_dw_kernel(const float* __restrict__ part, uint32_t parts, uint32_t cols,
-                                                         float* __restrict__ dw) {
-  __shared__ float sum[4][64];
+// dw[c] = sum of part[p][c]: 16 waves take every 16th row, in order, then add
+// up in order.
+__global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(const float* __restrict__ part, uint32_t parts, uint32_t cols,
+                                                          float* __restrict__ dw) {
+  __shared__ float sum[16][64];
   const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const uint32_t c = blockIdx.x * 64 + lane;
   float s = 0.0f;
-  if (c < cols)
-    for (uint32_t p = wave; p < parts; p += 4) s += part[(int64_t)p * cols + c];
+  if (c < cols) {
+#pragma unroll 8
+    for (uint32_t p = wave; p < parts; p += 16) s += part[(int64_t)p * cols + c];
+  }
   sum[wave][lane] = s;
   __syncthreads();
-  if (wave == 0 && c < cols) dw[c] = (sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]);
+  if (wave == 0 && c < cols) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t += sum[i][lane];
+    dw[c] = t;
+  }
 }
 
-// Waves per row and units per lane for a row of upr units.
+// Waves per row and units per lane.
 struct NormShape {
-  uint32_t wpr, threads;
-  int nu;
+  int wpr, nu;
 };
 NormShape norm_shape(int64_t cols) {
-  const uint32_t upr = (uint32_t)(cols / kLaneElems);
+  const int upr = (int)(cols / kLaneElems);
   NormShape n;
   n.wpr = upr <= 512 ? 1 : upr <= 2048 ? 4 : 16;
-  n.nu = (int)((upr + 64 * n.wpr - 1) / (64 * n.wpr));
-  n.threads = n.wpr <= 4 ? 256 : 1024;  // 1024 threads leave 128 registers: 4 units per lane at most
+  n.nu = (upr + 64 * n.wpr - 1) / (64 * n.wpr);
   return n;
 }
-uint32_t norm_blocks(int64_t rows, const NormShape& n, int64_t cap) {
-  const int64_t rpw = n.threads / 64 / n.wpr;
+// Workgroups for the rows, at rpw rows a round, at most cap.
+uint32_t norm_blocks(int64_t rows, int64_t rpw, int64_t cap) {
   const int64_t b = (rows + rpw - 1) / rpw;
   return (uint32_t)(b < cap ? b : cap);
 }
+// Waves of a workgroup with WPR = 1.  Backward: 8, all that a compute unit
+// takes at two per SIMD, so that there is one row of partial sums per compute
+// unit.
+constexpr int kForwardWaves = 4, kBackwardWaves = 8;
 
 template <typename InT, int FMT, bool CEIL, bool KEEP>
 void swiglu_forward(const void* x, int64_t rows, int64_t cols, int64_t ldx, uint8_t* h, int64_t ldh, uint8_t* hs,
@@ -394,20 +481,25 @@ void rmsnorm_forward(const void* x, int64_t rows, int64_t cols, int64_t ldx, con
                      int64_t ldy, uint8_t* ys, uint8_t* kept, int64_t ldk, uint8_t* ks, float* rstd,
                      hipStream_t stream) {
   const NormShape n = norm_shape(cols);
-  const uint32_t upr = (uint32_t)(cols / kLaneElems);
-  const dim3 grid(norm_blocks(rows, n, 256 * 4));
-#define MXFP8_NF(NU, THREADS)                                                                                               \
-  case NU:                                                                                                         \
-    hipLaunchKernelGGL((rmsnorm_forward_kernel<InT, FMT, CEIL, NU, THREADS>), grid, dim3(n.threads), 0, stream,             \
-                       static_cast<const InT*>(x), ldx, rows, upr, n.wpr, w, eps, y, ldy, ys, kept, ldk, ks, rstd); \
+#define MXFP8_NF(WPR, NU, WAVES)                                                                                    \
+  case NU:                                                                                                          \
+    hipLaunchKernelGGL((rmsnorm_forward_kernel<InT, FMT, CEIL, NU, WPR, 64 * WAVES>),                               \
+                       dim3(norm_blocks(rows, WAVES / WPR, 1024)), dim3(64 * WAVES), (uint32_t)cols * 4, stream,    \
+                       static_cast<const InT*>(x), ldx, rows, (uint32_t)(cols / kLaneElems), w, eps, y, ldy, ys,    \
+                       kept, ldk, ks, rstd);                                                                        \
     break;
-  if (n.threads > 256) {
-    switch (n.nu) { MXFP8_NF(3, 1024) MXFP8_NF(4, 1024) }
-  } else {
+  if (n.wpr == 1) {
     switch (n.nu) {
-      MXFP8_NF(1, 256) MXFP8_NF(2, 256) MXFP8_NF(3, 256) MXFP8_NF(4, 256)
-      MXFP8_NF(5, 256) MXFP8_NF(6, 256) MXFP8_NF(7, 256) MXFP8_NF(8, 256)
+      MXFP8_NF(1, 1, kForwardWaves) MXFP8_NF(1, 2, kForwardWaves) MXFP8_NF(1, 3, kForwardWaves)
+      MXFP8_NF(1, 4, kForwardWaves) MXFP8_NF(1, 5, kForwardWaves) MXFP8_NF(1, 6, kForwardWaves)
+      MXFP8_NF(1, 7, kForwardWaves) MXFP8_NF(1, 8, kForwardWaves)
     }
+  } else if (n.wpr == 4) {
+    switch (n.nu) {
+      MXFP8_NF(4, 3, 4) MXFP8_NF(4, 4, 4) MXFP8_NF(4, 5, 4) MXFP8_NF(4, 6, 4) MXFP8_NF(4, 7, 4) MXFP8_NF(4, 8, 4)
+    }
+  } else {
+    switch (n.nu) { MXFP8_NF(16, 3, 16) MXFP8_NF(16, 4, 16) }
   }
 #undef MXFP8_NF
 }
@@ -417,20 +509,25 @@ void rmsnorm_backward(const uint8_t* kept, int64_t ldk, const uint8_t* ks, const
                       const void* dy, int64_t lddy, int64_t rows, int64_t cols, void* dx, int64_t lddx, float* part,
                       int64_t parts, hipStream_t stream) {
   const NormShape n = norm_shape(cols);
-  const uint32_t upr = (uint32_t)(cols / kLaneElems);
-  const dim3 grid((uint32_t)parts);
-#define MXFP8_NB(NU, THREADS)                                                                                              \
-  case NU:                                                                                                        \
-    hipLaunchKernelGGL((rmsnorm_backward_kernel<T, FMT, NU, THREADS>), grid, dim3(n.threads), 0, stream, kept, ldk, ks, rstd, \
-                       w, static_cast<const T*>(dy), lddy, rows, upr, n.wpr, static_cast<T*>(dx), lddx, part);    \
+#define MXFP8_NB(WPR, NU, WAVES)                                                                                   \
+  case NU:                                                                                                         \
+    hipLaunchKernelGGL((rmsnorm_backward_kernel<T, FMT, NU, WPR, 64 * WAVES>), dim3((uint32_t)parts),              \
+                       dim3(64 * WAVES), (uint32_t)cols * 4, stream, kept, ldk, ks, rstd, w,                       \
+                       static_cast<const T*>(dy), lddy, rows, (uint32_t)(cols / kLaneElems), static_cast<T*>(dx),  \
+                       lddx, part);                                                                                \
     break;
-  if (n.threads > 256) {
-    switch (n.nu) { MXFP8_NB(3, 1024) MXFP8_NB(4, 1024) }
-  } else {
+  if (n.wpr == 1) {
     switch (n.nu) {
-      MXFP8_NB(1, 256) MXFP8_NB(2, 256) MXFP8_NB(3, 256) MXFP8_NB(4, 256)
-      MXFP8_NB(5, 256) MXFP8_NB(6, 256) MXFP8_NB(7, 256) MXFP8_NB(8, 256)
+      MXFP8_NB(1, 1, kBackwardWaves) MXFP8_NB(1, 2, kBackwardWaves) MXFP8_NB(1, 3, kBackwardWaves)
+      MXFP8_NB(1, 4, kBackwardWaves) MXFP8_NB(1, 5, kBackwardWaves) MXFP8_NB(1, 6, kBackwardWaves)
+      MXFP8_NB(1, 7, kBackwardWaves) MXFP8_NB(1, 8, kBackwardWaves)
     }
+  } else if (n.wpr == 4) {
+    switch (n.nu) {
+      MXFP8_NB(4, 3, 4) MXFP8_NB(4, 4, 4) MXFP8_NB(4, 5, 4) MXFP8_NB(4, 6, 4) MXFP8_NB(4, 7, 4) MXFP8_NB(4, 8, 4)
+    }
+  } else {
+    switch (n.nu) { MXFP8_NB(16, 3, 16) MXFP8_NB(16, 4, 16) }
   }
 #undef MXFP8_NB
 }
@@ -474,7 +571,7 @@ void launch_mx_rmsnorm_forward(const void* x, int dtype, int64_t rows, int64_t c
 
 int64_t rmsnorm_backward_parts(int64_t rows, int64_t cols) {
   const NormShape n = norm_shape(cols);
-  return norm_blocks(rows, n, 256 * 2);
+  return norm_blocks(rows, n.wpr == 1 ? kBackwardWaves : 1, n.wpr == 4 ? 512 : 256);
 }
 
 void launch_mx_rmsnorm_backward(const uint8_t* kept, int64_t ldk, const uint8_t* ks, const float* rstd, int fmt,
@@ -488,7 +585,7 @@ void launch_mx_rmsnorm_backward(const uint8_t* kept, int64_t ldk, const uint8_t*
   else fmt == 0 ? MXFP8_B(uint16_t, 0) : MXFP8_B(uint16_t, 1);
 #undef MXFP8_B
   }
-  hipLaunchKernelGGL(rmsnorm_dw_kernel, dim3((uint32_t)((cols + 63) / 64)), dim3(256), 0, stream, workspace,
+  hipLaunchKernelGGL(rmsnorm_dw_kernel, dim3((uint32_t)((cols + 63) / 64)), dim3(1024), 0, stream, workspace,
                      (uint32_t)parts, (uint32_t)cols, dw);
 }
 
