@@ -220,13 +220,17 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_forward_kernel(
   constexpr uint32_t USTEP = WPR * 64;
   const uint32_t nb = upr >> 2;
   const float inv_cols = 1.0f / (float)(upr * 8);
+#if defined(__HIP_DEVICE_COMPILE__)
+  // Lane offsets: one per tensor; the last unit's own, outside past the row's end.
+  const bool last_in = unit0 + (NU - 1) * USTEP < upr;
+  const uint32_t cx = unit0 * 8 * sizeof(InT), cq = unit0 * 8, cs = (lane & 3) == 0 ? unit0 >> 2 : kNowhere;
+  auto at = [&](int i, uint32_t off) __attribute__((always_inline)) {
+    return i < NU - 1 || last_in ? off : kNowhere;
+  };
   auto load = [&](int64_t row, MxRaw<InT> (&raw)[NU]) __attribute__((always_inline)) {
+    const mx_rsrc rx = mx_run(x + row * ldx);
 #pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      const uint32_t unit = unit0 + i * USTEP;
-      if (i < NU - 1 || unit < upr) mx_load_raw<false>(x + row * ldx + unit * 8, raw[i]);
-      else mx_zero_raw(raw[i]);
-    }
+    for (int i = 0; i < NU; ++i) mx_get(rx, at(i, cx), i * USTEP * 8 * sizeof(InT), raw[i]);
   };
   const WeightLds wl(lds, upr);
   MxRaw<InT> next[NU];
@@ -254,30 +258,27 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_forward_kernel(
 #pragma unroll
     for (int i = 0; i < NU; ++i) again(raw[i]);
     const float r = 1.0f / __builtin_sqrtf(ss * inv_cols + eps);
+    const mx_rsrc ry = mx_run(y + row * ldy), rys = mx_run(ys + row * nb);
+    const mx_rsrc rk = mx_run(kept + row * ldk), rks = mx_run(ks + row * nb);
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const uint32_t unit = unit0 + i * USTEP;
-      const bool act = i < NU - 1 || unit < upr;
       float f[8], v[8], wf[8];
-      wl.get(unit, upr, wf);
+      wl.get(unit0 + i * USTEP, upr, wf);
       mx_unpack(raw[i], f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = f[j] * r * wf[j];
       const MxScale sv = mx_scale<FMT, CEIL>(max_quad(absmax8(v)));
-      if (act) {
-        mx_store_codes8<FMT>(y + row * ldy + unit * 8, mx_codes8<FMT, CEIL>(v, sv));
-        if ((lane & 3) == 0) ys[row * nb + (unit >> 2)] = (uint8_t)sv.byte;
-      }
+      mx_put_codes(ry, at(i, cq), i * USTEP * 8, mx_codes8<FMT, CEIL>(v, sv));
+      mx_put_byte(rys, at(i, cs), i * USTEP / 4, sv.byte);
       if (kept) {
         const MxScale sk = mx_scale<FMT, CEIL>(max_quad(absmax8(f)));
-        if (act) {
-          mx_store_codes8<FMT>(kept + row * ldk + unit * 8, mx_codes8<FMT, CEIL>(f, sk));
-          if ((lane & 3) == 0) ks[row * nb + (unit >> 2)] = (uint8_t)sk.byte;
-        }
+        mx_put_codes(rk, at(i, cq), i * USTEP * 8, mx_codes8<FMT, CEIL>(f, sk));
+        mx_put_byte(rks, at(i, cs), i * USTEP / 4, sk.byte);
       }
     }
     if (kept && unit0 == 0) rstd[row] = r;
   }
+#endif
 }
 
 // One row's share of a lane, as read.
@@ -305,19 +306,21 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(
   constexpr uint32_t USTEP = WPR * 64;
   const uint32_t nb = upr >> 2;
   const float inv_cols = 1.0f / (float)(upr * 8);
+#if defined(__HIP_DEVICE_COMPILE__)
   typedef BackwardIn<T, NU> In;
+  // Lane offsets: one per tensor; the last unit's own, outside past the row's end.
+  const bool last_in = unit0 + (NU - 1) * USTEP < upr;
+  const uint32_t ck = unit0 * 8, cd = unit0 * 8 * sizeof(T), cs = unit0 >> 2;
+  auto at = [&](int i, uint32_t off) __attribute__((always_inline)) {
+    return i < NU - 1 || last_in ? off : kNowhere;
+  };
   auto load = [&](int64_t row, In& in) __attribute__((always_inline)) {
+    const mx_rsrc rk = mx_run(kept + row * ldk), rs = mx_run(ks + row * nb), rd = mx_run(dy + row * lddy);
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const uint32_t unit = unit0 + i * USTEP;
-      in.code[i] = make_uint2(0u, 0u);
-      in.b[i] = 0;
-      mx_zero_raw(in.dy[i]);
-      if (i < NU - 1 || unit < upr) {
-        in.code[i] = mx_load_codes8<FMT>(kept + row * ldk + unit * 8);
-        in.b[i] = ks[row * nb + (unit >> 2)];
-        mx_load_raw<false>(dy + row * lddy + unit * 8, in.dy[i]);
-      }
+      in.code[i] = mx_get_codes(rk, at(i, ck), i * USTEP * 8);
+      in.b[i] = mx_get_byte(rs, at(i, cs), i * USTEP / 4);
+      mx_get(rd, at(i, cd), i * USTEP * 8 * sizeof(T), in.dy[i]);
     }
     in.r = rstd[row];
   };
@@ -356,6 +359,7 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(
       __builtin_amdgcn_sched_barrier(0);  // unit after unit: side by side they need every register
     }
     const float k = row_sum<WPR>(dot, wave, red) * inv_cols;
+    const mx_rsrc rx = mx_run(dx + row * lddx);
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
       again(in.code[i]);
@@ -363,14 +367,13 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(
     }
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const uint32_t unit = unit0 + i * USTEP;
       float xh[8], d[8], wf[8];
-      wl.get(unit, upr, wf);
+      wl.get(unit0 + i * USTEP, upr, wf);
       mx_decode8<FMT>(in.code[i], mx_factor(in.b[i]) * in.r, xh);
       mx_unpack(in.dy[i], d);
 #pragma unroll
       for (int j = 0; j < 8; ++j) d[j] = in.r * __builtin_fmaf(xh[j], -k, d[j] * wf[j]);
-      if (i < NU - 1 || unit < upr) mx_store8(dx + row * lddx + unit * 8, d);
+      mx_put8(rx, at(i, cd), i * USTEP * 8 * sizeof(T), d, T());
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (!AHEAD) load(ahead, next);
@@ -397,6 +400,7 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(
     out[2 * u] = wl.lo[u];
     out[2 * u + 1] = wl.hi[u];
   }
+#endif
 }
 
 // dw[c] = sum of part[p][c]: 16 waves take every 16th row, in order, then add

@@ -205,4 +205,57 @@ __device__ __forceinline__ void mx_unpack(const MxRaw<float>& r, float (&f)[8]) 
   f[4] = r.b.x; f[5] = r.b.y; f[6] = r.b.z; f[7] = r.b.w;
 }
 
+// A row (or any run below 2 GiB) behind a buffer descriptor: accesses are a
+// lane's 32-bit offset plus a uniform one, so the offsets of a lane's units
+// cost one register per tensor and not two per unit.  A lane offset of
+// kNowhere is outside the descriptor's range: it reads zeros and writes
+// nothing.
+#if defined(__HIP_DEVICE_COMPILE__)
+typedef __amdgpu_buffer_rsrc_t mx_rsrc;
+constexpr uint32_t kNowhere = 0xF8000000u;
+__device__ __forceinline__ mx_rsrc mx_run(const void* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)0xF0000000u, 0x00020000);
+}
+__device__ __forceinline__ void mx_get(mx_rsrc r, uint32_t lane, uint32_t at, MxRaw<uint16_t>& v) {
+  v.v = __builtin_bit_cast(nt_u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane, at, 0));
+}
+__device__ __forceinline__ void mx_get(mx_rsrc r, uint32_t lane, uint32_t at, MxRaw<float>& v) {
+  v.a = __builtin_bit_cast(nt_f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane, at, 0));
+  v.b = __builtin_bit_cast(nt_f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane, at + 16, 0));
+}
+__device__ __forceinline__ uint2 mx_get_codes(mx_rsrc r, uint32_t lane, uint32_t at) {
+  const auto v = __builtin_amdgcn_raw_buffer_load_b64(r, lane, at, 0);
+  return make_uint2(v[0], v[1]);
+}
+__device__ __forceinline__ uint32_t mx_get_byte(mx_rsrc r, uint32_t lane, uint32_t at) {
+  return (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, lane, at, 0);
+}
+typedef unsigned int mx_u4 __attribute__((vector_size(16)));
+typedef unsigned int mx_u2 __attribute__((vector_size(8)));
+// 16-byte stores take the whole offset in the lane's register.  A store of
+// more than 8 bytes still reads its data registers when the next instruction
+// may write them; the compiler waits for that with a constant uniform offset
+// but not with one in a register, and the first of the four words was then
+// wrong now and then (seen on fp32 rows, 16 lanes at a time).
+__device__ __forceinline__ void mx_put16(mx_rsrc r, uint32_t off, mx_u4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 0);
+}
+__device__ __forceinline__ void mx_put8(mx_rsrc r, uint32_t lane, uint32_t at, const float (&f)[8], uint16_t) {
+  mx_put16(r, lane + at, mx_u4{mx_bf16x2(f[0], f[1]), mx_bf16x2(f[2], f[3]), mx_bf16x2(f[4], f[5]),
+                               mx_bf16x2(f[6], f[7])});
+}
+__device__ __forceinline__ void mx_put8(mx_rsrc r, uint32_t lane, uint32_t at, const float (&f)[8], float) {
+  mx_put16(r, lane + at,
+           mx_u4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])});
+  mx_put16(r, lane + at + 16,
+           mx_u4{__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])});
+}
+__device__ __forceinline__ void mx_put_codes(mx_rsrc r, uint32_t lane, uint32_t at, uint2 v) {
+  __builtin_amdgcn_raw_buffer_store_b64(mx_u2{v.x, v.y}, r, lane, at, 0);
+}
+__device__ __forceinline__ void mx_put_byte(mx_rsrc r, uint32_t lane, uint32_t at, uint32_t v) {
+  __builtin_amdgcn_raw_buffer_store_b8((uint8_t)v, r, lane, at, 0);
+}
+#endif
+
 }  // namespace mxfp8
