@@ -22,7 +22,13 @@ namespace mxfp8 {
 namespace mx_act_detail {
 
 constexpr int kThreads = 256;
-constexpr uint32_t kMaxBlocks = 256 * 8;
+// SwiGLU's workgroups at most, grid-stride beyond, and units per lane.  With
+// 8192x18944 bf16 (us, 8 / 64 / 256 / 1024 workgroups per compute unit,
+// stores past the caches): forward two units a lane 178 / 163 / 166 / 174,
+// one unit 169 at 256; backward two units 232 / 209 / 199 / 199, one unit 194
+// at 256.  With ordinary stores of what is kept and of dx: 214 and 221 at 64.
+constexpr uint32_t kForwardBlocks = 256 * 64, kBackwardBlocks = 256 * 256;
+constexpr int kForwardUnits = 2;
 
 // sigma(g).  exp2 and rcp are the hardware's (1 ulp each); the argument's own
 // rounding puts a relative error of |g| * 2^-24 on top.  2^(-g log2 e) = inf
@@ -72,8 +78,8 @@ __global__ __launch_bounds__(kThreads) void swiglu_forward_kernel(
         const MxScale su = mx_scale<FMT, CEIL>(max_quad(absmax8(u)));
         if (unit < upr) {
           uint8_t* kr = kept + row * ldk;
-          mx_store_codes8<FMT>(kr + unit * 8, mx_codes8<FMT, CEIL>(g, sg));
-          mx_store_codes8<FMT>(kr + cols + unit * 8, mx_codes8<FMT, CEIL>(u, su));
+          mx_keep_codes8<NT>(kr + unit * 8, mx_codes8<FMT, CEIL>(g, sg));
+          mx_keep_codes8<NT>(kr + cols + unit * 8, mx_codes8<FMT, CEIL>(u, su));
           if ((lane & 3) == 0) {
             ks[row * (2 * nb) + (unit >> 2)] = (uint8_t)sg.byte;
             ks[row * (2 * nb) + nb + (unit >> 2)] = (uint8_t)su.byte;
@@ -88,7 +94,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_forward_kernel(
   }
 }
 
-template <typename T, int FMT, int U, bool NT>
+template <typename T, int FMT, bool NT>
 __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(
     const uint8_t* __restrict__ kept, int64_t ldk, const uint8_t* __restrict__ ks, const T* __restrict__ dh,
     int64_t lddh, int64_t rows, uint32_t upr, T* __restrict__ dx, int64_t lddx) {
@@ -96,47 +102,30 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(
   const uint32_t wave = blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t nwaves = gridDim.x * (kThreads / 64);
   const uint32_t cols = upr * 8, nb = upr >> 2;
-  const uint32_t ipr = (upr + 64 * U - 1) / (64 * U);
+  const uint32_t ipr = (upr + 63) / 64;
   const int64_t items = rows * ipr;
   for (int64_t it = wave; it < items; it += nwaves) {
     const int64_t row = it <= (int64_t)UINT32_MAX ? (int64_t)((uint32_t)it / ipr) : it / ipr;
-    const uint32_t unit0 = (uint32_t)(it - row * ipr) * (64 * U) + lane;
-    uint2 wg[U], wu[U];
-    uint32_t bg[U], bu[U];
-    MxRaw<T> rd[U];
+    const uint32_t unit = (uint32_t)(it - row * ipr) * 64 + lane;
+    if (unit >= upr) continue;
+    const uint2 wg = mx_load_codes8<FMT>(kept + row * ldk + unit * 8);
+    const uint2 wu = mx_load_codes8<FMT>(kept + row * ldk + cols + unit * 8);
+    const uint32_t bg = ks[row * (2 * nb) + (unit >> 2)], bu = ks[row * (2 * nb) + nb + (unit >> 2)];
+    MxRaw<T> rd;
+    mx_load_raw<NT>(dh + row * lddh + unit * 8, rd);
+    float g[8], u[8], d[8], dg[8], du[8];
+    mx_decode8<FMT>(wg, mx_factor(bg), g);
+    mx_decode8<FMT>(wu, mx_factor(bu), u);
+    mx_unpack(rd, d);
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const uint32_t unit = unit0 + i * 64;
-      wg[i] = wu[i] = make_uint2(0u, 0u);
-      bg[i] = bu[i] = 0;
-      mx_zero_raw(rd[i]);
-      if (unit < upr) {
-        wg[i] = mx_load_codes8<FMT>(kept + row * ldk + unit * 8);
-        wu[i] = mx_load_codes8<FMT>(kept + row * ldk + cols + unit * 8);
-        bg[i] = ks[row * (2 * nb) + (unit >> 2)];
-        bu[i] = ks[row * (2 * nb) + nb + (unit >> 2)];
-        mx_load_raw<NT>(dh + row * lddh + unit * 8, rd[i]);
-      }
+    for (int j = 0; j < 8; ++j) {
+      const float s = sigmoid(g[j]);
+      const float a = d[j] * s;
+      du[j] = a * g[j];
+      dg[j] = a * u[j] * __builtin_fmaf(g[j], 1.0f - s, 1.0f);
     }
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const uint32_t unit = unit0 + i * 64;
-      float g[8], u[8], d[8], dg[8], du[8];
-      mx_decode8<FMT>(wg[i], mx_factor(bg[i]), g);
-      mx_decode8<FMT>(wu[i], mx_factor(bu[i]), u);
-      mx_unpack(rd[i], d);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float s = sigmoid(g[j]);
-        const float a = d[j] * s;
-        du[j] = a * g[j];
-        dg[j] = a * u[j] * __builtin_fmaf(g[j], 1.0f - s, 1.0f);
-      }
-      if (unit < upr) {
-        mx_store8(dx + row * lddx + unit * 8, dg);
-        mx_store8(dx + row * lddx + cols + unit * 8, du);
-      }
-    }
+    mx_store8<NT>(dx + row * lddx + unit * 8, dg);
+    mx_store8<NT>(dx + row * lddx + cols + unit * 8, du);
   }
 }
 
@@ -450,16 +439,16 @@ template <typename InT, int FMT, bool CEIL, bool KEEP>
 void swiglu_forward(const void* x, int64_t rows, int64_t cols, int64_t ldx, uint8_t* h, int64_t ldh, uint8_t* hs,
                     uint8_t* kept, int64_t ldk, uint8_t* ks, hipStream_t stream) {
   const uint32_t upr = (uint32_t)(cols / kLaneElems);
-  const bool deep = rows * upr >= (int64_t)kThreads * 2 * 4 * device_cus();
-  const int u = deep ? 2 : 1;
+  const bool deep = rows * upr >= (int64_t)kThreads * kForwardUnits * 4 * device_cus();
+  const int u = deep ? kForwardUnits : 1;
   const int64_t items = rows * ((upr + 64 * u - 1) / (64 * u)), need = (items + 3) / 4;
-  const uint32_t blocks = (uint32_t)(need < kMaxBlocks ? need : kMaxBlocks);
+  const uint32_t blocks = (uint32_t)(need < kForwardBlocks ? need : kForwardBlocks);
 #define MXFP8_SF(U, NT)                                                                                          \
   hipLaunchKernelGGL((swiglu_forward_kernel<InT, FMT, CEIL, KEEP, U, NT>), dim3(blocks), dim3(kThreads), 0, stream, \
                      static_cast<const InT*>(x), ldx, rows, upr, h, ldh, hs, kept, ldk, ks)
   if (!deep) MXFP8_SF(1, false);
-  else if (stream_loads(rows, 2 * cols, sizeof(InT))) MXFP8_SF(2, true);
-  else MXFP8_SF(2, false);
+  else if (stream_loads(rows, 2 * cols, sizeof(InT))) MXFP8_SF(kForwardUnits, true);
+  else MXFP8_SF(kForwardUnits, false);
 #undef MXFP8_SF
 }
 
@@ -467,16 +456,13 @@ template <typename T, int FMT>
 void swiglu_backward(const uint8_t* kept, int64_t ldk, const uint8_t* ks, const void* dh, int64_t lddh, int64_t rows,
                      int64_t cols, void* dx, int64_t lddx, hipStream_t stream) {
   const uint32_t upr = (uint32_t)(cols / kLaneElems);
-  const bool deep = rows * upr >= (int64_t)kThreads * 2 * 4 * device_cus();
-  const int u = deep ? 2 : 1;
-  const int64_t items = rows * ((upr + 64 * u - 1) / (64 * u)), need = (items + 3) / 4;
-  const uint32_t blocks = (uint32_t)(need < kMaxBlocks ? need : kMaxBlocks);
-#define MXFP8_SB(U, NT)                                                                                             \
-  hipLaunchKernelGGL((swiglu_backward_kernel<T, FMT, U, NT>), dim3(blocks), dim3(kThreads), 0, stream, kept, ldk, ks, \
+  const int64_t items = rows * ((upr + 63) / 64), need = (items + 3) / 4;
+  const uint32_t blocks = (uint32_t)(need < kBackwardBlocks ? need : kBackwardBlocks);
+#define MXFP8_SB(NT)                                                                                              \
+  hipLaunchKernelGGL((swiglu_backward_kernel<T, FMT, NT>), dim3(blocks), dim3(kThreads), 0, stream, kept, ldk, ks, \
                      static_cast<const T*>(dh), lddh, rows, upr, static_cast<T*>(dx), lddx)
-  if (!deep) MXFP8_SB(1, false);
-  else if (stream_loads(rows, cols, sizeof(T))) MXFP8_SB(2, true);
-  else MXFP8_SB(2, false);
+  if (stream_loads(rows, cols, sizeof(T))) MXFP8_SB(true);
+  else MXFP8_SB(false);
 #undef MXFP8_SB
 }
 

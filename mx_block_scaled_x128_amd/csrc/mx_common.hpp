@@ -165,19 +165,34 @@ __device__ __forceinline__ void mx_store_codes8(uint8_t* p, uint2 v) {
   if constexpr (FMT == kE2M1) *reinterpret_cast<uint32_t*>(p) = v.x;
   else store_codes(p, v);
 }
+// NT: past the caches, for codes that nobody reads soon (what is kept for a
+// backward pass).
+template <bool NT>
+__device__ __forceinline__ void mx_keep_codes8(uint8_t* p, uint2 v) {
+  if constexpr (NT) __builtin_nontemporal_store(nt_u32x2{v.x, v.y}, reinterpret_cast<nt_u32x2*>(p));
+  else store_codes(p, v);
+}
 
 // Eight fp32 values out, as fp32 or rounded (nearest even) to bf16.
 typedef __bf16 mx_bf2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t mx_bf16x2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((mx_f2{lo, hi}), mx_bf2));
 }
-__device__ __forceinline__ void mx_store8(float* p, const float (&f)[8]) {
-  *reinterpret_cast<nt_f32x4*>(p) = nt_f32x4{f[0], f[1], f[2], f[3]};
-  *reinterpret_cast<nt_f32x4*>(p + 4) = nt_f32x4{f[4], f[5], f[6], f[7]};
+// NT: past the caches, for outputs larger than they are.
+template <bool NT, typename V>
+__device__ __forceinline__ void mx_store16(void* p, V v) {
+  if constexpr (NT) __builtin_nontemporal_store(v, static_cast<V*>(p));
+  else *static_cast<V*>(p) = v;
 }
+template <bool NT>
+__device__ __forceinline__ void mx_store8(float* p, const float (&f)[8]) {
+  mx_store16<NT>(p, nt_f32x4{f[0], f[1], f[2], f[3]});
+  mx_store16<NT>(p + 4, nt_f32x4{f[4], f[5], f[6], f[7]});
+}
+template <bool NT>
 __device__ __forceinline__ void mx_store8(uint16_t* p, const float (&f)[8]) {
-  *reinterpret_cast<nt_u32x4*>(p) = nt_u32x4{mx_bf16x2(f[0], f[1]), mx_bf16x2(f[2], f[3]), mx_bf16x2(f[4], f[5]),
-                                             mx_bf16x2(f[6], f[7])};
+  mx_store16<NT>(p, nt_u32x4{mx_bf16x2(f[0], f[1]), mx_bf16x2(f[2], f[3]), mx_bf16x2(f[4], f[5]),
+                             mx_bf16x2(f[6], f[7])});
 }
 
 // Raw words of eight input elements, converted where they are used.

@@ -17,7 +17,13 @@ namespace mxfp8 {
 namespace mx_quant_detail {
 
 constexpr int kThreads = 256;
-constexpr uint32_t kMaxBlocks = 256 * 8;  // 8 workgroups per compute unit, grid-stride beyond that
+// Workgroups at most, grid-stride beyond.  The quantizer keeps 8 per compute
+// unit (18944x3584 bf16: 30.2 us, 64 per unit 32.3); dequantizing to 16 bits
+// writes twice what it reads and is faster with 64 and two units a lane
+// (8192x18944: 74.5 us; 8 per unit and four units 81.9; 86.4 with ordinary
+// stores).
+constexpr uint32_t kQuantBlocks = 256 * 8, kDequantBlocks = 256 * 64;
+constexpr int kQuantUnits = 4, kDequantUnits = 2;
 
 // The row-wise kernels walk units of 8 elements in row-major order; a wave
 // takes U * 64 consecutive units at a time, so only one division per wave and
@@ -80,7 +86,7 @@ __global__ __launch_bounds__(kThreads) void mxfp4_rows_kernel(const InT* __restr
   }
 }
 
-template <int FMT, typename OutT, int U>
+template <int FMT, typename OutT, int U, bool NT>
 __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const uint8_t* __restrict__ q, int64_t ldq,
                                                                  const uint8_t* __restrict__ s, uint32_t upr,
                                                                  int64_t total, OutT* __restrict__ y, int64_t ldy) {
@@ -108,49 +114,64 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const uint8_t* 
     for (int u = 0; u < U; ++u) {
       float f[8];
       mx_decode8<FMT>(w[u], mx_factor(b[u]), f);
-      if (act[u]) mx_store8(y + p[u].row * ldy + p[u].unit * 8, f);
+      if (act[u]) mx_store8<NT>(y + p[u].row * ldy + p[u].unit * 8, f);
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// 32-token blocks down the columns, transposed.  One workgroup of 8 waves per
-// 128 tokens x 128 channels: a thread holds 4 tokens x 8 channels, the 8 lanes
-// of a wave that share a channel chunk hold 32 tokens of it, which are one MX
-// block: its maximum is three DPP steps and no barrier.  Codes go through an
-// LDS tile (rows of 128 codes, padded) and leave as whole rows of the output;
-// the tile's 128 x 4 scale bytes leave as one dword per channel.
+// 32-token blocks down the columns, transposed.  One workgroup per 128 tokens
+// x 128 channels.  A thread holds 4 tokens x CH channels (16 bytes of a row,
+// or 32 of fp32), so that each load instruction takes 8 whole 128-byte (or
+// 256-byte) row segments; the 8 lanes of a wave that share a channel chunk
+// hold 32 tokens of it, which are one MX block: its maximum is three DPP steps
+// and no barrier.  Codes go through an LDS tile (rows of 128 codes, padded)
+// and leave as whole rows of the output; the tile's 128 x 4 scale bytes leave
+// as one dword per channel.
+// Tiles are taken token by token, each XCD (workgroups go round them) a
+// contiguous run: the 4-byte pieces that neighbouring tiles write of one line
+// of scales, and read of one line of a source's, then meet in one L2
+// (channel by channel across the XCDs, 8 codes to a load: 4099x8960 codes 21.6
+// us, 8960x1536 fp32 into E2M1 13.1; this way @REQ@ and @F32@).
 // SRC: MXFP8_F32 / MXFP8_BF16 elements, or 2 + FP8 format for codes with
 // scales per 32 columns.
 // ---------------------------------------------------------------------------
-constexpr int kTThreads = 512;
-
-template <int SRC> struct Source;
+template <int SRC> struct Source {  // codes
+  typedef uint8_t T;
+  static constexpr int CH = 16;
+};
 template <> struct Source<0> {
   typedef float T;
+  static constexpr int CH = 8;
 };
 template <> struct Source<1> {
   typedef uint16_t T;
+  static constexpr int CH = 8;
 };
+constexpr int kTile = 128;
+template <int SRC> constexpr int kTThreads = kTile / 4 * (kTile / Source<SRC>::CH);
 
 template <int SRC, int FMT, bool CEIL, bool NT>
-__global__ __launch_bounds__(kTThreads) void mx_transpose_kernel(
+__global__ __launch_bounds__(kTThreads<SRC>) void mx_transpose_kernel(
     const void* __restrict__ x, int64_t ldx, const uint8_t* __restrict__ s, uint32_t rows, uint32_t cols,
     uint8_t* __restrict__ qt, int64_t ldqt, uint32_t rows_out, uint8_t* __restrict__ st) {
-  constexpr int RB = 128 * MxFmt<FMT>::code_bits / 8;  // bytes of 128 codes
+  constexpr int THREADS = kTThreads<SRC>, CH = Source<SRC>::CH;
+  constexpr int RB = kTile * MxFmt<FMT>::code_bits / 8;  // bytes of 128 codes
   constexpr int PITCH = RB + 8;
-  __shared__ __attribute__((aligned(16))) uint8_t tile[128 * PITCH];
-  __shared__ __attribute__((aligned(4))) uint8_t stile[128 * 4];
+  __shared__ __attribute__((aligned(16))) uint8_t tile[kTile * PITCH];
+  __shared__ __attribute__((aligned(4))) uint8_t stile[kTile * 4];
   const uint32_t tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const uint32_t tr = (lane & 7) + 8 * (w & 3);    // token chunk: tokens tr*4 .. tr*4+3
-  const uint32_t tc = (lane >> 3) + 8 * (w >> 2);  // channel chunk: channels tc*8 .. tc*8+7
-  const uint32_t gx = (cols + 127) >> 7;
-  const uint32_t by = blockIdx.x / gx, bx = blockIdx.x - by * gx;
-  const uint32_t c0 = bx * 128, t0 = by * 128;
-  const bool cact = c0 + tc * 8 < cols;
-  float f[4][8];
+  const uint32_t tc = (lane >> 3) + 8 * (w >> 2);  // channel chunk: channels tc*CH .. tc*CH+CH-1
+  const uint32_t gx = (cols + 127) >> 7, gy = (rows_out + 127) >> 7;
+  const uint32_t t = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+  if (t >= gx * gy) return;  // the grid is a multiple of 8
+  const uint32_t bx = t / gy, by = t - bx * gy;
+  const uint32_t c0 = bx * kTile, t0 = by * kTile;
+  const bool cact = c0 + tc * CH < cols;
+  float f[4][CH];
   if constexpr (SRC < 2) {
-    typedef typename Source<SRC < 2 ? SRC : 0>::T T;
+    typedef typename Source<SRC>::T T;
     MxRaw<T> raw[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -161,46 +182,57 @@ __global__ __launch_bounds__(kTThreads) void mx_transpose_kernel(
 #pragma unroll
     for (int i = 0; i < 4; ++i) mx_unpack(raw[i], f[i]);
   } else {
-    uint2 word[4];
+    nt_u32x4 word[4];
     uint32_t b[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t r = t0 + tr * 4 + i;
-      word[i] = make_uint2(0u, 0u);
+      word[i] = nt_u32x4{0, 0, 0, 0};
       b[i] = 0;
       if (cact && r < rows) {
-        word[i] = mx_load_codes8<0>(static_cast<const uint8_t*>(x) + (int64_t)r * ldx + c0 + tc * 8);
-        b[i] = s[(int64_t)r * (cols >> 5) + ((c0 + tc * 8) >> 5)];
+        word[i] = *reinterpret_cast<const nt_u32x4*>(static_cast<const uint8_t*>(x) + (int64_t)r * ldx + c0 + tc * 16);
+        b[i] = s[(int64_t)r * (cols >> 5) + ((c0 + tc * 16) >> 5)];
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mx_decode8<(SRC < 2 ? 0 : SRC - 2)>(word[i], mx_factor(b[i]), f[i]);
+    for (int i = 0; i < 4; ++i) {
+      constexpr int QF = SRC < 2 ? 0 : SRC - 2;
+      const float factor = mx_factor(b[i]);
+      float lo[8], hi[8];
+      mx_decode8<QF>(make_uint2(word[i].x, word[i].y), factor, lo);
+      mx_decode8<QF>(make_uint2(word[i].z, word[i].w), factor, hi);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        f[i][j] = lo[j];
+        f[i][CH - 8 + j] = hi[j];
+      }
+    }
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < CH; ++j) {
     const uint32_t m = max_oct(max(max(abs_bits(f[0][j]), abs_bits(f[1][j])), max(abs_bits(f[2][j]), abs_bits(f[3][j]))));
     const MxScale sc = mx_scale<FMT, CEIL>(m);
     uint32_t o = mx_cvt4<FMT>(mx_fit<FMT, CEIL>(f[0][j], sc.inv), mx_fit<FMT, CEIL>(f[1][j], sc.inv),
                               mx_fit<FMT, CEIL>(f[2][j], sc.inv), mx_fit<FMT, CEIL>(f[3][j], sc.inv));
     if (sc.byte == 255u) o = 0;
-    if constexpr (FMT == kE2M1) *reinterpret_cast<uint16_t*>(tile + (tc * 8 + j) * PITCH + tr * 2) = (uint16_t)o;
-    else *reinterpret_cast<uint32_t*>(tile + (tc * 8 + j) * PITCH + tr * 4) = o;
-    if ((lane & 7) == 0) stile[(tc * 8 + j) * 4 + (w & 3)] = (uint8_t)sc.byte;
+    if constexpr (FMT == kE2M1) *reinterpret_cast<uint16_t*>(tile + (tc * CH + j) * PITCH + tr * 2) = (uint16_t)o;
+    else *reinterpret_cast<uint32_t*>(tile + (tc * CH + j) * PITCH + tr * 4) = o;
+    if ((lane & 7) == 0) stile[(tc * CH + j) * 4 + (w & 3)] = (uint8_t)sc.byte;
   }
   __syncthreads();
   constexpr int CPR = RB / 16;  // 16-byte chunks per tile row
 #pragma unroll
-  for (int rep = 0; rep < 128 * CPR / kTThreads; ++rep) {
-    const uint32_t idx = rep * kTThreads + tid;
+  for (int rep = 0; rep < kTile * CPR / THREADS; ++rep) {
+    const uint32_t idx = rep * THREADS + tid;
     const uint32_t ch = idx / CPR, ck = idx % CPR;
-    if (c0 + ch < cols && t0 + ck * (128 / CPR) < rows_out) {
+    if (c0 + ch < cols && t0 + ck * (kTile / CPR) < rows_out) {
       const uint2 a = *reinterpret_cast<const uint2*>(tile + ch * PITCH + ck * 16);
       const uint2 b = *reinterpret_cast<const uint2*>(tile + ch * PITCH + ck * 16 + 8);
-      store_codes(qt + (int64_t)(c0 + ch) * ldqt + t0 * RB / 128 + ck * 16, make_uint4(a.x, a.y, b.x, b.y));
+      store_codes(qt + (int64_t)(c0 + ch) * ldqt + t0 * RB / kTile + ck * 16, make_uint4(a.x, a.y, b.x, b.y));
     }
   }
   const uint32_t ngt = rows_out >> 5;
-  if (tid < 128 && c0 + tid < cols) {
+  if (tid < kTile && c0 + tid < cols) {
     uint8_t* dst = st + (int64_t)(c0 + tid) * ngt + (t0 >> 5);
     if ((ngt & 3) == 0 && ((uintptr_t)st & 3) == 0) {
       *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(stile + tid * 4);
@@ -212,14 +244,14 @@ __global__ __launch_bounds__(kTThreads) void mx_transpose_kernel(
   }
 }
 
-uint32_t row_blocks(int64_t total, int u) {
+uint32_t row_blocks(int64_t total, int u, uint32_t most) {
   const int64_t per = (int64_t)kThreads * u;
   const int64_t n = (total + per - 1) / per;
-  return (uint32_t)(n < kMaxBlocks ? n : kMaxBlocks);
+  return (uint32_t)(n < most ? n : most);
 }
 
-// Units each lane has in flight: 4 where that still fills the chip with
-// workgroups, else 1.
+// Several units in flight per lane where that still fills the chip with
+// workgroups, else one.
 bool deep(int64_t total) { return total >= (int64_t)kThreads * 4 * device_cus(); }
 
 template <typename InT, bool CEIL>
@@ -228,11 +260,11 @@ void rows4(const InT* x, int64_t rows, int64_t cols, int64_t ldx, uint8_t* q, in
   const uint32_t upr = (uint32_t)(cols / kLaneElems);
   const int64_t total = rows * upr;
 #define MXFP8_ROWS4(U, NT)                                                                                         \
-  hipLaunchKernelGGL((mxfp4_rows_kernel<InT, CEIL, U, NT>), dim3(row_blocks(total, U)), dim3(kThreads), 0, stream, \
+  hipLaunchKernelGGL((mxfp4_rows_kernel<InT, CEIL, U, NT>), dim3(row_blocks(total, U, kQuantBlocks)), dim3(kThreads), 0, stream, \
                      x, ldx, upr, total, q, ldq, s)
   if (!deep(total)) MXFP8_ROWS4(1, false);
-  else if (stream_loads(rows, cols, sizeof(InT))) MXFP8_ROWS4(4, true);
-  else MXFP8_ROWS4(4, false);
+  else if (stream_loads(rows, cols, sizeof(InT))) MXFP8_ROWS4(kQuantUnits, true);
+  else MXFP8_ROWS4(kQuantUnits, false);
 #undef MXFP8_ROWS4
 }
 template <typename InT>
@@ -247,23 +279,24 @@ void dequantize(const uint8_t* q, int64_t ldq, const uint8_t* s, int64_t rows, i
                 hipStream_t stream) {
   const uint32_t upr = (uint32_t)(cols / kLaneElems);
   const int64_t total = rows * upr;
-  if (deep(total))
-    hipLaunchKernelGGL((mx_dequantize_kernel<FMT, OutT, 4>), dim3(row_blocks(total, 4)), dim3(kThreads), 0, stream, q,
-                       ldq, s, upr, total, y, ldy);
-  else
-    hipLaunchKernelGGL((mx_dequantize_kernel<FMT, OutT, 1>), dim3(row_blocks(total, 1)), dim3(kThreads), 0, stream, q,
-                       ldq, s, upr, total, y, ldy);
+#define MXFP8_DEQ(U, NT)                                                                                            \
+  hipLaunchKernelGGL((mx_dequantize_kernel<FMT, OutT, U, NT>), dim3(row_blocks(total, U, kDequantBlocks)),          \
+                     dim3(kThreads), 0, stream, q, ldq, s, upr, total, y, ldy)
+  if (!deep(total)) MXFP8_DEQ(1, false);
+  else if (stream_loads(rows, cols, sizeof(OutT))) MXFP8_DEQ(kDequantUnits, true);
+  else MXFP8_DEQ(kDequantUnits, false);
+#undef MXFP8_DEQ
 }
 
 template <int SRC, int FMT, bool CEIL>
 void transpose(const void* x, int64_t ldx, const uint8_t* s, int64_t rows, int64_t cols, uint8_t* qt, int64_t ldqt,
                int64_t rows_out, uint8_t* st, hipStream_t stream) {
-  const int64_t tiles = ((cols + 127) / 128) * ((rows_out + 127) / 128);
+  const dim3 grid((uint32_t)((((cols + 127) / 128) * ((rows_out + 127) / 128) + 7) / 8 * 8));
   if (SRC < 2 && stream_loads(rows, cols, SRC == 0 ? 4 : 2))
-    hipLaunchKernelGGL((mx_transpose_kernel<SRC, FMT, CEIL, (SRC < 2)>), dim3((uint32_t)tiles), dim3(kTThreads), 0,
+    hipLaunchKernelGGL((mx_transpose_kernel<SRC, FMT, CEIL, (SRC < 2)>), grid, dim3(kTThreads<SRC>), 0,
                        stream, x, ldx, s, (uint32_t)rows, (uint32_t)cols, qt, ldqt, (uint32_t)rows_out, st);
   else
-    hipLaunchKernelGGL((mx_transpose_kernel<SRC, FMT, CEIL, false>), dim3((uint32_t)tiles), dim3(kTThreads), 0,
+    hipLaunchKernelGGL((mx_transpose_kernel<SRC, FMT, CEIL, false>), grid, dim3(kTThreads<SRC>), 0,
                        stream, x, ldx, s, (uint32_t)rows, (uint32_t)cols, qt, ldqt, (uint32_t)rows_out, st);
 }
 
