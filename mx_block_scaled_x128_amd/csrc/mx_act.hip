@@ -72,23 +72,23 @@ __global__ __launch_bounds__(kThreads) void swiglu_forward_kernel(
       mx_unpack(ru[i], u);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = g[j] * sigmoid(g[j]) * u[j];
-      const MxScale sv = mx_scale<FMT, CEIL>(max_quad(absmax8(v)));
+      const uint32_t sv = mx_scale<FMT, CEIL>(max_quad(absmax8(v)));
       if constexpr (KEEP) {
-        const MxScale sg = mx_scale<FMT, CEIL>(max_quad(absmax8(g)));
-        const MxScale su = mx_scale<FMT, CEIL>(max_quad(absmax8(u)));
+        const uint32_t sg = mx_scale<FMT, CEIL>(max_quad(absmax8(g)));
+        const uint32_t su = mx_scale<FMT, CEIL>(max_quad(absmax8(u)));
         if (unit < upr) {
           uint8_t* kr = kept + row * ldk;
           mx_keep_codes8<NT>(kr + unit * 8, mx_codes8<FMT, CEIL>(g, sg));
           mx_keep_codes8<NT>(kr + cols + unit * 8, mx_codes8<FMT, CEIL>(u, su));
           if ((lane & 3) == 0) {
-            ks[row * (2 * nb) + (unit >> 2)] = (uint8_t)sg.byte;
-            ks[row * (2 * nb) + nb + (unit >> 2)] = (uint8_t)su.byte;
+            ks[row * (2 * nb) + (unit >> 2)] = (uint8_t)sg;
+            ks[row * (2 * nb) + nb + (unit >> 2)] = (uint8_t)su;
           }
         }
       }
       if (unit < upr) {
         mx_store_codes8<FMT>(h + row * ldh + unit * 8, mx_codes8<FMT, CEIL>(v, sv));
-        if ((lane & 3) == 0) hs[row * nb + (unit >> 2)] = (uint8_t)sv.byte;
+        if ((lane & 3) == 0) hs[row * nb + (unit >> 2)] = (uint8_t)sv;
       }
     }
   }
@@ -256,13 +256,13 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_forward_kernel(
       mx_unpack(raw[i], f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = f[j] * r * wf[j];
-      const MxScale sv = mx_scale<FMT, CEIL>(max_quad(absmax8(v)));
+      const uint32_t sv = mx_scale<FMT, CEIL>(max_quad(absmax8(v)));
       mx_put_codes(ry, at(i, cq), i * USTEP * 8, mx_codes8<FMT, CEIL>(v, sv));
-      mx_put_byte(rys, at(i, cs), i * USTEP / 4, sv.byte);
+      mx_put_byte(rys, at(i, cs), i * USTEP / 4, sv);
       if (kept) {
-        const MxScale sk = mx_scale<FMT, CEIL>(max_quad(absmax8(f)));
+        const uint32_t sk = mx_scale<FMT, CEIL>(max_quad(absmax8(f)));
         mx_put_codes(rk, at(i, cq), i * USTEP * 8, mx_codes8<FMT, CEIL>(f, sk));
-        mx_put_byte(rks, at(i, cs), i * USTEP / 4, sk.byte);
+        mx_put_byte(rks, at(i, cs), i * USTEP / 4, sk);
       }
     }
     if (kept && unit0 == 0) rstd[row] = r;

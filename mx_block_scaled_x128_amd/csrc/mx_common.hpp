@@ -38,75 +38,67 @@ template <> struct MxFmt<kE2M1> {
   static constexpr int code_bits = 4;
 };
 
-// Exponent of a finite block maximum (its fp32 bits).  ceil: the smallest e
-// with amax <= fmax * 2^e; otherwise floor(log2 amax) - q; both clamped to
-// [-127, 127].  A subnormal amax gives -127 under both rules.
+// Scale byte of a block from the bits of its largest |x|.  The exponent e is,
+// ceil: the smallest with amax <= fmax * 2^e; otherwise floor(log2 amax) - q;
+// clamped to [-127, 127], which a subnormal amax reaches at the low end; the
+// byte is e + 127.  fmax = (1 + frac_max / 2^23) * 2^q, so under the ceil rule
+// the exponent field grows by one exactly when the fraction passes frac_max,
+// that is when adding 0x7FFFFF - frac_max carries into it.  255 for a block
+// with an infinity or a NaN.
 template <int FMT, bool CEIL>
-__device__ __forceinline__ int mx_exp(uint32_t amax_bits) {
-  const int E = (int)(amax_bits >> 23);
-  int e = E - 127 - MxFmt<FMT>::q;
-  if (CEIL && (amax_bits & 0x7FFFFFu) > MxFmt<FMT>::frac_max) ++e;
-  return E == 0 || e < -127 ? -127 : e;  // e <= 127 - q + 1 for finite amax
+__device__ __forceinline__ uint32_t mx_scale(uint32_t amax_bits) {
+  const uint32_t field = (amax_bits + (CEIL ? 0x7FFFFFu - MxFmt<FMT>::frac_max : 0u)) >> 23;
+  const uint32_t byte = __builtin_elementwise_sub_sat(field, (uint32_t)MxFmt<FMT>::q);
+  return amax_bits < kInfBits ? byte : 255u;
 }
 
-// Scale byte and the factor 2^-e of a block.  A block with a non-finite
-// element: byte 255 and factor 0 (mx_cast then gives zero codes, see there).
-struct MxScale {
-  uint32_t byte;
-  float inv;
-};
-template <int FMT, bool CEIL>
-__device__ __forceinline__ MxScale mx_scale(uint32_t amax_bits) {
-  const int e = mx_exp<FMT, CEIL>(amax_bits);
-  const bool ok = amax_bits < kInfBits;
-  return MxScale{ok ? (uint32_t)(e + 127) : 255u, ok ? pow2_neg(e) : 0.0f};
-}
-
-// x * 2^-e for the cast.  The floor rule leaves values up to 2^(q+1), which
-// are held to +-fmax here; the ceil rule leaves none above fmax.  A block with
-// factor 0 may give NaN (inf * 0): its codes are dropped after the cast.
-template <int FMT, bool CEIL>
-__device__ __forceinline__ float mx_fit(float x, float inv) {
-  if constexpr (CEIL) return x * inv;
+// Codes of values under scale byte `byte` (not 255): cast(x * 2^-e), to
+// nearest even, saturating.  The conversions divide by the scale themselves
+// (they take 2^e as a float, of which they use the exponent field); E2M1 ones
+// saturate.  FP8 ones do not, so where values can pass fmax (the floor rule
+// leaves them up to 2^(q+1)) the value is scaled and held to +-fmax first.
+template <int FMT>
+__device__ __forceinline__ float mx_fit(float x, uint32_t byte) {
+  const float inv = __uint_as_float((254u - byte) << 23);  // 2^-e
   return __builtin_amdgcn_fmed3f(x * inv, -MxFmt<FMT>::fmax, MxFmt<FMT>::fmax);
 }
-
-// Four values in range -> four codes: FP8 in 32 bits, E2M1 in the low 16.
-// v_cvt_scalef32_pk_fp4_f32 with scale 1 rounds to nearest even.
-template <int FMT>
-__device__ __forceinline__ uint32_t mx_cvt4(float a, float b, float c, float d) {
+// Four values: FP8 codes in 32 bits, E2M1 codes in the low 16.
+typedef short mx_s2 __attribute__((ext_vector_type(2)));
+template <int FMT, bool CEIL>
+__device__ __forceinline__ uint32_t mx_codes4(float a, float b, float c, float d, uint32_t byte) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const float scale = __uint_as_float(byte << 23);
   if constexpr (FMT == kE2M1) {
     uint32_t w = 0;
-#if defined(__HIP_DEVICE_COMPILE__)
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, a, b, 1.0f, 0);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, c, d, 1.0f, 1);
-#endif
-    return w;
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, a, b, scale, 0);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, c, d, scale, 1);
+  } else if constexpr (CEIL && FMT == 0) {
+    mx_s2 w = {0, 0};
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a, b, scale, false);
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c, d, scale, true));
+  } else if constexpr (CEIL) {
+    mx_s2 w = {0, 0};
+    w = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(w, a, b, scale, false);
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(w, c, d, scale, true));
   } else {
-    return cvt4<FMT>(a, b, c, d);
+    return cvt4<FMT>(mx_fit<FMT>(a, byte), mx_fit<FMT>(b, byte), mx_fit<FMT>(c, byte), mx_fit<FMT>(d, byte));
   }
+#else
+  return 0;
+#endif
 }
 
-// Eight codes: FP8 in both words, E2M1 in the first.
+// Eight codes: FP8 in both words, E2M1 in the first; zeros under scale byte 255.
 template <int FMT, bool CEIL>
-__device__ __forceinline__ uint2 mx_codes8(const float (&f)[8], const MxScale& s) {
+__device__ __forceinline__ uint2 mx_codes8(const float (&f)[8], uint32_t byte) {
   uint2 o = make_uint2(0u, 0u);
-#if defined(__HIP_DEVICE_COMPILE__)
   if constexpr (FMT == kE2M1) {
-    uint32_t w = 0;
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, mx_fit<FMT, CEIL>(f[0], s.inv), mx_fit<FMT, CEIL>(f[1], s.inv), 1.0f, 0);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, mx_fit<FMT, CEIL>(f[2], s.inv), mx_fit<FMT, CEIL>(f[3], s.inv), 1.0f, 1);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, mx_fit<FMT, CEIL>(f[4], s.inv), mx_fit<FMT, CEIL>(f[5], s.inv), 1.0f, 2);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, mx_fit<FMT, CEIL>(f[6], s.inv), mx_fit<FMT, CEIL>(f[7], s.inv), 1.0f, 3);
-    o.x = w;
+    o.x = mx_codes4<FMT, CEIL>(f[0], f[1], f[2], f[3], byte) | mx_codes4<FMT, CEIL>(f[4], f[5], f[6], f[7], byte) << 16;
   } else {
-    o.x = cvt4<FMT>(mx_fit<FMT, CEIL>(f[0], s.inv), mx_fit<FMT, CEIL>(f[1], s.inv), mx_fit<FMT, CEIL>(f[2], s.inv),
-                    mx_fit<FMT, CEIL>(f[3], s.inv));
-    o.y = cvt4<FMT>(mx_fit<FMT, CEIL>(f[4], s.inv), mx_fit<FMT, CEIL>(f[5], s.inv), mx_fit<FMT, CEIL>(f[6], s.inv),
-                    mx_fit<FMT, CEIL>(f[7], s.inv));
+    o.x = mx_codes4<FMT, CEIL>(f[0], f[1], f[2], f[3], byte);
+    o.y = mx_codes4<FMT, CEIL>(f[4], f[5], f[6], f[7], byte);
   }
-#endif
-  if (s.byte == 255u) o = make_uint2(0u, 0u);
+  if (byte == 255u) o = make_uint2(0u, 0u);
   return o;
 }
 

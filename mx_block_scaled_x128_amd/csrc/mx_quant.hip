@@ -76,11 +76,11 @@ __global__ __launch_bounds__(kThreads) void mxfp4_rows_kernel(const InT* __restr
       float f[8];
       mx_unpack(raw[u], f);
       // a row holds whole blocks, so a quad never straddles rows or the end
-      const MxScale sc = mx_scale<kE2M1, CEIL>(max_quad(absmax8(f)));
+      const uint32_t sc = mx_scale<kE2M1, CEIL>(max_quad(absmax8(f)));
       const uint2 w = mx_codes8<kE2M1, CEIL>(f, sc);
       if (act[u]) {
         mx_store_codes8<kE2M1>(q + p[u].row * ldq + p[u].unit * 4, w);
-        if ((lane & 3) == 0) s[p[u].row * (upr >> 2) + (p[u].unit >> 2)] = (uint8_t)sc.byte;
+        if ((lane & 3) == 0) s[p[u].row * (upr >> 2) + (p[u].unit >> 2)] = (uint8_t)sc;
       }
     }
   }
@@ -211,13 +211,12 @@ __global__ __launch_bounds__(kTThreads<SRC>) void mx_transpose_kernel(
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
     const uint32_t m = max_oct(max(max(abs_bits(f[0][j]), abs_bits(f[1][j])), max(abs_bits(f[2][j]), abs_bits(f[3][j]))));
-    const MxScale sc = mx_scale<FMT, CEIL>(m);
-    uint32_t o = mx_cvt4<FMT>(mx_fit<FMT, CEIL>(f[0][j], sc.inv), mx_fit<FMT, CEIL>(f[1][j], sc.inv),
-                              mx_fit<FMT, CEIL>(f[2][j], sc.inv), mx_fit<FMT, CEIL>(f[3][j], sc.inv));
-    if (sc.byte == 255u) o = 0;
+    const uint32_t sc = mx_scale<FMT, CEIL>(m);
+    uint32_t o = mx_codes4<FMT, CEIL>(f[0][j], f[1][j], f[2][j], f[3][j], sc);
+    if (sc == 255u) o = 0;
     if constexpr (FMT == kE2M1) *reinterpret_cast<uint16_t*>(tile + (tc * CH + j) * PITCH + tr * 2) = (uint16_t)o;
     else *reinterpret_cast<uint32_t*>(tile + (tc * CH + j) * PITCH + tr * 4) = o;
-    if ((lane & 7) == 0) stile[(tc * CH + j) * 4 + (w & 3)] = (uint8_t)sc.byte;
+    if ((lane & 7) == 0) stile[(tc * CH + j) * 4 + (w & 3)] = (uint8_t)sc;
   }
   __syncthreads();
   constexpr int CPR = RB / 16;  // 16-byte chunks per tile row
