@@ -380,7 +380,7 @@ int mx_requantize_t(const uint8_t* q, int64_t ldq, int q_fmt, const uint8_t* sca
  * a: [M][lda] codes (a_fmt), a_scales [M][K / 32].
  * b: [N][ldb >= K / 2 bytes] E2M1 codes, b_scales [N][K / 32].
  * c: [M][ldc >= N], fp32 or bf16 (c_dtype), overwritten.
- * Requires K % 128 == 0, 4-byte aligned scale pointers, lda and ldb <= 2^24;
+ * Requires K % 128 == 0, 4-byte aligned scale pointers, lda and ldb <= 2^22;
  * M and N are arbitrary.  Accuracy as for mx_gemm.
  */
 int mxfp4_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, int a_fmt, const uint8_t* a_scales,
@@ -411,7 +411,8 @@ int mx_swiglu_backward(const uint8_t* kept, int64_t ldk, const uint8_t* kept_sca
 /*
  * mx_rmsnorm_forward -- y = x * r * w, r = 1 / sqrt(mean over the row of x^2 + eps),
  * computed in fp32 and written as MX codes along rows.
- *   x: [rows][ldx >= cols] fp32 or bf16;  w: [cols] fp32, 16-byte aligned;  eps >= 0 and finite.
+ *   x: [rows][ldx >= cols] fp32 or bf16;  w: [cols] fp32, 16-byte aligned;
+ *   eps >= 0 and finite (MXFP8_ERR_SHAPE otherwise).
  *   y: [rows][ldy >= cols] codes of fmt (E4M3 or E5M2), y_scales [rows][cols / 32].
  *   kept: [rows][ldk >= cols] codes of x, kept_scales [rows][cols / 32], and
  *         rstd: [rows] fp32 = r, for mx_rmsnorm_backward.  All three NULL:

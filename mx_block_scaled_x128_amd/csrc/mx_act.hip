@@ -199,6 +199,7 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_forward_kernel(
     const InT* __restrict__ x, int64_t ldx, int64_t rows, uint32_t upr, const float* __restrict__ w,
     float eps, uint8_t* __restrict__ y, int64_t ldy, uint8_t* __restrict__ ys, uint8_t* __restrict__ kept, int64_t ldk,
     uint8_t* __restrict__ ks, float* __restrict__ rstd) {
+#if defined(__HIP_DEVICE_COMPILE__)
   extern __shared__ nt_f32x4 lds[];
   __shared__ float red[16];
   const uint32_t lane = threadIdx.x & 63;
@@ -209,7 +210,6 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_forward_kernel(
   constexpr uint32_t USTEP = WPR * 64;
   const uint32_t nb = upr >> 2;
   const float inv_cols = 1.0f / (float)(upr * 8);
-#if defined(__HIP_DEVICE_COMPILE__)
   // Lane offsets: one per tensor; the last unit's own, outside past the row's end.
   const bool last_in = unit0 + (NU - 1) * USTEP < upr;
   const uint32_t cx = unit0 * 8 * sizeof(InT), cq = unit0 * 8, cs = (lane & 3) == 0 ? unit0 >> 2 : kNowhere;
@@ -285,6 +285,7 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(
     const uint8_t* __restrict__ kept, int64_t ldk, const uint8_t* __restrict__ ks, const float* __restrict__ rstd,
     const float* __restrict__ w, const T* __restrict__ dy, int64_t lddy, int64_t rows, uint32_t upr,
     T* __restrict__ dx, int64_t lddx, float* __restrict__ part) {
+#if defined(__HIP_DEVICE_COMPILE__)
   extern __shared__ nt_f32x4 lds[];
   __shared__ float red[16];
   const uint32_t lane = threadIdx.x & 63;
@@ -295,7 +296,6 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(
   constexpr uint32_t USTEP = WPR * 64;
   const uint32_t nb = upr >> 2;
   const float inv_cols = 1.0f / (float)(upr * 8);
-#if defined(__HIP_DEVICE_COMPILE__)
   typedef BackwardIn<T, NU> In;
   // Lane offsets: one per tensor; the last unit's own, outside past the row's end.
   const bool last_in = unit0 + (NU - 1) * USTEP < upr;

@@ -12,7 +12,9 @@
 
 namespace {
 
-constexpr int64_t kMaxGemmLd = int64_t(1) << 24;
+// The product addresses a tile of up to 256 rows, and K along them, with
+// offsets below 2^31.
+constexpr int64_t kMaxGemmLd = int64_t(1) << 22;
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 bool fp8(int fmt) { return fmt == MXFP8_E4M3 || fmt == MXFP8_E5M2; }

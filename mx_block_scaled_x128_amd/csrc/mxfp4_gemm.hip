@@ -396,7 +396,9 @@ __device__ __forceinline__ void gemm_tile(int M, int N, int K, const uint8_t* __
   const int n0 = (((within / gsz) << sn) + (sub & ((1 << sn) - 1))) * BN;
   if (m0 >= M || n0 >= N) return;
 
-  const int nkb = (K + T::KB - 1) / T::KB, sk = K >> 5;
+  // K blocks that hold something, up to `last`; at least two are multiplied,
+  // those past it as zeros.
+  const int last = (K + T::KB - 1) / T::KB - 1, nkb = max(last + 1, 2), sk = K >> 5;
   const __amdgpu_buffer_rsrc_t ra = descriptor(A + (int64_t)m0 * lda), rb = descriptor(B + (int64_t)n0 * ldb);
   const uint8_t *pa = SA + (int64_t)m0 * sk, *pb = SB + (int64_t)n0 * sk;
   const __amdgpu_buffer_rsrc_t rsa = descriptor(pa), rsb = descriptor(pb), rsw = descriptor(wave < 2 ? pa : pb);
@@ -428,13 +430,13 @@ __device__ __forceinline__ void gemm_tile(int M, int N, int K, const uint8_t* __
   constexpr int DMA_ITEMS = A_LOADS + B_LOADS;
   auto dma_item = [&](int p, int kb, int item) __attribute__((always_inline)) {
     uint8_t* buf = buf_ptr(p);
-    const bool cut = half_last && kb == nkb - 1;
+    const bool none = kb > last, cut = half_last && kb == last;
     if (item < A_LOADS) {
-      const uint32_t off = cut && a_unit >= 64 ? kOutside : a_off[item];
+      const uint32_t off = none || (cut && a_unit >= 64) ? kOutside : a_off[item];
       load_lds<16>(ra, buf + (item * 4 + wave) * 1024, off, kb * T::AB);
     } else {
       const int j = item - A_LOADS;
-      const uint32_t off = cut && b_unit >= 64 ? kOutside : b_off[j];
+      const uint32_t off = none || (cut && b_unit >= 64) ? kOutside : b_off[j];
       load_lds<16>(rb, buf + T::A_ST + (j * 4 + wave) * 1024, off, kb * T::BB);
     }
   };
@@ -639,7 +641,7 @@ __device__ __forceinline__ void gemm_tile(int M, int N, int K, const uint8_t* __
     }
   };
 
-  // K >= 2 K blocks (the launcher's condition): blocks 0 and 1 in flight.
+  // K blocks 0 and 1 in flight.
   scale_loads(0);
 #pragma unroll
   for (int item = 0; item < DMA_ITEMS; ++item) dma_item(0, 0, item);
@@ -752,17 +754,17 @@ void gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const 
   // M N = 700000 (us, few rows / tiles, E5M2-or-E4M3 x E2M1: 64x8960x1536
   // 7.7 / 8.5, 96x8960x1536 10.0 / 8.6, 128x3584x3584 13.6 / 18.3, 256x3584x3584
   // 25.5 / 19.0, 512x1536x8960 42 / 44; E2M1 pairs: 128x3584x3584 7.7 / 11.3,
-  // 256x3584x3584 14.0 / 12.4).  The tile kernel takes two K blocks at least,
-  // the few-row kernel as many scales as fit in LDS.
+  // 256x3584x3584 14.0 / 12.4).  The few-row kernel takes as many scales as fit
+  // in LDS and 2^26 rows of B (its grid).
   const int chunks = (int)(K / 128);
   const int64_t n16 = (N + 15) / 16, pairs = ((N + 31) / 32) * ((M + 31) / 32);
-  const bool one_block = K <= Tile<256, 256, AFMT>::KB;
-  const bool few = (M <= 16 || M * N <= 700000) && few_rows_lds<AFMT, 2, 2, 4, false>(0, (int)K) <= kFewRowsLds;
+  const bool few = (M <= 16 ? N <= (int64_t(1) << 26) : M * N <= 700000) &&
+                   few_rows_lds<AFMT, 2, 2, 4, false>(0, (int)K) <= kFewRowsLds;
 #define MXFP4_FEW(MT, NT, WAVES, U)                                                                           \
   (few_rows_lds<AFMT, MT, NT, WAVES, true>((int)(M < 16 * MT ? M : 16 * MT), (int)K) <= kFewRowsLds           \
        ? few_rows<AFMT, MT, NT, WAVES, U, true>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, stream)     \
        : few_rows<AFMT, MT, NT, WAVES, U, false>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, stream))
-  if (few || one_block) {
+  if (few) {
     if (M <= 16) {
       // Waves of a workgroup: they cost to start (1 us per 1000), so two where
       // a run of K is short (1x8960x1536: two 3.5 us, four 4.0; 1x18944x3584:
@@ -772,7 +774,7 @@ void gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const 
       if (wide_a) MXFP4_FEW(1, 2, 8, 2);
       else if (chunks <= 16) MXFP4_FEW(1, 1, 2, 4);
       else MXFP4_FEW(1, 1, 4, 4);
-    } else if (pairs < 128 && !one_block) {
+    } else if (pairs < 128) {
       // Few workgroups of 32 x 32: smaller ones with K over eight waves
       // (37x1536x8960: 7.5 us against 8.2-11.4, E4M3 10.9 against 12.6-16.0).
       MXFP4_FEW(1, 2, 8, 2);

@@ -142,3 +142,61 @@ def test_full_k_and_large_extents():
         b, sb = operand(N, K, mx.E2M1, 2, spread=0)
         y, t = product(a, sa, fmt, b, sb)
         assert_gemm_close(run(a, sa, fmt, b, sb, torch.float32), y, t, False, what=str((M, N, K)))
+
+
+@pytest.mark.parametrize("a_fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [(900, 900, 128), (900, 900, 256), (2100, 420, 384), (700, 1100, 0)])
+def test_tiles_with_one_k_block_or_none(M, N, K, a_fmt):
+    a, sa = operand(M, K, a_fmt, 3) if K else (np.zeros((M, 0), np.uint8), np.zeros((M, 0), np.uint8))
+    b, sb = operand(N, K, mx.E2M1, 4) if K else (np.zeros((N, 0), np.uint8), np.zeros((N, 0), np.uint8))
+    y, t = product(a, sa, a_fmt, b, sb) if K else (np.zeros((M, N)), np.zeros((M, N)))
+    assert_gemm_close(run(a, sa, a_fmt, b, sb, torch.float32), y, t, False)
+
+
+@pytest.mark.parametrize("a_fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [(2600, 2570, 512), (2600, 2570, 640), (4100, 4200, 256), (512, 8704, 1152)])
+def test_large_tiles_and_their_tail(M, N, K, a_fmt):
+    """256 x 256 tiles, with and without a last round cut in quadrants, sampled against fp64."""
+    a, sa = operand(M, K, a_fmt, 5, spread=2)
+    b, sb = operand(N, K, mx.E2M1, 6, spread=2)
+    y, t = product(a, sa, a_fmt, b, sb)
+    assert_gemm_close(run(a, sa, a_fmt, b, sb, torch.float32), y, t, False)
+    assert_gemm_close(run(a, sa, a_fmt, b, sb, torch.bfloat16, pad=32), y, t, True)
+
+
+@pytest.mark.parametrize("a_fmt", FMTS)
+def test_scales_at_odd_addresses(a_fmt):
+    """Scale pointers on 4-byte boundaries only (the copies and tiles then load 4 bytes a lane)."""
+    for M, N, K in ((3, 100, 512), (40, 200, 1024), (1000, 1000, 1024)):
+        a, sa = operand(M, K, a_fmt, 7)
+        b, sb = operand(N, K, mx.E2M1, 8)
+        flat_a = torch.empty(sa.size + 4, dtype=torch.uint8, device="cuda")
+        flat_b = torch.empty(sb.size + 4, dtype=torch.uint8, device="cuda")
+        va, vb = flat_a[4:].view(sa.shape), flat_b[4:].view(sb.shape)
+        va.copy_(dev(sa))
+        vb.copy_(dev(sb))
+        out = mx.mxfp4_scaled_gemm(dev_ld16(a), va, a_fmt, dev_ld16(b), vb)
+        y, t = product(a, sa, a_fmt, b, sb)
+        assert_gemm_close(host(out), y, t, False, what=str((M, N, K)))
+
+
+@pytest.mark.parametrize("a_fmt", FMTS)
+def test_graph_and_stream(a_fmt):
+    a, sa = operand(9, 1024, a_fmt, 1)
+    b, sb = operand(300, 1024, mx.E2M1, 2)
+    a_d, sa_d, b_d, sb_d = dev(a), dev(sa), dev(b), dev(sb)
+    out = torch.zeros((9, 304), device="cuda")[:, :300]
+    want = mx.mxfp4_scaled_gemm(a_d, sa_d, a_fmt, b_d, sb_d)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    mx.mxfp4_scaled_gemm(a_d, sa_d, a_fmt, b_d, sb_d, out=out, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(out, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mx.mxfp4_scaled_gemm(a_d, sa_d, a_fmt, b_d, sb_d, out=out)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, mx.mxfp4_scaled_gemm(a_d, sa_d, a_fmt, b_d, sb_d))
