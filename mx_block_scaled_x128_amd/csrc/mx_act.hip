@@ -209,7 +209,6 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_forward_kernel(
   const uint32_t unit0 = (WPR == 1 ? 0 : wave * 64) + lane;
   constexpr uint32_t USTEP = WPR * 64;
   const uint32_t nb = upr >> 2;
-  const float inv_cols = 1.0f / (float)(upr * 8);
   // Lane offsets: one per tensor; the last unit's own, outside past the row's end.
   const bool last_in = unit0 + (NU - 1) * USTEP < upr;
   const uint32_t cx = unit0 * 8 * sizeof(InT), cq = unit0 * 8, cs = (lane & 3) == 0 ? unit0 >> 2 : kNowhere;
@@ -233,20 +232,21 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_forward_kernel(
 #pragma unroll
     for (int i = 0; i < NU; ++i) raw[i] = next[i];
     load(ahead, next);
-    float ss = 0.0f;
+    // Eight chains over the units, joined pair by pair, and the row's few last
+    // steps in 64 bits: what r is off by moves a whole row across the casts' ties.
+    float sq[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
       float f[8];
       mx_unpack(raw[i], f);
-      float part = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) part = __builtin_fmaf(f[j], f[j], part);
-      ss += part;
+      for (int j = 0; j < 8; ++j) sq[j] = __builtin_fmaf(f[j], f[j], sq[j]);
     }
+    float ss = ((sq[0] + sq[1]) + (sq[2] + sq[3])) + ((sq[4] + sq[5]) + (sq[6] + sq[7]));
     ss = row_sum<WPR>(ss, wave, red);
 #pragma unroll
     for (int i = 0; i < NU; ++i) again(raw[i]);
-    const float r = 1.0f / __builtin_sqrtf(ss * inv_cols + eps);
+    const float r = (float)(1.0 / __builtin_sqrt((double)ss / (double)(upr * 8) + (double)eps));
     const mx_rsrc ry = mx_run(y + row * ldy), rys = mx_run(ys + row * nb);
     const mx_rsrc rk = mx_run(kept + row * ldk), rks = mx_run(ks + row * nb);
 #pragma unroll
