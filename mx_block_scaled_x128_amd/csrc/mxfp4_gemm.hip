@@ -367,12 +367,13 @@ __device__ __forceinline__ uint32_t opaque(uint32_t x) {
 
 // SW: scale rows that start on 16-byte boundaries are loaded 16 bytes a lane,
 // others 4.
-template <int BM, int BN, int AFMT, bool SW, typename OutT>
+template <int BM, int BN, int AFMT, bool SW, int RING, typename OutT>
 __device__ __forceinline__ void gemm_tile(int M, int N, int K, const uint8_t* __restrict__ A, int64_t lda,
                                           const uint8_t* __restrict__ SA, const uint8_t* __restrict__ B, int64_t ldb,
                                           const uint8_t* __restrict__ SB, OutT* __restrict__ C, int64_t ldc,
                                           int tiles_m, int tiles_n, int tile_first, int sm, int sn, int wg, int nwg,
-                                          uint8_t* kbuf0, uint8_t* kbuf1, uint8_t* sgrp) {
+                                          uint8_t* kbuf0, uint8_t* kbuf1, uint8_t* kbuf2, uint8_t* kbuf3,
+                                          uint8_t* sgrp) {
 #if defined(__HIP_DEVICE_COMPILE__)
   typedef Tile<BM, BN, AFMT> T;
   constexpr bool A4 = T::A4;
@@ -426,7 +427,9 @@ __device__ __forceinline__ void gemm_tile(int M, int N, int K, const uint8_t* __
   // The last K block of E2M1 pairs may be half full: its upper half reads as zeros.
   const bool half_last = A4 && (K & 255) != 0;
 
-  auto buf_ptr = [&](int p) __attribute__((always_inline)) -> uint8_t* { return p == 0 ? kbuf0 : kbuf1; };
+  auto buf_ptr = [&](int p) __attribute__((always_inline)) -> uint8_t* {
+    return p == 0 ? kbuf0 : p == 1 ? kbuf1 : p == 2 ? kbuf2 : kbuf3;
+  };
   constexpr int DMA_ITEMS = A_LOADS + B_LOADS;
   auto dma_item = [&](int p, int kb, int item) __attribute__((always_inline)) {
     uint8_t* buf = buf_ptr(p);
@@ -541,7 +544,7 @@ __device__ __forceinline__ void gemm_tile(int M, int N, int K, const uint8_t* __
   // One stage: matrix instruction i, then the LDS reads of the next stage and
   // the loads whose turn comes after it.  rd: read stage next_h of
   // buffer next_p into nf; sc: K block kb + 1's scales too.  dma: load K block
-  // kb + 2 into buffer p.  sg: load the next scale group.
+  // kb + RING into buffer p.  sg: load the next scale group.
   constexpr int MFMAS = MT * NT * STEPS;
     // Fragment reads over the first half of the stage, loads over all of it
   // (8192x3584x18944, E2M1 pairs / E5M2 x E2M1: half 243 / 373 us, three
@@ -580,19 +583,20 @@ __device__ __forceinline__ void gemm_tile(int M, int N, int K, const uint8_t* __
         if (rd && item * DS_SPAN / DS_ITEMS == i) ds_item(next_p, next_h, item, nf);
 #pragma unroll
       for (int item = 0; item < DMA_ITEMS; ++item)
-        if (dma && item * MFMAS / DMA_ITEMS == i) dma_item(p, kb + 2, item);
+        if (dma && item * MFMAS / DMA_ITEMS == i) dma_item(p, kb + RING, item);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
 
   Frags f0, f1;
   int sa0[MT], sb0[NT], sa1[MT], sb1[NT];
-  // K block kb in buffer p.  dma: K block kb + 2 exists; next: kb + 1 does.
+  // K block kb in buffer p.  dma: K block kb + RING exists; next: kb + 1 does.
+  // With four buffers two K blocks stay in flight across the wait.
   auto kblock = [&](int p, int kb, bool dma, bool next, bool sg, const int (&sa)[MT], const int (&sb)[NT],
                     int (&nsa)[MT], int (&nsb)[NT]) __attribute__((always_inline)) {
     stage(p, 0, kb, true, p, 1, false, false, false, f0, f1, sa, sb, nsa, nsb);
-    if (next) wait_loads_and_meet<0>();
-    stage(p, 1, kb, next, p ^ 1, 0, next, dma, sg, f1, f0, sa, sb, nsa, nsb);
+    if (next) wait_loads_and_meet<(RING - 2) * DMA_ITEMS>();
+    stage(p, 1, kb, next, (p + 1) % RING, 0, next, dma, sg, f1, f0, sa, sb, nsa, nsb);
   };
 
   // Epilogue: each wave stages a 32-row strip at a time in its own part of a
@@ -641,17 +645,40 @@ __device__ __forceinline__ void gemm_tile(int M, int N, int K, const uint8_t* __
     }
   };
 
-  // K blocks 0 and 1 in flight.
+  // The first RING K blocks in flight.
   scale_loads(0);
 #pragma unroll
-  for (int item = 0; item < DMA_ITEMS; ++item) dma_item(0, 0, item);
+  for (int q = 0; q < RING; ++q)
 #pragma unroll
-  for (int item = 0; item < DMA_ITEMS; ++item) dma_item(1, 1, item);
-  wait_loads_and_meet<DMA_ITEMS>();
+    for (int item = 0; item < DMA_ITEMS; ++item) dma_item(q, q, item);
+  wait_loads_and_meet<(RING - 1) * DMA_ITEMS>();
 #pragma unroll
   for (int item = 0; item < DS_ITEMS; ++item) ds_item(0, 0, item, f0);
   read_scales(0, sa0, sb0);
 
+  if constexpr (RING == 4) {
+    // K blocks in fours, then up to three more.  Every one loads the block four
+    // later and reads the next one's fragments, whether or not they exist (then
+    // zeros), so that the waits count the same loads everywhere.
+    int kb = 0;
+#pragma nounroll
+    for (; kb + 4 <= nkb; kb += 4) {
+      kblock(0, kb, true, true, true, sa0, sb0, sa1, sb1);
+      kblock(1, kb + 1, true, true, false, sa1, sb1, sa0, sb0);
+      kblock(2, kb + 2, true, true, false, sa0, sb0, sa1, sb1);
+      kblock(3, kb + 3, true, true, false, sa1, sb1, sa0, sb0);
+    }
+    if (kb < nkb) {
+      kblock(0, kb, true, true, true, sa0, sb0, sa1, sb1);
+      if (kb + 1 < nkb) {
+        kblock(1, kb + 1, true, true, false, sa1, sb1, sa0, sb0);
+        if (kb + 2 < nkb) kblock(2, kb + 2, true, true, false, sa0, sb0, sa1, sb1);
+      }
+    }
+    mfma_retire_pad();
+    wait_loads_and_meet<0>();  // nothing is on its way to the buffers any more
+    epilogue(kbuf0);
+  } else {
   // K blocks whose second stage loads a later one, in fours (one scale group
   // each), then a pair and a lone one.
   const int main_kb = nkb - 2;
@@ -686,11 +713,12 @@ __device__ __forceinline__ void gemm_tile(int M, int N, int K, const uint8_t* __
 #pragma unroll
     for (int j = 0; j < NT; ++j) asm volatile("" : "+a"(acc[i][j]));  // the accumulators stay where they are
   epilogue(buf_ptr(p));
+  }
 #endif
 }
 
-template <int BM, int BN, int AFMT, bool SW, typename OutT>
-__global__ __launch_bounds__(kTileThreads, BM == 128 ? 2 : 1) void tile_kernel(
+template <int BM, int BN, int AFMT, bool SW, int RING, typename OutT>
+__global__ __launch_bounds__(kTileThreads, BM == 128 && RING == 2 ? 2 : 1) void tile_kernel(
     int M, int N, int K, const uint8_t* __restrict__ A, int64_t lda, const uint8_t* __restrict__ SA,
     const uint8_t* __restrict__ B, int64_t ldb, const uint8_t* __restrict__ SB, OutT* __restrict__ C, int64_t ldc,
     int tiles_m, int tiles_n) {
@@ -699,8 +727,15 @@ __global__ __launch_bounds__(kTileThreads, BM == 128 ? 2 : 1) void tile_kernel(
   __shared__ __attribute__((aligned(1024))) uint8_t kbuf0[T::PB];
   __shared__ __attribute__((aligned(1024))) uint8_t kbuf1[T::PB];
   __shared__ __attribute__((aligned(1024))) uint8_t sgrp[T::SGRP];
-  gemm_tile<BM, BN, AFMT, SW, OutT>(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, tiles_m, tiles_n, 0, 0, 0, blockIdx.x,
-                                    gridDim.x, kbuf0, kbuf1, sgrp);
+  if constexpr (RING == 4) {
+    __shared__ __attribute__((aligned(1024))) uint8_t kbuf2[T::PB];
+    __shared__ __attribute__((aligned(1024))) uint8_t kbuf3[T::PB];
+    gemm_tile<BM, BN, AFMT, SW, RING, OutT>(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, tiles_m, tiles_n, 0, 0, 0,
+                                            blockIdx.x, gridDim.x, kbuf0, kbuf1, kbuf2, kbuf3, sgrp);
+  } else {
+    gemm_tile<BM, BN, AFMT, SW, RING, OutT>(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, tiles_m, tiles_n, 0, 0, 0,
+                                            blockIdx.x, gridDim.x, kbuf0, kbuf1, nullptr, nullptr, sgrp);
+  }
 #endif
 }
 
@@ -718,11 +753,11 @@ __global__ __launch_bounds__(kTileThreads, 1) void tail_kernel(
   __shared__ __attribute__((aligned(1024))) uint8_t sgrp[T::SGRP];
   const int nq = (int)gridDim.x - big, b = blockIdx.x;
   if (b >= nq)
-    gemm_tile<256, 256, AFMT, SW, OutT>(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, tiles_m, tiles_n, 0, 0, 0, b - nq,
-                                        big, kbuf0, kbuf1, sgrp);
+    gemm_tile<256, 256, AFMT, SW, 2, OutT>(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, tiles_m, tiles_n, 0, 0, 0, b - nq,
+                                        big, kbuf0, kbuf1, nullptr, nullptr, sgrp);
   else
-    gemm_tile<128, 128, AFMT, SW, OutT>(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, tiles_m, tiles_n, big, 1, 1, b, nq,
-                                        kbuf0, kbuf1, sgrp);
+    gemm_tile<128, 128, AFMT, SW, 2, OutT>(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, tiles_m, tiles_n, big, 1, 1, b, nq,
+                                        kbuf0, kbuf1, nullptr, nullptr, sgrp);
 #endif
 }
 
@@ -731,8 +766,18 @@ void tiles(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const
            int64_t ldb, const uint8_t* sb, OutT* c, int64_t ldc, hipStream_t stream) {
   const int bm = (int)((M + 255) / 256), bn = (int)((N + 255) / 256), big = bm * bn;
   const int sm = (int)((M + 127) / 128), sn = (int)((N + 127) / 128), cus = device_cus();
+  // 128 x 128 tiles while they fit on the CUs at two per CU.  At one per CU
+  // nothing else hides a K block's load, so four buffers hold it (us, four /
+  // two: E4M3 x E2M1 256x3584x18944 59 / 88, 1024x3584x3584 15.9 / 20.4; E2M1
+  // pairs 38 / 57, 11.6 / 13.4); a short K is over before that pays
+  // (1000x1024x1024 6.4 / 6.1, 5.8 / 5.2; 512x8960x1536 12.8 / 12.7, 9.6 / 9.8).
+  if (sm * sn <= cus && K >= 1536) {
+    hipLaunchKernelGGL((tile_kernel<128, 128, AFMT, SW, 4, OutT>), dim3(sm * sn), dim3(kTileThreads), 0, stream, (int)M,
+                       (int)N, (int)K, a, lda, sa, b, ldb, sb, c, ldc, sm, sn);
+    return;
+  }
   if (sm * sn <= 2 * cus) {
-    hipLaunchKernelGGL((tile_kernel<128, 128, AFMT, SW, OutT>), dim3(sm * sn), dim3(kTileThreads), 0, stream, (int)M,
+    hipLaunchKernelGGL((tile_kernel<128, 128, AFMT, SW, 2, OutT>), dim3(sm * sn), dim3(kTileThreads), 0, stream, (int)M,
                        (int)N, (int)K, a, lda, sa, b, ldb, sb, c, ldc, sm, sn);
     return;
   }
@@ -741,7 +786,7 @@ void tiles(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const
     hipLaunchKernelGGL((tail_kernel<AFMT, SW, OutT>), dim3(big + 3 * tail), dim3(kTileThreads), 0, stream, (int)M,
                        (int)N, (int)K, a, lda, sa, b, ldb, sb, c, ldc, bm, bn, big - tail);
   else
-    hipLaunchKernelGGL((tile_kernel<256, 256, AFMT, SW, OutT>), dim3(big), dim3(kTileThreads), 0, stream, (int)M,
+    hipLaunchKernelGGL((tile_kernel<256, 256, AFMT, SW, 2, OutT>), dim3(big), dim3(kTileThreads), 0, stream, (int)M,
                        (int)N, (int)K, a, lda, sa, b, ldb, sb, c, ldc, bm, bn);
 }
 
@@ -751,14 +796,14 @@ void gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const 
   // Few rows or tiles.  Up to 16 rows B crosses a CU's load path once however
   // wide it is.  Beyond, the few-row kernel's time goes with M N K, that of
   // the tile kernel with K alone while its tiles fit on the CUs; they meet near
-  // M N = 700000 (us, few rows / tiles, E5M2-or-E4M3 x E2M1: 64x8960x1536
-  // 7.7 / 8.5, 96x8960x1536 10.0 / 8.6, 128x3584x3584 13.6 / 18.3, 256x3584x3584
-  // 25.5 / 19.0, 512x1536x8960 42 / 44; E2M1 pairs: 128x3584x3584 7.7 / 11.3,
-  // 256x3584x3584 14.0 / 12.4).  The few-row kernel takes as many scales as fit
-  // in LDS and 2^26 rows of B (its grid).
+  // M N = 600000 (us, few rows / tiles, E4M3 x E2M1: 64x8960x1536 7.7 / 8.5,
+  // 96x8960x1536 10.0 / 8.6, 256x3584x3584 25.5 / 14.2, 512x1536x8960 42 / 31,
+  // 128x3584x18944 54 / 59; E2M1 pairs: 64x8960x1536 6.9 / 6.2, 256x3584x3584
+  // 14.0 / 10.1, 512x1024x1024 4.8 / 5.1).  The few-row kernel takes as many
+  // scales as fit in LDS and 2^26 rows of B (its grid).
   const int chunks = (int)(K / 128);
   const int64_t n16 = (N + 15) / 16, pairs = ((N + 31) / 32) * ((M + 31) / 32);
-  const bool few = (M <= 16 ? N <= (int64_t(1) << 26) : M * N <= 700000) &&
+  const bool few = (M <= 16 ? N <= (int64_t(1) << 26) : M * N <= 600000) &&
                    few_rows_lds<AFMT, 2, 2, 4, false>(0, (int)K) <= kFewRowsLds;
 #define MXFP4_FEW(MT, NT, WAVES, U)                                                                           \
   (few_rows_lds<AFMT, MT, NT, WAVES, true>((int)(M < 16 * MT ? M : 16 * MT), (int)K) <= kFewRowsLds           \

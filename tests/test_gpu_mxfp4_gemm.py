@@ -200,3 +200,14 @@ def test_graph_and_stream(a_fmt):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, mx.mxfp4_scaled_gemm(a_d, sa_d, a_fmt, b_d, sb_d))
+
+
+@pytest.mark.parametrize("a_fmt", FMTS)
+@pytest.mark.parametrize("K", [1536, 1664, 1792, 1920, 2048, 2176, 2304, 2432])
+def test_long_k_in_few_tiles(K, a_fmt):
+    """Every remainder of the K blocks, in 128 x 128 tiles that leave compute units idle."""
+    M, N = 700, 1000
+    a, sa = operand(M, K, a_fmt, 9, spread=2)
+    b, sb = operand(N, K, mx.E2M1, 10, spread=2)
+    y, t = product(a, sa, a_fmt, b, sb)
+    assert_gemm_close(run(a, sa, a_fmt, b, sb, torch.float32), y, t, False)
