@@ -796,14 +796,15 @@ void gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const 
   // Few rows or tiles.  Up to 16 rows B crosses a CU's load path once however
   // wide it is.  Beyond, the few-row kernel's time goes with M N K, that of
   // the tile kernel with K alone while its tiles fit on the CUs; they meet near
-  // M N = 600000 (us, few rows / tiles, E4M3 x E2M1: 64x8960x1536 7.7 / 8.5,
-  // 96x8960x1536 10.0 / 8.6, 256x3584x3584 25.5 / 14.2, 512x1536x8960 42 / 31,
-  // 128x3584x18944 54 / 59; E2M1 pairs: 64x8960x1536 6.9 / 6.2, 256x3584x3584
-  // 14.0 / 10.1, 512x1024x1024 4.8 / 5.1).  The few-row kernel takes as many
-  // scales as fit in LDS and 2^26 rows of B (its grid).
+  // M N = 480000 (us, few rows / tiles, E4M3 x E2M1: 64x3584x3584 8.5 / 12.1,
+  // 256x1536x8960 30.6 / 30.4, 128x3584x18944 56 / 59, 64x8960x1536 8.7 / 7.6,
+  // 512x1536x8960 45 / 31; E2M1 pairs: 64x3584x3584 6.8 / 9.0, 256x1536x8960
+  // 21.6 / 20.2, 128x3584x3584 9.0 / 9.5, 256x3584x3584 16.0 / 10.2).  The
+  // few-row kernel takes as many scales as fit in LDS and 2^26 rows of B (its
+  // grid).
   const int chunks = (int)(K / 128);
   const int64_t n16 = (N + 15) / 16, pairs = ((N + 31) / 32) * ((M + 31) / 32);
-  const bool few = (M <= 16 ? N <= (int64_t(1) << 26) : M * N <= 600000) &&
+  const bool few = (M <= 16 ? N <= (int64_t(1) << 26) : M * N <= 480000) &&
                    few_rows_lds<AFMT, 2, 2, 4, false>(0, (int)K) <= kFewRowsLds;
 #define MXFP4_FEW(MT, NT, WAVES, U)                                                                           \
   (few_rows_lds<AFMT, MT, NT, WAVES, true>((int)(M < 16 * MT ? M : 16 * MT), (int)K) <= kFewRowsLds           \
@@ -811,17 +812,22 @@ void gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const 
        : few_rows<AFMT, MT, NT, WAVES, U, false>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, stream))
   if (few) {
     if (M <= 16) {
-      // Waves of a workgroup: they cost to start (1 us per 1000), so two where
-      // a run of K is short (1x8960x1536: two 3.5 us, four 4.0; 1x18944x3584:
-      // 8.3 and 8.2).  Where many workgroups would hold much of A each, wider
-      // ones (16x18944x3584, E4M3: 11.2 us against 14.0).
+      // Two waves a workgroup where a run of K is short or the workgroups are
+      // many (E4M3, two / four waves: 1x8960x1536 3.8 / 4.2 us, 1x18944x3584
+      // 8.2 / 8.7; 1x3584x18944 9.1 / 8.8, 8x4096x4096 5.4 / 5.2), unless each
+      // then copies many rows of A (E2M1 pairs, 16x18944x3584: 11.9 / 10.3).
+      // Where many workgroups would hold much of A each, wider ones (E4M3,
+      // 16x18944x3584: 12.8 against 15.6).
       const bool wide_a = M * (AFMT == kE2M1 ? K / 2 : K) > 32 * 1024 && n16 >= 512;
       if (wide_a) MXFP4_FEW(1, 2, 8, 2);
-      else if (chunks <= 16) MXFP4_FEW(1, 1, 2, 4);
+      else if (chunks <= 16 || (n16 >= 512 && M <= 8)) MXFP4_FEW(1, 1, 2, 4);
       else MXFP4_FEW(1, 1, 4, 4);
+    } else if (pairs < 128 && M <= 48) {
+      // Few workgroups of 32 x 32 (us, 16x16, 16x32 and 32x32 ones, E4M3 x
+      // E2M1 and E2M1 pairs: 37x1536x8960 10.8 / 7.7, 11.9 / 8.1, 16.7 / 12.0;
+      // 64x1536x8960 15.7 / 8.6, 12.3 / 8.5, 17.0 / 12.3).
+      MXFP4_FEW(1, 1, 4, 4);
     } else if (pairs < 128) {
-      // Few workgroups of 32 x 32: smaller ones with K over eight waves
-      // (37x1536x8960: 7.5 us against 8.2-11.4, E4M3 10.9 against 12.6-16.0).
       MXFP4_FEW(1, 2, 8, 2);
     } else {
       MXFP4_FEW(2, 2, 4, 4);
