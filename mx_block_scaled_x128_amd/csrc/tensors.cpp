@@ -170,7 +170,7 @@ py::tuple quantize_mxfp4(const at::Tensor& x, int rule, const py::object& stream
 at::Tensor dequantize_mx(const at::Tensor& q, const at::Tensor& s, int fmt, at::ScalarType dtype,
                          const py::object& stream) {
   format(fmt, "fmt", true);
-  const int64_t rows = q.size(0), cols = codes(q, fmt, "q");
+  const int64_t cols = codes(q, fmt, "q"), rows = q.size(0);
   blocks32(cols, "q");
   scales(s, "scales", rows, cols / 32);
   REQUIRE(dtype == at::kFloat || dtype == at::kBFloat16, "dtype must be float32 or bfloat16, got ", dtype);
@@ -199,7 +199,7 @@ py::tuple requantize_mx_t(const at::Tensor& q, const at::Tensor& s, int q_fmt, i
                           const c10::optional<int64_t>& rows_out, const py::object& stream) {
   format(q_fmt, "q_fmt", false);
   format(fmt, "fmt", true);
-  const int64_t rows = q.size(0), cols = codes(q, q_fmt, "q"), out = filled_rows(rows, rows_out);
+  const int64_t cols = codes(q, q_fmt, "q"), rows = q.size(0), out = filled_rows(rows, rows_out);
   blocks32(cols, "q");
   scales(s, "scales", rows, cols / 32);
   const int dev = device_of({&q, &s});
@@ -258,7 +258,7 @@ py::tuple swiglu_mx(const at::Tensor& x, int fmt, int rule, bool keep, const py:
 at::Tensor swiglu_mx_backward(const at::Tensor& k, const at::Tensor& ks, int fmt, const at::Tensor& dh,
                               const py::object& stream) {
   format(fmt, "kept.fmt", false);
-  const int64_t rows = k.size(0), wide = codes(k, fmt, "kept.codes");
+  const int64_t wide = codes(k, fmt, "kept.codes"), rows = k.size(0);
   REQUIRE(wide % 64 == 0, "kept.codes must have twice a multiple of 32 columns, got ", wide);
   scales(ks, "kept.scales", rows, wide / 32);
   real_matrix(dh, "dh");
@@ -295,7 +295,7 @@ py::tuple rmsnorm_mx(const at::Tensor& x, const at::Tensor& w, double eps, int f
 py::tuple rmsnorm_mx_backward(const at::Tensor& k, const at::Tensor& ks, const at::Tensor& r, int fmt,
                               const at::Tensor& w, const at::Tensor& dy, const py::object& stream) {
   format(fmt, "kept.fmt", false);
-  const int64_t rows = k.size(0), cols = codes(k, fmt, "kept.codes");
+  const int64_t cols = codes(k, fmt, "kept.codes"), rows = k.size(0);
   blocks32(cols, "kept.codes");
   scales(ks, "kept.scales", rows, cols / 32);
   vector(r, "kept.rstd", rows);

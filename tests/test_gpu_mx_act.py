@@ -184,3 +184,28 @@ def test_other_stream():
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(y, want[0]) and torch.equal(ys, want[1])
     assert torch.equal(dx, want_b[0]) and torch.equal(dw, want_b[1])
+
+
+def test_past_four_gib():
+    """Offsets beyond 32 bits in every tensor: 4.6 GB of x, of dx and of what is kept, and the last
+    rows against a call on them alone."""
+    rows, cols = 70400, 16384
+    x = torch.zeros((rows, 2 * cols), dtype=torch.bfloat16, device="cuda")
+    dh = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    tail_x, tail_d = tensor(given((16, 2 * cols), 2.0, 1, "bf16"), "bf16"), tensor(given((16, cols), 1.0, 2, "bf16"), "bf16")
+    x[-16:], dh[-16:] = tail_x, tail_d
+    h, hs, kept = mx.swiglu_mx(x)
+    want = mx.swiglu_mx(tail_x)
+    assert torch.equal(h[-16:], want[0]) and torch.equal(hs[-16:], want[1])
+    assert torch.equal(kept.codes[-16:], want[2].codes) and not kept.codes[:-16].any()
+    dx = mx.swiglu_mx_backward(kept, dh)
+    assert torch.equal(dx[-16:], mx.swiglu_mx_backward(want[2], tail_d)) and not dx[:-16].any()
+    del h, hs, kept, dx, dh
+    w = torch.rand(2 * cols, device="cuda")
+    y, ys, kept = mx.rmsnorm_mx(x, w, 1e-6)
+    want = mx.rmsnorm_mx(tail_x, w, 1e-6)
+    assert torch.equal(y[-16:], want[0]) and torch.equal(kept.rstd[-16:], want[2].rstd)
+    dx, dw = mx.rmsnorm_mx_backward(kept, w, x)
+    want_dx, want_dw = mx.rmsnorm_mx_backward(want[2], w, tail_x)
+    assert torch.equal(dx[-16:], want_dx)
+    assert torch.allclose(dw, want_dw, rtol=1e-5, atol=1e-4)  # another order of the same 16 rows' sum

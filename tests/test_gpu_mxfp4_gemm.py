@@ -211,3 +211,17 @@ def test_long_k_in_few_tiles(K, a_fmt):
     b, sb = operand(N, K, mx.E2M1, 10, spread=2)
     y, t = product(a, sa, a_fmt, b, sb)
     assert_gemm_close(run(a, sa, a_fmt, b, sb, torch.float32), y, t, False)
+
+
+def test_output_past_four_gib():
+    """C of 4.6 GB: its last rows and columns against fp64."""
+    M, N, K = 70000, 33000, 256
+    a, sa = operand(64, K, mx.E4M3, 11, spread=1)
+    b, sb = operand(N, K, mx.E2M1, 12, spread=1)
+    a_d = torch.zeros((M, K), dtype=torch.uint8, device="cuda")
+    sa_d = torch.full((M, K // 32), 127, dtype=torch.uint8, device="cuda")
+    a_d[-64:], sa_d[-64:] = dev(a), dev(sa)
+    out = mx.mxfp4_scaled_gemm(a_d, sa_d, mx.E4M3, dev(b), dev(sb), out_dtype=torch.bfloat16)
+    y, t = product(a, sa, mx.E4M3, b, sb)
+    assert_gemm_close(host(out[-64:]), y, t, True)
+    assert not out[:-64].any()
