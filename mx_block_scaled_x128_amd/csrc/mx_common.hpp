@@ -43,13 +43,16 @@ template <> struct MxFmt<kE2M1> {
 // clamped to [-127, 127], which a subnormal amax reaches at the low end; the
 // byte is e + 127.  fmax = (1 + frac_max / 2^23) * 2^q, so under the ceil rule
 // the exponent field grows by one exactly when the fraction passes frac_max,
-// that is when adding 0x7FFFFF - frac_max carries into it.  255 for a block
-// with an infinity or a NaN.
+// that is when adding 0x7FFFFF - frac_max carries into it.
+template <int FMT, bool CEIL>
+__device__ __forceinline__ uint32_t mx_scale_finite(uint32_t amax_bits) {
+  const uint32_t field = (amax_bits + (CEIL ? 0x7FFFFFu - MxFmt<FMT>::frac_max : 0u)) >> 23;
+  return __builtin_elementwise_sub_sat(field, (uint32_t)MxFmt<FMT>::q);
+}
+// The same, and 255 for a block with an infinity or a NaN.
 template <int FMT, bool CEIL>
 __device__ __forceinline__ uint32_t mx_scale(uint32_t amax_bits) {
-  const uint32_t field = (amax_bits + (CEIL ? 0x7FFFFFu - MxFmt<FMT>::frac_max : 0u)) >> 23;
-  const uint32_t byte = __builtin_elementwise_sub_sat(field, (uint32_t)MxFmt<FMT>::q);
-  return amax_bits < kInfBits ? byte : 255u;
+  return amax_bits < kInfBits ? mx_scale_finite<FMT, CEIL>(amax_bits) : 255u;
 }
 
 // Codes of values under scale byte `byte` (not 255): cast(x * 2^-e), to

@@ -9,6 +9,8 @@
 // For a block with largest magnitude amax, e its exponent (mx_scale):
 //   scale byte = e + 127,  code = cast(x * 2^-e), to nearest even, saturating.
 // All four move each byte once; HBM bounds them.
+#include <type_traits>
+
 #include "mx_common.hpp"
 #include "mx_launch.hpp"
 
@@ -170,54 +172,72 @@ __global__ __launch_bounds__(kTThreads<SRC>) void mx_transpose_kernel(
   const uint32_t bx = t / gy, by = t - bx * gy;
   const uint32_t c0 = bx * kTile, t0 = by * kTile;
   const bool cact = c0 + tc * CH < cols;
-  float f[4][CH];
-  if constexpr (SRC < 2) {
-    typedef typename Source<SRC>::T T;
-    MxRaw<T> raw[4];
+  // The four tokens as read; eight channels at a time are converted.
+  typedef typename Source<SRC>::T T;
+  typename std::conditional<SRC < 2, MxRaw<T>, nt_u32x4>::type raw[4];
+  float factor[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t r = t0 + tr * 4 + i;
-      if (cact && r < rows) mx_load_raw<NT>(static_cast<const T*>(x) + (int64_t)r * ldx + c0 + tc * 8, raw[i]);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t r = t0 + tr * 4 + i;
+    const bool in = cact && r < rows;
+    if constexpr (SRC < 2) {
+      if (in) mx_load_raw<NT>(static_cast<const T*>(x) + (int64_t)r * ldx + c0 + tc * CH, raw[i]);
       else mx_zero_raw(raw[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) mx_unpack(raw[i], f[i]);
-  } else {
-    nt_u32x4 word[4];
-    uint32_t b[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t r = t0 + tr * 4 + i;
-      word[i] = nt_u32x4{0, 0, 0, 0};
-      b[i] = 0;
-      if (cact && r < rows) {
-        word[i] = *reinterpret_cast<const nt_u32x4*>(static_cast<const uint8_t*>(x) + (int64_t)r * ldx + c0 + tc * 16);
-        b[i] = s[(int64_t)r * (cols >> 5) + ((c0 + tc * 16) >> 5)];
+    } else {
+      raw[i] = nt_u32x4{0, 0, 0, 0};
+      uint32_t b = 0;
+      if (in) {
+        raw[i] = *reinterpret_cast<const nt_u32x4*>(static_cast<const uint8_t*>(x) + (int64_t)r * ldx + c0 + tc * CH);
+        b = s[(int64_t)r * (cols >> 5) + ((c0 + tc * CH) >> 5)];
       }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      constexpr int QF = SRC < 2 ? 0 : SRC - 2;
-      const float factor = mx_factor(b[i]);
-      float lo[8], hi[8];
-      mx_decode8<QF>(make_uint2(word[i].x, word[i].y), factor, lo);
-      mx_decode8<QF>(make_uint2(word[i].z, word[i].w), factor, hi);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        f[i][j] = lo[j];
-        f[i][CH - 8 + j] = hi[j];
-      }
+      factor[i] = mx_factor(b);
     }
   }
 #pragma unroll
-  for (int j = 0; j < CH; ++j) {
-    const uint32_t m = max_oct(max(max(abs_bits(f[0][j]), abs_bits(f[1][j])), max(abs_bits(f[2][j]), abs_bits(f[3][j]))));
-    const uint32_t sc = mx_scale<FMT, CEIL>(m);
-    uint32_t o = mx_codes4<FMT, CEIL>(f[0][j], f[1][j], f[2][j], f[3][j], sc);
-    if (sc == 255u) o = 0;
-    if constexpr (FMT == kE2M1) *reinterpret_cast<uint16_t*>(tile + (tc * CH + j) * PITCH + tr * 2) = (uint16_t)o;
-    else *reinterpret_cast<uint32_t*>(tile + (tc * CH + j) * PITCH + tr * 4) = o;
-    if ((lane & 7) == 0) stile[(tc * CH + j) * 4 + (w & 3)] = (uint8_t)sc;
+  for (int part = 0; part < CH / 8; ++part) {
+    float f[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (SRC < 2) {
+        mx_unpack(raw[i], f[i]);
+      } else {
+        const uint2 w8 = part == 0 ? make_uint2(raw[i].x, raw[i].y) : make_uint2(raw[i].z, raw[i].w);
+        mx_decode8<(SRC < 2 ? 0 : SRC - 2)>(w8, factor[i], f[i]);
+      }
+    }
+    uint32_t sc[8], top = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t m = max_oct(max(max(abs_bits(f[0][j]), abs_bits(f[1][j])), max(abs_bits(f[2][j]), abs_bits(f[3][j]))));
+      sc[j] = mx_scale_finite<FMT, CEIL>(m);
+      top = max(top, m);
+    }
+    const uint32_t ch = tc * CH + part * 8;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t o = mx_codes4<FMT, CEIL>(f[0][j], f[1][j], f[2][j], f[3][j], sc[j]);
+      if constexpr (FMT == kE2M1) *reinterpret_cast<uint16_t*>(tile + (ch + j) * PITCH + tr * 2) = (uint16_t)o;
+      else *reinterpret_cast<uint32_t*>(tile + (ch + j) * PITCH + tr * 4) = o;
+    }
+    // Channels with an infinity or a NaN, once more (rare: one test for eight).
+    if (top >= kInfBits) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max(m, abs_bits(f[i][j]));
+        m = max_oct(m);  // the same in the eight lanes of the block, which all are here
+        if (m < kInfBits) continue;
+        sc[j] = 255u;
+        if constexpr (FMT == kE2M1) *reinterpret_cast<uint16_t*>(tile + (ch + j) * PITCH + tr * 2) = 0;
+        else *reinterpret_cast<uint32_t*>(tile + (ch + j) * PITCH + tr * 4) = 0;
+      }
+    }
+    if ((lane & 7) == 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) stile[(ch + j) * 4 + (w & 3)] = (uint8_t)sc[j];
+    }
+    __builtin_amdgcn_sched_barrier(0);
   }
   __syncthreads();
   constexpr int CPR = RB / 16;  // 16-byte chunks per tile row

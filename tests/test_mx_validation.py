@@ -207,3 +207,19 @@ def test_reference_gradients_against_differences():
         e = np.zeros(32)
         e[k] = 1e-6
         assert np.allclose(((y(x, w + e) - y(x, w - e)) * dy).sum() / 2e-6, dw[k], rtol=1e-6, atol=1e-8)
+
+
+def test_tensor_functions_fail_loudly_without_the_extension(monkeypatch):
+    import importlib
+
+    def missing(name, *a):
+        raise ImportError("no module named " + name)
+    monkeypatch.setattr(mx, "_tensors", None)
+    monkeypatch.setattr(importlib, "import_module", missing)
+    with pytest.raises(ImportError, match="_tensors is not built"):
+        mx.quantize_mxfp4(torch.zeros(1, 32))
+
+
+def test_library_errors_name_their_call():
+    with pytest.raises(mx.MxFp8Error, match="mx_rmsnorm_forward"):
+        mx._check(2, "mx_rmsnorm_forward")
