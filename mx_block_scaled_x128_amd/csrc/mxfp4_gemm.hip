@@ -797,18 +797,21 @@ template <int AFMT>
 void gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const uint8_t* sa, const uint8_t* b,
           int64_t ldb, const uint8_t* sb, void* c, int64_t ldc, int c_dtype, hipStream_t stream) {
   // Few rows or tiles.  Up to 16 rows B crosses a CU's load path once however
-  // wide it is.  Beyond, the few-row kernel's time goes with M N K, that of
-  // the tile kernel with K alone while its tiles fit on the CUs; they meet near
-  // M N = 480000 (us, few rows / tiles, E4M3 x E2M1: 64x3584x3584 8.5 / 12.1,
-  // 256x1536x8960 30.6 / 30.4, 128x3584x18944 56 / 59, 64x8960x1536 8.7 / 7.6,
-  // 512x1536x8960 45 / 31; E2M1 pairs: 64x3584x3584 6.8 / 9.0, 256x1536x8960
-  // 21.6 / 20.2, 128x3584x3584 9.0 / 9.5, 256x3584x3584 16.0 / 10.2).  The
-  // few-row kernel takes as many scales as fit in LDS and 2^26 rows of B (its
-  // grid).
+  // wide it is.  Beyond, the few-row kernel is the faster one while its
+  // workgroups all fit on the chip, one to a CU, since it has four times or
+  // more as many of them as there are tiles; with a second round of them the
+  // tiles win (us, few rows / tiles, E4M3 x E2M1 and E2M1 pairs, one round:
+  // 64x3584x8960 17.2 / 26.7, 12.6 / 18.8; 128x3584x3584 8.8 / 13.4, 7.8 / 9.5;
+  // 512x1024x1024 5.5 / 6.1, 4.9 / 5.2; 32x14336x4096 12.2 / 14.1, 10.0 / 10.4;
+  // more: 40x16384x3584 17 / 13, 12.1 / 10.0; 256x3584x3584 19.2 / 14.2,
+  // 15.7 / 10.3; 1024x1024x1024 9.1 / 6.2, 8.4 / 5.3).  The few-row kernel
+  // takes as many scales as fit in LDS and 2^26 rows of B (its grid).
   const int chunks = (int)(K / 128);
   const int64_t n16 = (N + 15) / 16, pairs = ((N + 31) / 32) * ((M + 31) / 32);
-  const bool few = (M <= 16 ? N <= (int64_t(1) << 26) : M * N <= 480000) &&
-                   few_rows_lds<AFMT, 2, 2, 4, false>(0, (int)K) <= kFewRowsLds;
+  const int64_t wide = ((N + 63) / 64) * ((M + 31) / 32), cus = device_cus();
+  const bool few = (M <= 16 ? N <= (int64_t(1) << 26) : wide <= cus) &&
+                   (M <= 16 || pairs <= cus ? few_rows_lds<AFMT, 2, 2, 4, false>(0, (int)K)
+                                            : few_rows_lds<AFMT, 2, 4, 4, false>(0, (int)K)) <= kFewRowsLds;
 #define MXFP4_FEW(MT, NT, WAVES, U)                                                                           \
   (few_rows_lds<AFMT, MT, NT, WAVES, true>((int)(M < 16 * MT ? M : 16 * MT), (int)K) <= kFewRowsLds           \
        ? few_rows<AFMT, MT, NT, WAVES, U, true>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, stream)     \
@@ -832,8 +835,13 @@ void gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const 
       MXFP4_FEW(1, 1, 4, 4);
     } else if (pairs < 128) {
       MXFP4_FEW(1, 2, 8, 2);
-    } else {
+    } else if (pairs <= cus) {
       MXFP4_FEW(2, 2, 4, 4);
+    } else {
+      // 32 x 64 ones where those of 32 x 32 would take a second round (us,
+      // 32x64 / 32x32: 128x3584x3584 8.8 / 15.5, 7.8 / 8.9; 256x1536x18944 37 /
+      // 55, 29 / 37).
+      MXFP4_FEW(2, 4, 4, 1);
     }
   } else {
     const bool sw = K % 512 == 0 && (((uintptr_t)sa | (uintptr_t)sb) & 15) == 0;

@@ -225,3 +225,26 @@ def test_output_past_four_gib():
     y, t = product(a, sa, mx.E4M3, b, sb)
     assert_gemm_close(host(out[-64:]), y, t, True)
     assert not out[:-64].any()
+
+
+@pytest.mark.parametrize("a_fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [(17, 8300, 128), (40, 7900, 256), (128, 3584, 384), (257, 1000, 640), (513, 900, 1920),
+                                   (250, 1100, 4864)])
+def test_one_round_of_wide_few_row_workgroups(M, N, K, a_fmt):
+    """More 32 x 32 blocks of C than compute units, fewer 32 x 64 ones: with A in LDS and without, runs of K shorter
+    than the waves are many, ragged edges."""
+    a, sa = operand(M, K, a_fmt, 13, spread=2)
+    b, sb = operand(N, K, mx.E2M1, 14, spread=2)
+    y, t = product(a, sa, a_fmt, b, sb)
+    first = run(a, sa, a_fmt, b, sb, torch.float32, pad=16)
+    assert_gemm_close(first, y, t, False)
+    assert_gemm_close(run(a, sa, a_fmt, b, sb, torch.bfloat16), y, t, True)
+    assert np.array_equal(run(a, sa, a_fmt, b, sb, torch.float32, pad=16), first)
+
+
+@pytest.mark.parametrize("K", [51200, 51328])
+def test_scales_that_just_fill_lds_and_that_do_not(K):
+    a, sa = operand(257, K, mx.E2M1, 15, spread=1)
+    b, sb = operand(900, K, mx.E2M1, 16, spread=1)
+    y, t = product(a, sa, mx.E2M1, b, sb)
+    assert_gemm_close(run(a, sa, mx.E2M1, b, sb, torch.float32), y, t, False)
