@@ -248,7 +248,7 @@ __global__ __launch_bounds__(kTThreads<SRC>) void mx_transpose_kernel(
     if (c0 + ch < cols && t0 + ck * (kTile / CPR) < rows_out) {
       const uint2 a = *reinterpret_cast<const uint2*>(tile + ch * PITCH + ck * 16);
       const uint2 b = *reinterpret_cast<const uint2*>(tile + ch * PITCH + ck * 16 + 8);
-      store_codes(qt + (int64_t)(c0 + ch) * ldqt + t0 * RB / kTile + ck * 16, make_uint4(a.x, a.y, b.x, b.y));
+      store_codes(qt + (int64_t)(c0 + ch) * ldqt + ((int64_t)by * RB + ck * 16), make_uint4(a.x, a.y, b.x, b.y));
     }
   }
   const uint32_t ngt = rows_out >> 5;

@@ -196,3 +196,30 @@ def test_past_four_gib():
     out = (rows + 127) // 128 * 128
     ref_q, ref_s = mxref.quantize_t(tail.astype(np.float64), mxref.E4M3, mxref.CEIL, 64 + out - rows)
     same(q[:, rows - 64:], s[:, (rows - 64) // 32:], ref_q, ref_s)
+
+
+@pytest.mark.parametrize("source", ["bf16", "codes"])
+@pytest.mark.parametrize("fmt,rows,cols", [(mx.E4M3, 2 ** 25 + 160, 32), (mx.E5M2, 2 ** 25 + 160, 32),
+                                           (mx.E2M1, 2 ** 26 + 160, 32)])
+def test_transposed_token_offsets_past_32_bits(fmt, rows, cols, source):
+    """More tokens than a 32-bit token * tile-bytes product holds (2^25 for FP8 codes, 2^26 for E2M1): the first
+    and the last tokens, which differ, against the plain form, and nothing but zeros between them."""
+    first, last = values(128, cols, 21, "bf16"), values(160, cols, 22, "bf16")
+    out = (rows + 127) // 128 * 128
+    if source == "bf16":
+        x = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+        x[:128], x[-160:] = to_dev(first, "bf16"), to_dev(last, "bf16")
+        q, s = mx.quantize_mx_t(x, fmt)
+        f64, l64 = first.astype(np.float64), last.astype(np.float64)
+    else:
+        x = torch.zeros((rows, cols), dtype=torch.uint8, device="cuda")
+        xs = torch.zeros((rows, cols // 32), dtype=torch.uint8, device="cuda")
+        (fq, fs), (lq, ls) = (mxref.quantize(v.astype(np.float64), mxref.E4M3, mxref.CEIL) for v in (first, last))
+        x[:128], x[-160:], xs[:128], xs[-160:] = dev(fq), dev(lq), dev(fs), dev(ls)
+        q, s = mx.requantize_mx_t(x, xs, mx.E4M3, fmt)
+        f64, l64 = mxref.dequantize(fq, fs, mxref.E4M3), mxref.dequantize(lq, ls, mxref.E4M3)
+    tail = 160 + out - rows
+    per = 2 if fmt == mx.E2M1 else 1  # tokens a byte
+    same(q[:, :128 // per], s[:, :4], *mxref.quantize_t(f64, fmt, mxref.CEIL, 128))
+    same(q[:, (out - tail) // per:], s[:, (out - tail) // 32:], *mxref.quantize_t(l64, fmt, mxref.CEIL, tail))
+    assert not q[:, 128 // per:(out - tail) // per].any() and not s[:, 4:(out - tail) // 32].any()
