@@ -604,7 +604,9 @@ def gaussws(w, bitwidths, seed, stream_id=0, out=None, stream=None):
 # csrc/tensors.cpp next to the library): the same in Python takes longer than
 # the small kernels.  ValueError for a tensor that does not fit, before any
 # call.  E2M1 codes are uint8 tensors with two elements to a byte:
-# [rows][cols / 2].
+# [rows][cols / 2].  With stream=, a call works as inside
+# torch.cuda.stream(stream): what it allocates is that stream's memory; what it
+# returns is marked as in use on the caller's current stream, too.
 
 SwigluKept = collections.namedtuple("SwigluKept", "codes scales fmt")
 SwigluKept.__doc__ = "What swiglu_mx keeps of its input: codes [rows][2 cols], scales [rows][2 cols / 32], their format."

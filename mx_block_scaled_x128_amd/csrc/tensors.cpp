@@ -5,6 +5,7 @@
 // Nothing computes here, and the C functions are those of the library that
 // mx_block_scaled_x128_amd loads (bind).
 #include <ATen/ATen.h>
+#include <c10/core/StreamGuard.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <dlfcn.h>
@@ -131,22 +132,51 @@ int device_of(std::initializer_list<const at::Tensor*> all) {
   REQUIRE(dev == cur, "tensors are on cuda:", dev, " but the current device is cuda:", cur);
   return dev;
 }
-void* stream_of(const py::object& stream, int dev) {
-  if (stream.is_none()) return c10::hip::getCurrentHIPStream(dev).stream();
-  const int i = stream.attr("device").attr("index").cast<int>();
-  REQUIRE(i == dev, "stream is on cuda:", i, " but the tensors are on cuda:", dev);
-  return reinterpret_cast<void*>(stream.attr("cuda_stream").cast<uintptr_t>());
-}
+// Where a call works: the given stream, or the current one.  A given stream is
+// the current one while this lives, so what the call allocates comes from its
+// memory: a block freed on another stream may still be in use there, and work
+// on the given one would not wait for that.
+class Place {
+ public:
+  Place(const py::object& stream, int dev) : dev_(dev) {
+    if (stream.is_none()) {
+      raw_ = c10::hip::getCurrentHIPStream(dev).stream();
+      return;
+    }
+    const int i = stream.attr("device").attr("index").cast<int>();
+    REQUIRE(i == dev, "stream is on cuda:", i, " but the tensors are on cuda:", dev);
+    const c10::Stream given = c10::Stream::unpack3(stream.attr("stream_id").cast<int64_t>(), (c10::DeviceIndex)dev,
+                                                   at::kCUDA);
+    raw_ = reinterpret_cast<void*>(stream.attr("cuda_stream").cast<uintptr_t>());
+    guard_.reset_stream(given);
+    if (*guard_.original_stream() != given) caller_ = guard_.original_stream();
+  }
+  void* stream() const { return raw_; }
+  // Uninitialized; for the length of the call.
+  at::Tensor scratch(at::IntArrayRef size, at::ScalarType type) const {
+    return at::empty(size, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, (c10::DeviceIndex)dev_)));
+  }
+  // Uninitialized; returned to the caller, whose current stream may read it
+  // until it is freed.
+  at::Tensor fresh(at::IntArrayRef size, at::ScalarType type) const {
+    at::Tensor t = scratch(size, type);
+    if (caller_) t.record_stream(*caller_);
+    return t;
+  }
+  // The same, [rows][cols] with rows of a multiple of 16 elements.
+  at::Tensor pitched(int64_t rows, int64_t cols, at::ScalarType type) const {
+    const int64_t pitch = std::max<int64_t>((cols + 15) / 16 * 16, 16);
+    at::Tensor t = fresh({rows, pitch}, type);
+    return pitch == cols ? t : t.narrow(1, 0, cols);
+  }
 
-at::Tensor fresh(at::IntArrayRef size, at::ScalarType type, int dev) {
-  return at::empty(size, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, (c10::DeviceIndex)dev)));
-}
-// Uninitialized [rows][cols] with rows of a multiple of 16 elements.
-at::Tensor pitched(int64_t rows, int64_t cols, at::ScalarType type, int dev) {
-  const int64_t pitch = std::max<int64_t>((cols + 15) / 16 * 16, 16);
-  at::Tensor t = fresh({rows, pitch}, type, dev);
-  return pitch == cols ? t : t.narrow(1, 0, cols);
-}
+ private:
+  int dev_;
+  void* raw_;
+  c10::OptionalStreamGuard guard_;
+  c10::optional<c10::Stream> caller_;
+};
+
 int64_t filled_rows(int64_t rows, const c10::optional<int64_t>& rows_out) {
   if (!rows_out.has_value()) return (rows + 127) / 128 * 128;
   REQUIRE(*rows_out % 32 == 0 && *rows_out >= rows, "rows_out must be a multiple of 32 and at least ", rows, ", got ",
@@ -160,10 +190,10 @@ py::tuple quantize_mxfp4(const at::Tensor& x, int rule, const py::object& stream
   real_matrix(x, "x");
   const int64_t rows = x.size(0), cols = x.size(1);
   blocks32(cols, "x");
-  const int dev = device_of({&x});
-  at::Tensor q = pitched(rows, cols / 2, at::kByte, dev), s = fresh({rows, cols / 32}, at::kByte, dev);
+  const Place on(stream, device_of({&x}));
+  at::Tensor q = on.pitched(rows, cols / 2, at::kByte), s = on.fresh({rows, cols / 32}, at::kByte);
   status(lib.mxfp4_quantize(ptr(x), real_type(x), rows, cols, ld(x), rule, bytes(q), ld(q), bytes(s),
-                            stream_of(stream, dev)), "mxfp4_quantize");
+                            on.stream()), "mxfp4_quantize");
   return py::make_tuple(q, s);
 }
 
@@ -174,10 +204,10 @@ at::Tensor dequantize_mx(const at::Tensor& q, const at::Tensor& s, int fmt, at::
   blocks32(cols, "q");
   scales(s, "scales", rows, cols / 32);
   REQUIRE(dtype == at::kFloat || dtype == at::kBFloat16, "dtype must be float32 or bfloat16, got ", dtype);
-  const int dev = device_of({&q, &s});
-  at::Tensor y = fresh({rows, cols}, dtype, dev);
+  const Place on(stream, device_of({&q, &s}));
+  at::Tensor y = on.fresh({rows, cols}, dtype);
   status(lib.mx_dequantize(bytes(q), ld(q), fmt, bytes(s), rows, cols, ptr(y), real_type(y), ld(y),
-                           stream_of(stream, dev)), "mx_dequantize");
+                           on.stream()), "mx_dequantize");
   return y;
 }
 
@@ -187,11 +217,11 @@ py::tuple quantize_mx_t(const at::Tensor& x, int fmt, int rule, const c10::optio
   real_matrix(x, "x");
   const int64_t rows = x.size(0), cols = x.size(1), out = filled_rows(rows, rows_out);
   REQUIRE(cols % 16 == 0, "x must have a multiple of 16 columns, got ", cols);
-  const int dev = device_of({&x});
-  at::Tensor qt = pitched(cols, fmt == MXFP8_E2M1 ? out / 2 : out, at::kByte, dev);
-  at::Tensor st = fresh({cols, out / 32}, at::kByte, dev);
+  const Place on(stream, device_of({&x}));
+  at::Tensor qt = on.pitched(cols, fmt == MXFP8_E2M1 ? out / 2 : out, at::kByte);
+  at::Tensor st = on.fresh({cols, out / 32}, at::kByte);
   status(lib.mx_quantize_t(ptr(x), real_type(x), rows, cols, ld(x), fmt, rule, bytes(qt), ld(qt), out, bytes(st),
-                           stream_of(stream, dev)), "mx_quantize_t");
+                           on.stream()), "mx_quantize_t");
   return py::make_tuple(qt, st);
 }
 
@@ -202,11 +232,11 @@ py::tuple requantize_mx_t(const at::Tensor& q, const at::Tensor& s, int q_fmt, i
   const int64_t cols = codes(q, q_fmt, "q"), rows = q.size(0), out = filled_rows(rows, rows_out);
   blocks32(cols, "q");
   scales(s, "scales", rows, cols / 32);
-  const int dev = device_of({&q, &s});
-  at::Tensor qt = pitched(cols, fmt == MXFP8_E2M1 ? out / 2 : out, at::kByte, dev);
-  at::Tensor st = fresh({cols, out / 32}, at::kByte, dev);
+  const Place on(stream, device_of({&q, &s}));
+  at::Tensor qt = on.pitched(cols, fmt == MXFP8_E2M1 ? out / 2 : out, at::kByte);
+  at::Tensor st = on.fresh({cols, out / 32}, at::kByte);
   status(lib.mx_requantize_t(bytes(q), ld(q), q_fmt, bytes(s), rows, cols, fmt, rule, bytes(qt), ld(qt), out,
-                             bytes(st), stream_of(stream, dev)), "mx_requantize_t");
+                             bytes(st), on.stream()), "mx_requantize_t");
   return py::make_tuple(qt, st);
 }
 
@@ -219,21 +249,17 @@ at::Tensor mxfp4_scaled_gemm(const at::Tensor& a, const at::Tensor& sa, int a_fm
   REQUIRE(K % 128 == 0, "mxfp4_scaled_gemm: K must be a multiple of 128, got ", K);
   scales(sa, "a_scales", M, K / 32);
   scales(sb, "b_scales", N, K / 32);
-  at::Tensor c;
-  int dev;
   if (out.has_value()) {
-    c = *out;
-    real_matrix(c, "out");
-    shape(c, "out", M, N);
-    dev = device_of({&a, &sa, &b, &sb, &c});
-  } else {
-    const at::ScalarType type = out_dtype.value_or(at::kFloat);
-    REQUIRE(type == at::kFloat || type == at::kBFloat16, "out_dtype must be float32 or bfloat16, got ", type);
-    dev = device_of({&a, &sa, &b, &sb});
-    c = pitched(M, N, type, dev);
+    real_matrix(*out, "out");
+    shape(*out, "out", M, N);
   }
+  const at::ScalarType type = out_dtype.value_or(at::kFloat);
+  REQUIRE(out.has_value() || type == at::kFloat || type == at::kBFloat16,
+          "out_dtype must be float32 or bfloat16, got ", type);
+  const Place on(stream, out.has_value() ? device_of({&a, &sa, &b, &sb, &*out}) : device_of({&a, &sa, &b, &sb}));
+  at::Tensor c = out.has_value() ? *out : on.pitched(M, N, type);
   status(lib.mxfp4_gemm(M, N, K, bytes(a), ld(a), a_fmt, bytes(sa), bytes(b), ld(b), bytes(sb), ptr(c), ld(c),
-                        real_type(c), stream_of(stream, dev)), "mxfp4_gemm");
+                        real_type(c), on.stream()), "mxfp4_gemm");
   return c;
 }
 
@@ -242,14 +268,14 @@ py::tuple swiglu_mx(const at::Tensor& x, int fmt, int rule, bool keep, const py:
   real_matrix(x, "x");
   const int64_t rows = x.size(0), wide = x.size(1), cols = wide / 2;
   REQUIRE(wide % 64 == 0, "x must have twice a multiple of 32 columns, got ", wide);
-  const int dev = device_of({&x});
-  at::Tensor h = fresh({rows, cols}, at::kByte, dev), hs = fresh({rows, cols / 32}, at::kByte, dev), k, ks;
+  const Place on(stream, device_of({&x}));
+  at::Tensor h = on.fresh({rows, cols}, at::kByte), hs = on.fresh({rows, cols / 32}, at::kByte), k, ks;
   if (keep) {
-    k = fresh({rows, wide}, at::kByte, dev);
-    ks = fresh({rows, wide / 32}, at::kByte, dev);
+    k = on.fresh({rows, wide}, at::kByte);
+    ks = on.fresh({rows, wide / 32}, at::kByte);
   }
   status(lib.mx_swiglu_forward(ptr(x), real_type(x), rows, cols, ld(x), fmt, rule, bytes(h), cols, bytes(hs),
-                               keep ? bytes(k) : nullptr, wide, keep ? bytes(ks) : nullptr, stream_of(stream, dev)),
+                               keep ? bytes(k) : nullptr, wide, keep ? bytes(ks) : nullptr, on.stream()),
          "mx_swiglu_forward");
   if (!keep) return py::make_tuple(h, hs);
   return py::make_tuple(h, hs, k, ks);
@@ -263,10 +289,10 @@ at::Tensor swiglu_mx_backward(const at::Tensor& k, const at::Tensor& ks, int fmt
   scales(ks, "kept.scales", rows, wide / 32);
   real_matrix(dh, "dh");
   shape(dh, "dh", rows, wide / 2);
-  const int dev = device_of({&k, &ks, &dh});
-  at::Tensor dx = fresh({rows, wide}, dh.scalar_type(), dev);
+  const Place on(stream, device_of({&k, &ks, &dh}));
+  at::Tensor dx = on.fresh({rows, wide}, dh.scalar_type());
   status(lib.mx_swiglu_backward(bytes(k), ld(k), bytes(ks), fmt, ptr(dh), real_type(dh), ld(dh), rows, wide / 2,
-                                ptr(dx), wide, stream_of(stream, dev)), "mx_swiglu_backward");
+                                ptr(dx), wide, on.stream()), "mx_swiglu_backward");
   return dx;
 }
 
@@ -277,17 +303,17 @@ py::tuple rmsnorm_mx(const at::Tensor& x, const at::Tensor& w, double eps, int f
   const int64_t rows = x.size(0), cols = x.size(1);
   blocks32(cols, "x");
   vector(w, "w", cols);
-  const int dev = device_of({&x, &w});
-  at::Tensor y = fresh({rows, cols}, at::kByte, dev), ys = fresh({rows, cols / 32}, at::kByte, dev), k, ks, r;
+  const Place on(stream, device_of({&x, &w}));
+  at::Tensor y = on.fresh({rows, cols}, at::kByte), ys = on.fresh({rows, cols / 32}, at::kByte), k, ks, r;
   if (keep) {
-    k = fresh({rows, cols}, at::kByte, dev);
-    ks = fresh({rows, cols / 32}, at::kByte, dev);
-    r = fresh({rows}, at::kFloat, dev);
+    k = on.fresh({rows, cols}, at::kByte);
+    ks = on.fresh({rows, cols / 32}, at::kByte);
+    r = on.fresh({rows}, at::kFloat);
   }
   status(lib.mx_rmsnorm_forward(ptr(x), real_type(x), rows, cols, ld(x), static_cast<float*>(ptr(w)), (float)eps, fmt,
                                 rule, bytes(y), cols, bytes(ys), keep ? bytes(k) : nullptr, cols,
                                 keep ? bytes(ks) : nullptr, keep ? static_cast<float*>(ptr(r)) : nullptr,
-                                stream_of(stream, dev)), "mx_rmsnorm_forward");
+                                on.stream()), "mx_rmsnorm_forward");
   if (!keep) return py::make_tuple(y, ys);
   return py::make_tuple(y, ys, k, ks, r);
 }
@@ -302,14 +328,12 @@ py::tuple rmsnorm_mx_backward(const at::Tensor& k, const at::Tensor& ks, const a
   vector(w, "w", cols);
   real_matrix(dy, "dy");
   shape(dy, "dy", rows, cols);
-  const int dev = device_of({&k, &ks, &r, &w, &dy});
-  void* on = stream_of(stream, dev);
-  at::Tensor dx = fresh({rows, cols}, dy.scalar_type(), dev), dw = fresh({cols}, at::kFloat, dev);
-  at::Tensor work = fresh({lib.mx_rmsnorm_backward_workspace(rows, cols)}, at::kByte, dev);
-  if (!stream.is_none()) py::cast(work).attr("record_stream")(stream);  // freed here, used there
+  const Place on(stream, device_of({&k, &ks, &r, &w, &dy}));
+  at::Tensor dx = on.fresh({rows, cols}, dy.scalar_type()), dw = on.fresh({cols}, at::kFloat);
+  at::Tensor work = on.scratch({lib.mx_rmsnorm_backward_workspace(rows, cols)}, at::kByte);
   status(lib.mx_rmsnorm_backward(bytes(k), ld(k), bytes(ks), static_cast<float*>(ptr(r)), fmt,
                                  static_cast<float*>(ptr(w)), ptr(dy), real_type(dy), ld(dy), rows, cols, ptr(dx),
-                                 cols, static_cast<float*>(ptr(dw)), ptr(work), on), "mx_rmsnorm_backward");
+                                 cols, static_cast<float*>(ptr(dw)), ptr(work), on.stream()), "mx_rmsnorm_backward");
   return py::make_tuple(dx, dw);
 }
 
