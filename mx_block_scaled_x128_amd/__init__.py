@@ -600,7 +600,7 @@ def gaussws(w, bitwidths, seed, stream_id=0, out=None, stream=None):
 
 # ------------------------------------------------------------------ MX operators
 #
-# Their checks, allocations and calls are in the extension _tensors (built from
+# Their checks, allocations and calls are in the extension _mx_tensors (built from
 # csrc/tensors.cpp next to the library): the same in Python takes longer than
 # the small kernels.  ValueError for a tensor that does not fit, before any
 # call.  E2M1 codes are uint8 tensors with two elements to a byte:
@@ -613,24 +613,25 @@ SwigluKept.__doc__ = "What swiglu_mx keeps of its input: codes [rows][2 cols], s
 RmsnormKept = collections.namedtuple("RmsnormKept", "codes scales rstd fmt")
 RmsnormKept.__doc__ = "What rmsnorm_mx keeps: the input's codes and scales, 1 / rms of each row (fp32), the codes' format."
 
-_tensors = None
+_tensors = None  # _mx_tensors once it is bound; not the submodule's name, which importing it would set
 
 
 def _ops():
     """The extension, its calls bound to the library."""
     global _tensors
-    if _tensors is None:
-        import importlib
-        load_library()
-        _torch()
-        try:
-            ops = importlib.import_module(__name__ + "._tensors")
-        except ImportError as e:
-            raise ImportError("the extension _tensors is not built (%s); run python -m mx_block_scaled_x128_amd.build"
-                              % e) from e
-        ops.bind(_LIB_PATH)
-        _tensors = ops
-    return _tensors
+    load_library()
+    _torch()
+    with _lock:
+        if _tensors is None:
+            import importlib
+            try:
+                ops = importlib.import_module(__name__ + "._mx_tensors")
+            except ImportError as e:
+                raise ImportError("the extension _mx_tensors is not built (%s); run python -m "
+                                  "mx_block_scaled_x128_amd.build" % e) from e
+            ops.bind(_LIB_PATH)
+            _tensors = ops
+        return _tensors
 
 
 def quantize_mxfp4(x, rule=RULE_FLOOR, stream=None):

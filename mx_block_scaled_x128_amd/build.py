@@ -1,5 +1,5 @@
 """Build libmxfp8.so (HIP kernels + C ABI) for gfx950 with hipcc, in-tree, and
-_tensors.so, the Python extension with the MX operators' tensor functions.
+_mx_tensors.so, the Python extension with the MX operators' tensor functions.
 
 The sources compile to objects in parallel (the GEMM once per pair of operand
 formats, plus its host dispatch; the MXFP4 product once per format of its left
@@ -19,7 +19,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmxfp8.so")
-TENSORS = os.path.join(HERE, "_tensors.so")
+TENSORS = os.path.join(HERE, "_mx_tensors.so")
 ARCH = "gfx950"
 # (source, extra flags, object name)
 UNITS = [("api.cpp", [], "api"), ("mx_api.cpp", [], "mx_api"), ("mx_quant.hip", [], "mx_quant"),
@@ -61,7 +61,7 @@ def tensors_command(cc, out):
     base = os.path.dirname(torch.__file__)
     inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"]]
-    return [cc, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-DTORCH_EXTENSION_NAME=_tensors",
+    return [cc, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-DTORCH_EXTENSION_NAME=_mx_tensors",
             "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI] + \
         [a for d in inc for a in ("-isystem", d)] + [os.path.join(CSRC, "tensors.cpp"), "-L" + os.path.join(base, "lib")] + \
         ["-l" + n for n in ("c10", "c10_hip", "torch_cpu", "torch", "torch_python")] + ["-o", out]

@@ -1,5 +1,5 @@
 // tensors.cpp -- the tensor functions of the MX operators as a Python
-// extension (_tensors): checks of the tensors, allocation of the outputs and
+// extension (_mx_tensors): checks of the tensors, allocation of the outputs and
 // one call of the C ABI each.  The same checks in Python cost about 9 us a
 // call, several times what the small kernels take; here they cost under one.
 // Nothing computes here, and the C functions are those of the library that
@@ -30,14 +30,18 @@ struct Library {
   decltype(&::mx_rmsnorm_backward_workspace) mx_rmsnorm_backward_workspace;
 } lib;
 
+bool bound = false;
+
+// All of the functions or, with an error, none.
 void bind(const std::string& path) {
   void* h = dlopen(path.c_str(), RTLD_NOW);
   if (!h) throw py::import_error(dlerror());
+  Library all;
   auto find = [&](auto& f, const char* name) {
     f = reinterpret_cast<std::decay_t<decltype(f)>>(dlsym(h, name));
     if (!f) throw py::import_error(std::string(name) + " is missing from " + path);
   };
-#define MXFP8_FIND(name) find(lib.name, #name)
+#define MXFP8_FIND(name) find(all.name, #name)
   MXFP8_FIND(mxfp4_quantize);
   MXFP8_FIND(mx_dequantize);
   MXFP8_FIND(mx_quantize_t);
@@ -49,6 +53,17 @@ void bind(const std::string& path) {
   MXFP8_FIND(mx_rmsnorm_backward);
   MXFP8_FIND(mx_rmsnorm_backward_workspace);
 #undef MXFP8_FIND
+  lib = all;
+  bound = true;
+}
+
+// The function, which raises while no library is bound.
+template <typename R, typename... A>
+auto once_bound(R (*f)(A...)) {
+  return [f](A... a) -> R {
+    if (!bound) throw py::import_error("libmxfp8.so is not bound to the extension");
+    return f(std::forward<A>(a)...);
+  };
 }
 
 // ---- checks.  The text is put together only when a check fails.
@@ -339,15 +354,15 @@ py::tuple rmsnorm_mx_backward(const at::Tensor& k, const at::Tensor& ks, const a
 
 }  // namespace
 
-PYBIND11_MODULE(_tensors, m) {
+PYBIND11_MODULE(_mx_tensors, m) {
   m.def("bind", &bind);
-  m.def("quantize_mxfp4", &quantize_mxfp4);
-  m.def("dequantize_mx", &dequantize_mx);
-  m.def("quantize_mx_t", &quantize_mx_t);
-  m.def("requantize_mx_t", &requantize_mx_t);
-  m.def("mxfp4_scaled_gemm", &mxfp4_scaled_gemm);
-  m.def("swiglu_mx", &swiglu_mx);
-  m.def("swiglu_mx_backward", &swiglu_mx_backward);
-  m.def("rmsnorm_mx", &rmsnorm_mx);
-  m.def("rmsnorm_mx_backward", &rmsnorm_mx_backward);
+  m.def("quantize_mxfp4", once_bound(&quantize_mxfp4));
+  m.def("dequantize_mx", once_bound(&dequantize_mx));
+  m.def("quantize_mx_t", once_bound(&quantize_mx_t));
+  m.def("requantize_mx_t", once_bound(&requantize_mx_t));
+  m.def("mxfp4_scaled_gemm", once_bound(&mxfp4_scaled_gemm));
+  m.def("swiglu_mx", once_bound(&swiglu_mx));
+  m.def("swiglu_mx_backward", once_bound(&swiglu_mx_backward));
+  m.def("rmsnorm_mx", once_bound(&rmsnorm_mx));
+  m.def("rmsnorm_mx_backward", once_bound(&rmsnorm_mx_backward));
 }

@@ -223,3 +223,52 @@ def test_tensor_functions_fail_loudly_without_the_extension(monkeypatch):
 def test_library_errors_name_their_call():
     with pytest.raises(mx.MxFp8Error, match="mx_rmsnorm_forward"):
         mx._check(2, "mx_rmsnorm_forward")
+
+
+def _in_a_new_process(code):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert run.returncode == 0, run.stderr
+
+
+def test_a_failed_binding_is_not_taken_for_a_bound_extension():
+    """The second call after a failed one fails the same way, and works once the library is there."""
+    _in_a_new_process("""
+import torch, mx_block_scaled_x128_amd as mx
+x, path = torch.zeros(1, 32), mx._LIB_PATH
+mx.load_library()
+mx._LIB_PATH = path + ".absent"
+for _ in range(2):
+    try:
+        mx.quantize_mxfp4(x)
+    except ImportError as e:
+        assert "absent" in str(e), e
+    else:
+        raise AssertionError("no error")
+mx._LIB_PATH = path
+try:
+    mx.quantize_mxfp4(x)
+except ValueError as e:
+    assert "CUDA tensor" in str(e), e
+else:
+    raise AssertionError("no error")
+""")
+
+
+def test_the_extension_alone_refuses_to_run():
+    """Imported without the package's binding, its functions raise; the package binds it all the same."""
+    _in_a_new_process("""
+import torch, mx_block_scaled_x128_amd as mx
+from mx_block_scaled_x128_amd import _mx_tensors
+x = torch.zeros(1, 32)
+for call, error in ((_mx_tensors.quantize_mxfp4, ImportError), (mx.quantize_mxfp4, ValueError)):
+    try:
+        call(x, 1, None)
+    except error:
+        pass
+    else:
+        raise AssertionError("no error")
+""")
