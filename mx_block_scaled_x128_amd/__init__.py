@@ -238,7 +238,8 @@ def mxfp8_version():
 # pointer: dtype, the exact shape the header documents for it, unit column
 # stride (dense for scale, count and bitwidth arrays), and that all tensors
 # live on the current CUDA device, whose current stream (or the given one)
-# the work goes to.  A mismatch raises ValueError before any call.
+# the work goes to.  A mismatch raises ValueError before any call.  With
+# stream=, outputs are allocated as inside torch.cuda.stream(stream).
 
 def _torch():
     import torch
@@ -360,11 +361,25 @@ def _cdiv(a, b):
     return (a + b - 1) // b
 
 
-def _codes(rows, cols, device):
-    """Uninitialized [rows][cols] uint8 view with a 16-element-aligned row pitch."""
+def _empty(shape, dtype, dev, stream):
+    """Uninitialized memory of the stream that will write it: the current one or the one
+    given (a block that another stream freed may still be in use there).  The caller's
+    current stream may read it until it is dropped."""
     torch = _torch()
-    buf = torch.empty((rows, _pad16(max(cols, 1))), dtype=torch.uint8, device=device)
-    return buf[:, :cols]
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _require(stream.device.index == dev, "stream is on %s but the tensors are on cuda:%d", stream.device, dev)
+    caller = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    if stream != caller:
+        t.record_stream(caller)
+    return t
+
+
+def _codes(rows, cols, dev, stream):
+    """Uninitialized [rows][cols] uint8 view with a 16-element-aligned row pitch."""
+    return _empty((rows, _pad16(max(cols, 1))), _torch().uint8, dev, stream)[:, :cols]
 
 
 def _check_out(out, out_dtype, M, N):
@@ -377,13 +392,13 @@ def _check_out(out, out_dtype, M, N):
         _matrix(out, "out", (torch.float32, torch.bfloat16), (M, N))
 
 
-def _out_matrix(out, out_dtype, M, N, device):
+def _out_matrix(out, out_dtype, M, N, dev, stream):
     """`out` (already checked), or a new [M][N] output with a 16-element row pitch."""
     torch = _torch()
     if out is not None:
         return out
     dt = torch.bfloat16 if out_dtype == torch.bfloat16 else torch.float32
-    buf = torch.empty((M, _pad16(max(N, 1))), dtype=dt, device=device)
+    buf = _empty((M, _pad16(max(N, 1))), dt, dev, stream)
     return buf[:, :N]
 
 
@@ -394,11 +409,11 @@ def quantize_token(x, fmt=E4M3, axis=ROW, stream=None):
     rows, cols = _input(x, "x")
     dev = _device_of([("x", x)])
     if axis == ROW:
-        q = _codes(rows, cols, dev)
-        s = torch.empty((rows, _cdiv(cols, 128)), dtype=torch.uint8, device=dev)
+        q = _codes(rows, cols, dev, stream)
+        s = _empty((rows, _cdiv(cols, 128)), torch.uint8, dev, stream)
     else:
-        q = _codes(cols, rows, dev)
-        s = torch.empty((cols, _cdiv(rows, 128)), dtype=torch.uint8, device=dev)
+        q = _codes(cols, rows, dev, stream)
+        s = _empty((cols, _cdiv(rows, 128)), torch.uint8, dev, stream)
     st = fp8_quantize_token(x.data_ptr(), _in_dtype(x), rows, cols, _ld(x), axis, fmt, q.data_ptr(), _ld(q),
                             s.data_ptr(), _stream(stream, dev))
     _check(st, "fp8_quantize_token")
@@ -410,8 +425,8 @@ def quantize_block(w, fmt=E4M3, stream=None):
     torch = _torch()
     rows, cols = _input(w, "w")
     dev = _device_of([("w", w)])
-    q = _codes(rows, cols, dev)
-    s = torch.empty((_cdiv(rows, 128), _cdiv(cols, 128)), dtype=torch.uint8, device=dev)
+    q = _codes(rows, cols, dev, stream)
+    s = _empty((_cdiv(rows, 128), _cdiv(cols, 128)), torch.uint8, dev, stream)
     st = fp8_quantize_block(w.data_ptr(), _in_dtype(w), rows, cols, _ld(w), fmt, q.data_ptr(), _ld(q),
                             s.data_ptr(), _stream(stream, dev))
     _check(st, "fp8_quantize_block")
@@ -424,11 +439,11 @@ def quantize_token_f32s(x, fmt=E4M3, axis=ROW, stream=None):
     rows, cols = _input(x, "x")
     dev = _device_of([("x", x)])
     if axis == ROW:
-        q = _codes(rows, cols, dev)
-        s = torch.empty((rows, _cdiv(cols, 128)), dtype=torch.float32, device=dev)
+        q = _codes(rows, cols, dev, stream)
+        s = _empty((rows, _cdiv(cols, 128)), torch.float32, dev, stream)
     else:
-        q = _codes(cols, rows, dev)
-        s = torch.empty((cols, _cdiv(rows, 128)), dtype=torch.float32, device=dev)
+        q = _codes(cols, rows, dev, stream)
+        s = _empty((cols, _cdiv(rows, 128)), torch.float32, dev, stream)
     st = fp8_quantize_token_f32s(x.data_ptr(), _in_dtype(x), rows, cols, _ld(x), axis, fmt, q.data_ptr(), _ld(q),
                                  s.data_ptr(), _stream(stream, dev))
     _check(st, "fp8_quantize_token_f32s")
@@ -440,8 +455,8 @@ def quantize_block_f32s(w, fmt=E4M3, stream=None):
     torch = _torch()
     rows, cols = _input(w, "w")
     dev = _device_of([("w", w)])
-    q = _codes(rows, cols, dev)
-    s = torch.empty((_cdiv(rows, 128), _cdiv(cols, 128)), dtype=torch.float32, device=dev)
+    q = _codes(rows, cols, dev, stream)
+    s = _empty((_cdiv(rows, 128), _cdiv(cols, 128)), torch.float32, dev, stream)
     st = fp8_quantize_block_f32s(w.data_ptr(), _in_dtype(w), rows, cols, _ld(w), fmt, q.data_ptr(), _ld(q),
                                  s.data_ptr(), _stream(stream, dev))
     _check(st, "fp8_quantize_block_f32s")
@@ -454,10 +469,10 @@ def quantize_token_dual(x, fmt=E4M3, stream=None):
     torch = _torch()
     rows, cols = _input(x, "x")
     dev = _device_of([("x", x)])
-    q = _codes(rows, cols, dev)
-    s = torch.empty((rows, _cdiv(cols, 128)), dtype=torch.uint8, device=dev)
-    qt = _codes(cols, rows, dev)
-    st = torch.empty((cols, _cdiv(rows, 128)), dtype=torch.uint8, device=dev)
+    q = _codes(rows, cols, dev, stream)
+    s = _empty((rows, _cdiv(cols, 128)), torch.uint8, dev, stream)
+    qt = _codes(cols, rows, dev, stream)
+    st = _empty((cols, _cdiv(rows, 128)), torch.uint8, dev, stream)
     r = fp8_quantize_token_dual(x.data_ptr(), _in_dtype(x), rows, cols, _ld(x), fmt, q.data_ptr(), _ld(q),
                                 s.data_ptr(), qt.data_ptr(), _ld(qt), st.data_ptr(), _stream(stream, dev))
     _check(r, "fp8_quantize_token_dual")
@@ -469,10 +484,10 @@ def quantize_block_dual(w, fmt=E4M3, stream=None):
     torch = _torch()
     rows, cols = _input(w, "w")
     dev = _device_of([("w", w)])
-    q = _codes(rows, cols, dev)
-    s = torch.empty((_cdiv(rows, 128), _cdiv(cols, 128)), dtype=torch.uint8, device=dev)
-    qt = _codes(cols, rows, dev)
-    st = torch.empty((_cdiv(cols, 128), _cdiv(rows, 128)), dtype=torch.uint8, device=dev)
+    q = _codes(rows, cols, dev, stream)
+    s = _empty((_cdiv(rows, 128), _cdiv(cols, 128)), torch.uint8, dev, stream)
+    qt = _codes(cols, rows, dev, stream)
+    st = _empty((_cdiv(cols, 128), _cdiv(rows, 128)), torch.uint8, dev, stream)
     r = fp8_quantize_block_dual(w.data_ptr(), _in_dtype(w), rows, cols, _ld(w), fmt, q.data_ptr(), _ld(q),
                                 s.data_ptr(), qt.data_ptr(), _ld(qt), st.data_ptr(), _stream(stream, dev))
     _check(r, "fp8_quantize_block_dual")
@@ -485,9 +500,9 @@ def quantize_mx(x, fmt=E4M3, rule=RULE_FLOOR, counts=True, stream=None):
     rows, cols = _input(x, "x")
     _require(cols % 32 == 0, "x must have a multiple of 32 columns, got %d", cols)
     dev = _device_of([("x", x)])
-    q = _codes(rows, cols, dev)
-    s = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
-    c = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev) if counts else None
+    q = _codes(rows, cols, dev, stream)
+    s = _empty((rows, cols // 32), torch.uint8, dev, stream)
+    c = _empty((rows, cols // 32), torch.uint8, dev, stream) if counts else None
     st = mx_quantize(x.data_ptr(), _in_dtype(x), rows, cols, _ld(x), fmt, rule, q.data_ptr(), _ld(q),
                      s.data_ptr(), c.data_ptr() if counts else None, _stream(stream, dev))
     _check(st, "mx_quantize")
@@ -531,7 +546,7 @@ def block_scaled_gemm(a, a_scales, a_fmt, b, b_scales, b_fmt, b_layout=B_NK, b_s
     _check_out(out, out_dtype, M, N)
     dev = _device_of([("a", a), ("a_scales", a_scales), ("b", b), ("b_scales", b_scales)]
                      + ([("out", out)] if out is not None else []))
-    out = _out_matrix(out, out_dtype, M, N, dev)
+    out = _out_matrix(out, out_dtype, M, N, dev, stream)
     c_dtype = F32 if out.dtype == _torch().float32 else BF16
     st = fp8_block_scaled_gemm(M, N, K, a.data_ptr(), _ld(a), a_fmt, a_scales.data_ptr(), b.data_ptr(), _ld(b),
                                b_fmt, b_layout, b_scales.data_ptr(), b_scale_mode, out.data_ptr(), _ld(out),
@@ -556,7 +571,7 @@ def mx_scaled_gemm(a, a_scales, a_fmt, b, b_scales, b_fmt, out_dtype=None, out=N
     _check_out(out, out_dtype, M, N)
     dev = _device_of([("a", a), ("a_scales", a_scales), ("b", b), ("b_scales", b_scales)]
                      + ([("out", out)] if out is not None else []))
-    out = _out_matrix(out, out_dtype, M, N, dev)
+    out = _out_matrix(out, out_dtype, M, N, dev, stream)
     c_dtype = F32 if out.dtype == _torch().float32 else BF16
     st = mx_gemm(M, N, K, a.data_ptr(), _ld(a), a_fmt, a_scales.data_ptr(), b.data_ptr(), _ld(b), b_fmt,
                  b_scales.data_ptr(), out.data_ptr(), _ld(out), c_dtype, _stream(stream, dev))
@@ -571,7 +586,7 @@ def gemm_f32s(a, a_scales, a_fmt, b, b_scales, b_fmt, b_layout=B_NK, b_scale_mod
     _check_out(out, out_dtype, M, N)
     dev = _device_of([("a", a), ("a_scales", a_scales), ("b", b), ("b_scales", b_scales)]
                      + ([("out", out)] if out is not None else []))
-    out = _out_matrix(out, out_dtype, M, N, dev)
+    out = _out_matrix(out, out_dtype, M, N, dev, stream)
     c_dtype = F32 if out.dtype == _torch().float32 else BF16
     st = fp8_gemm_f32s(M, N, K, a.data_ptr(), _ld(a), a_fmt, a_scales.data_ptr(), b.data_ptr(), _ld(b), b_fmt,
                        b_layout, b_scales.data_ptr(), b_scale_mode, out.data_ptr(), _ld(out), c_dtype,
@@ -590,7 +605,7 @@ def gaussws(w, bitwidths, seed, stream_id=0, out=None, stream=None):
         _matrix(out, "out", (torch.bfloat16,), (rows, cols))
     dev = _device_of([("w", w), ("bitwidths", bitwidths)] + ([("out", out)] if out is not None else []))
     if out is None:
-        buf = torch.empty((rows, _pad16(max(cols, 1))), dtype=torch.bfloat16, device=dev)
+        buf = _empty((rows, _pad16(max(cols, 1))), torch.bfloat16, dev, stream)
         out = buf[:, :cols]
     st = gaussws_sample(w.data_ptr(), _in_dtype(w), rows, cols, _ld(w), bitwidths.data_ptr(), seed, stream_id,
                         out.data_ptr(), _ld(out), _stream(stream, dev))
