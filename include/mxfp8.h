@@ -354,7 +354,7 @@ int mx_dequantize(const uint8_t* q, int64_t ldq, int fmt, const uint8_t* scales,
  *             can be filled up to the K that a product takes.
  *   scales_t: [cols][rows_out / 32].
  * Requires cols % 16 == 0, rows_out % 32 == 0, rows_out >= rows, and at most
- * 2^23 - 1 tiles of 128 x 128.
+ * 2^23 - 8 tiles of 128 x 128.
  */
 int mx_quantize_t(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, int fmt, int rule,
                   uint8_t* qt, int64_t ldqt, int64_t rows_out, uint8_t* scales_t, void* stream);

@@ -45,7 +45,9 @@ int launch_status() { return hipGetLastError() == hipSuccess ? MXFP8_OK : MXFP8_
 int transposed_extents(int64_t rows, int64_t cols, int64_t rows_out, int64_t multiple) {
   if (!extents(rows, cols) || rows_out < rows || rows_out > INT32_MAX) return MXFP8_ERR_SHAPE;
   if (cols % multiple != 0 || rows_out % 32 != 0) return MXFP8_ERR_SHAPE;
-  if (((cols + 127) / 128) * ((rows_out + 127) / 128) >= (int64_t(1) << 23)) return MXFP8_ERR_SHAPE;
+  // The grid is the tiles rounded up to a multiple of 8, of at most 512 threads
+  // each; a launch takes fewer than 2^32 threads.
+  if (((cols + 127) / 128) * ((rows_out + 127) / 128) > (int64_t(1) << 23) - 8) return MXFP8_ERR_SHAPE;
   return MXFP8_OK;
 }
 

@@ -272,3 +272,16 @@ for call, error in ((_mx_tensors.quantize_mxfp4, ImportError), (mx.quantize_mxfp
     else:
         raise AssertionError("no error")
 """)
+
+
+@pytest.mark.parametrize("fmt", [0, 1, 2])
+def test_transposed_grids_stay_below_the_launch_limit(fmt):
+    """Tiles are launched in multiples of 8 with up to 512 threads each, fewer than 2^32 in all: 2^23 - 8 tiles pass
+    the shape check (the null pointer is then what is refused), one more does not."""
+    most = 2 ** 23 - 8
+    for tiles, status in ((most, NULL), (most + 1, SHAPE), (most + 7, SHAPE), (most + 8, SHAPE)):
+        out = 128 * tiles
+        ld = out // 2 if fmt == 2 else out
+        assert mx.mx_quantize_t(None, 1, 100, 128, 128, fmt, 0, Q, ld, out, S, None) == status, tiles
+        assert mx.mx_requantize_t(None, 128, 0, P, 100, 128, fmt, 0, Q, ld, out, S, None) == status, tiles
+    assert mx.mx_quantize_t(None, 1, 100, 112, 112, fmt, 0, Q, ld, 128 * most - 96, S, None) == NULL
