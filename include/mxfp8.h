@@ -410,7 +410,10 @@ int mx_swiglu_backward(const uint8_t* kept, int64_t ldk, const uint8_t* kept_sca
 
 /*
  * mx_rmsnorm_forward -- y = x * r * w, r = 1 / sqrt(mean over the row of x^2 + eps),
- * computed in fp32 and written as MX codes along rows.
+ * computed in fp32 (the mean and its root in 64 bits, rows whose squares leave
+ * fp32's range throughout) and written as MX codes along rows.  r is an fp32
+ * value: infinite for a row whose mean(x^2) + eps is below about 2^-256, zeros
+ * with eps = 0 among them, which makes the row's blocks NaN.
  *   x: [rows][ldx >= cols] fp32 or bf16;  w: [cols] fp32, 16-byte aligned;
  *   eps >= 0 and finite (MXFP8_ERR_SHAPE otherwise).
  *   y: [rows][ldy >= cols] codes of fmt (E4M3 or E5M2), y_scales [rows][cols / 32].

@@ -140,20 +140,22 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(
 // and 5 us for the last sum of dw; with w in registers and no row ahead the
 // backward pass took 87 us.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float wave_sum(float v) {
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v) {
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
   return v;
 }
 // Sum over the waves of one row, the same order in each of them.
-template <int WPR>
-__device__ __forceinline__ float row_sum(float v, uint32_t wave, float* red) {
+template <int WPR, typename T>
+__device__ __forceinline__ T row_sum(T v, uint32_t wave, double* shared) {
   v = wave_sum(v);
   if constexpr (WPR > 1) {
+    T* red = reinterpret_cast<T*>(shared);
     __syncthreads();  // red of the row before has been read
     if ((threadIdx.x & 63) == 0) red[wave] = v;
     __syncthreads();
-    v = 0.0f;
+    v = 0;
 #pragma unroll
     for (int i = 0; i < WPR; ++i) v += red[i];
   }
@@ -204,7 +206,7 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_forward_kernel(
     uint8_t* __restrict__ ks, float* __restrict__ rstd) {
 #if defined(__HIP_DEVICE_COMPILE__)
   extern __shared__ nt_f32x4 lds[];
-  __shared__ float red[16];
+  __shared__ double red[16];
   const uint32_t lane = threadIdx.x & 63;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   constexpr uint32_t RPW = WPR == 1 ? THREADS / 64 : 1;  // rows per workgroup and round
@@ -249,7 +251,22 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_forward_kernel(
     ss = row_sum<WPR>(ss, wave, red);
 #pragma unroll
     for (int i = 0; i < NU; ++i) again(raw[i]);
-    const float r = (float)(1.0 / __builtin_sqrt((double)ss / (double)(upr * 8) + (double)eps));
+    double sum = ss;
+    // Squares that overflow in fp32, or so few bits left that eps does not cover
+    // the loss: once more in 64 bits (the same branch in all waves of the row).
+    if (!(ss < __builtin_inff()) || ss + eps * (float)(upr * 8) < 0x1p-100f) {
+      sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        float f[8];
+        mx_unpack(raw[i], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = __builtin_fma((double)f[j], (double)f[j], sum);
+        again(raw[i]);
+      }
+      sum = row_sum<WPR>(sum, wave, red);
+    }
+    const float r = (float)(1.0 / __builtin_sqrt(sum / (double)(upr * 8) + (double)eps));
     const mx_rsrc ry = mx_run(y + row * ldy), rys = mx_run(ys + row * nb);
     const mx_rsrc rk = mx_run(kept + row * ldk), rks = mx_run(ks + row * nb);
 #pragma unroll
@@ -290,7 +307,7 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(
     T* __restrict__ dx, int64_t lddx, float* __restrict__ part) {
 #if defined(__HIP_DEVICE_COMPILE__)
   extern __shared__ nt_f32x4 lds[];
-  __shared__ float red[16];
+  __shared__ double red[16];
   const uint32_t lane = threadIdx.x & 63;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   constexpr uint32_t RPW = WPR == 1 ? THREADS / 64 : 1;

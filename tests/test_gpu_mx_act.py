@@ -209,3 +209,39 @@ def test_past_four_gib():
     want_dx, want_dw = mx.rmsnorm_mx_backward(want[2], w, tail_x)
     assert torch.equal(dx[-16:], want_dx)
     assert torch.allclose(dw, want_dw, rtol=1e-5, atol=1e-4)  # another order of the same 16 rows' sum
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [544, 8960, 20480])
+def test_rmsnorm_of_rows_whose_squares_leave_fp32(cols, dtype):
+    """Rows scaled by powers of two whose squares overflow or vanish in fp32, with eps = 0, at every number of waves
+    a row; a zero row has no root (0 / 0), rows with an infinity or a NaN are as ever."""
+    powers = np.array([0, 40, 66, 100, 120, -40, -52, -66, -100, -110, 0, 90, -90])
+    rows = len(powers)
+    x = given((rows, cols), mxref.pow2(powers)[:, None], 31, dtype)
+    x64 = x.astype(np.float64)
+    w = (1 + 0.2 * np.random.default_rng(9).normal(0, 1, cols)).astype(np.float32)
+    w64, wd = w.astype(np.float64), torch.from_numpy(w).cuda()
+    y, ys, kept = mx.rmsnorm_mx(tensor(x, dtype), wd, 0.0)
+    r = mxref.rstd(x64, 0.0)
+    d = (12 + np.sqrt(cols)) * U
+    close(kept.rstd, r, d * r)
+    check_codes(y, ys, x64 * r[:, None] * w64, np.full(x.shape, d), mx.E4M3, mx.RULE_CEIL)
+    ref_q, ref_s = mxref.quantize(x64, mx.E4M3, mx.RULE_CEIL)
+    assert np.array_equal(host(kept.scales), ref_s) and np.array_equal(host(kept.codes), ref_q)
+    dy = given((rows, cols), 1e-3, 6, dtype)
+    dx, dw = mx.rmsnorm_mx_backward(kept, wd, tensor(dy, dtype))
+    rk, d64, xk = host(kept.rstd).astype(np.float64), dy.astype(np.float64), mxref.dequantize(ref_q, ref_s, mx.E4M3)
+    ex, ew = mxref.rmsnorm_grad(xk, rk, w64, d64)
+    xh, c = np.abs(xk * rk[:, None]), np.abs(d64 * w64)
+    tol = (c + xh * (c * xh).mean(1, keepdims=True)) * rk[:, None] * d
+    smallest = {"f32": 2.0 ** -149, "bf16": 2.0 ** -133}[dtype]  # the type's own step below its normal range
+    close(dx, ex, tol + OWN[dtype] * (np.abs(ex) + tol) + smallest)
+    close(dw, ew, (np.abs(d64) * xh).sum(0) * (8 + np.sqrt(rows)) * U + 1e-44)
+    # rows without a finite root
+    x[0], x[1, 5], x[2, 40] = 0.0, np.inf, np.nan
+    y, ys, kept = mx.rmsnorm_mx(tensor(x, dtype), wd, 0.0)
+    v, rk = host(mx.dequantize_mx(y, ys, mx.E4M3)), host(kept.rstd)
+    assert np.isnan(v[0]).all() and np.isnan(v[2]).all() and np.isnan(v[1, :32]).all() and not v[1, 32:].any()
+    assert np.isinf(rk[0]) and rk[1] == 0 and np.isnan(rk[2]) and np.isfinite(v[3:]).all()
+    close(kept.rstd[3:], r[3:], d * r[3:])
