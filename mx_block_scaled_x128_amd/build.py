@@ -23,7 +23,7 @@ TENSORS = os.path.join(HERE, "_mx_tensors.so")
 ARCH = "gfx950"
 # (source, extra flags, object name)
 UNITS = [("api.cpp", [], "api"), ("mx_api.cpp", [], "mx_api"), ("mx_quant.hip", [], "mx_quant"),
-         ("mx_act.hip", [], "mx_act"), 
+         ("mx_act.hip", [], "mx_act"),
          ("mxfp4_gemm.hip", ["-DMXFP4_GEMM_FMT=-1"], "mxfp4_gemm_dispatch"),
          ("quant.hip", [], "quant"), ("gaussws.hip", [], "gaussws"),
          ("gemm.hip", ["-DMXFP8_GEMM_FMT=-1"], "gemm_dispatch")] + \
@@ -68,32 +68,42 @@ def tensors_command(cc, out):
 
 
 def build(verbose=False, jobs=None):
+    """Build the library and the extension; return the library's path.  The library needs hipcc
+    alone and is in place before an error of the extension (no torch, or a failed compilation)
+    is raised."""
     cc = hipcc()
     tmpdir = tempfile.mkdtemp(prefix="mxfp8_build_")
+    parts = []
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        err = _run(cmd)
+        if verbose and err.strip():
+            print(err, file=sys.stderr)
+
+    def put(make, path):
+        """make(path) written next to its place, then moved there."""
+        part = path + ".tmp"
+        parts.append(part)
+        run(make(part))
+        os.replace(part, path)
+
     try:
         cmds = [[cc] + FLAGS + extra + ["-c", os.path.join(CSRC, src), "-o", os.path.join(tmpdir, name + ".o")]
                 for src, extra, name in UNITS]
-        cmds.insert(0, tensors_command(cc, TENSORS + ".tmp"))  # the longest first
-        if verbose:
-            for c in cmds:
-                print(" ".join(c), flush=True)
-        jobs = jobs or min(len(cmds), max(1, os.cpu_count() or 1))
+        jobs = jobs or min(len(cmds) + 1, max(1, os.cpu_count() or 1))
         with concurrent.futures.ThreadPoolExecutor(max_workers=jobs) as pool:
-            errs = list(pool.map(_run, cmds))
-        tmp = LIB + ".tmp"
-        link = [cc, "--offload-arch=" + ARCH, "-shared", "-fPIC"] + \
-               [os.path.join(tmpdir, name + ".o") for _, _, name in UNITS] + ["-o", tmp]
-        if verbose:
-            print(" ".join(link), flush=True)
-        errs.append(_run(link))
-        if verbose:
-            for e in errs:
-                if e.strip():
-                    print(e, file=sys.stderr)
-        os.replace(tmp, LIB)
-        os.replace(TENSORS + ".tmp", TENSORS)
+            tensors = pool.submit(put, lambda out: tensors_command(cc, out), TENSORS)  # the longest first
+            list(pool.map(run, cmds))
+            put(lambda out: [cc, "--offload-arch=" + ARCH, "-shared", "-fPIC"] +
+                [os.path.join(tmpdir, name + ".o") for _, _, name in UNITS] + ["-o", out], LIB)
+            tensors.result()
     finally:
         shutil.rmtree(tmpdir, ignore_errors=True)
+        for part in parts:
+            if os.path.exists(part):
+                os.remove(part)
     return LIB
 
 
