@@ -826,7 +826,8 @@ void gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const 
       // 16x18944x3584: 12.8 against 15.6).
       const bool wide_a = M * (AFMT == kE2M1 ? K / 2 : K) > 32 * 1024 && n16 >= 512;
       if (wide_a) MXFP4_FEW(1, 2, 8, 2);
-      else if (chunks <= 16 || (n16 >= 512 && M <= 8)) MXFP4_FEW(1, 1, 2, 4);
+      else if (chunks <= 16 || (n16 >= 512 && M <= 8))  // A, 32 KB at most, always fits
+        few_rows<AFMT, 1, 1, 2, 4, true>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, stream);
       else MXFP4_FEW(1, 1, 4, 4);
     } else if (pairs < 128 && M <= 48) {
       // Few workgroups of 32 x 32 (us, 16x16, 16x32 and 32x32 ones, E4M3 x
