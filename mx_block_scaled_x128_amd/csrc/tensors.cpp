@@ -88,7 +88,8 @@ void status(int st, const char* where) {
 
 bool is_real(const at::Tensor& t) { return t.scalar_type() == at::kFloat || t.scalar_type() == at::kBFloat16; }
 int real_type(const at::Tensor& t) { return t.scalar_type() == at::kFloat ? MXFP8_F32 : MXFP8_BF16; }
-int64_t ld(const at::Tensor& t) { return t.size(0) > 1 ? t.stride(0) : std::max(t.stride(0), t.size(1)); }
+// One row has no leading dimension, whatever its stride: the least that the C functions take.
+int64_t ld(const at::Tensor& t) { return t.size(0) > 1 ? t.stride(0) : (t.size(1) + 15) / 16 * 16; }
 void* ptr(const at::Tensor& t) { return t.data_ptr(); }
 uint8_t* bytes(const at::Tensor& t) { return static_cast<uint8_t*>(t.data_ptr()); }
 

@@ -248,3 +248,29 @@ def test_scales_that_just_fill_lds_and_that_do_not(K):
     b, sb = operand(900, K, mx.E2M1, 16, spread=1)
     y, t = product(a, sa, mx.E2M1, b, sb)
     assert_gemm_close(run(a, sa, mx.E2M1, b, sb, torch.float32), y, t, False)
+
+
+@pytest.mark.parametrize("a_fmt", FMTS)
+def test_one_row_of_any_stride(a_fmt):
+    """The last token of one long sequence: a single row 2^22 + 16 bytes and more from its neighbour, and an odd dense
+    output row."""
+    K, N = 512, 300
+    a, sa = operand(1, K, a_fmt, 17)
+    b, sb = operand(N, K, mx.E2M1, 18)
+    width = a.shape[1]
+    for stride in ((1 << 22) + 16, width + 1):
+        far = torch.zeros(2 * stride, dtype=torch.uint8, device="cuda").as_strided((1, width), (stride, 1))
+        far.copy_(dev(a))
+        out = torch.full((1, N), 7.0, device="cuda")
+        mx.mxfp4_scaled_gemm(far, dev(sa), a_fmt, dev_ld16(b), dev(sb), out=out)
+        y, t = product(a, sa, a_fmt, b, sb)
+        assert_gemm_close(host(out), y, t, False)
+    row = torch.randn(65, device="cuda")[:64].as_strided((1, 64), (65, 1))
+    q, s = mx.quantize_mxfp4(row)
+    want = mx.quantize_mxfp4(row.clone())
+    assert torch.equal(q, want[0]) and torch.equal(s, want[1])
+    h, hs, kept = mx.swiglu_mx(row)
+    dx = mx.swiglu_mx_backward(kept, row[:, :32])
+    want = mx.swiglu_mx(row.clone())
+    assert torch.equal(h, want[0]) and torch.equal(hs, want[1])
+    assert torch.equal(dx, mx.swiglu_mx_backward(want[2], row[:, :32].clone()))
