@@ -285,3 +285,12 @@ def test_transposed_grids_stay_below_the_launch_limit(fmt):
         assert mx.mx_quantize_t(None, 1, 100, 128, 128, fmt, 0, Q, ld, out, S, None) == status, tiles
         assert mx.mx_requantize_t(None, 128, 0, P, 100, 128, fmt, 0, Q, ld, out, S, None) == status, tiles
     assert mx.mx_quantize_t(None, 1, 100, 112, 112, fmt, 0, Q, ld, 128 * most - 96, S, None) == NULL
+
+
+@pytest.mark.parametrize("fmt", [0, 1, 2])
+def test_mxfp4_gemm_refuses_rows_past_its_offsets(fmt):
+    """2^22 bytes from row to row are taken (a misaligned output is what is refused here), 16 more are not."""
+    most = 1 << 22
+    for lda, ldb, status in ((most, most, OK), (most + 16, 256, LD), (512, most + 16, LD)):
+        got = mx.mxfp4_gemm(64, 256, 512, X, lda, fmt, S, Q, ldb, P, MIS if status == OK else C, 256, 0, None)
+        assert got == (ALIGN if status == OK else status)
