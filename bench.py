@@ -23,8 +23,9 @@ dualq (the two-orientation quantizers), gaussws7b (GaussWS sampling of the 7B
 weight from fp32 master weights), mxstress (MX quantization with clamp counts of
 64 distinct 4096x4096 fp32 tensors, with the clamp statistics).  gemmsweep times
 the GEMM alone over N and K; vendorgemm times the GEMM beside the FP8 products
-of the ROCm BLAS library (torch._scaled_mm) on the same shapes; copy times a
-plain 256 MiB device copy.
+of the ROCm BLAS library (torch._scaled_mm) on the same shapes; mxops times the MX
+operators (MXFP4 quantizer and product, transposed quantizers, SwiGLU, RMSNorm)
+case by case; copy times a plain 256 MiB device copy.
 
 Usage: python bench.py [--gpus 1] [--steps K] [--warmup W] [--workload NAME] [--no-cpu]
                        [--cpu-rows R]
@@ -45,7 +46,7 @@ FP8_PEAK_TFLOPS = 5000.0   # MI355X dense FP8 MFMA, TFLOP/s
 METRIC = "FP8 quantize GB/s + block-scaled FP8 GEMM TFLOP/s, % of MI355X peak"
 HERE = os.path.dirname(os.path.abspath(__file__))
 WORKLOADS = ["dgrad7b", "fprop1p5b", "wgrad", "mxfprop1p5b", "f32sfprop1p5b", "dualq", "gaussws7b", "mxstress",
-             "copy", "gemmsweep", "vendorgemm"]
+             "copy", "gemmsweep", "vendorgemm", "mxops"]
 
 
 def parse():
@@ -1044,6 +1045,58 @@ def bench_vendor_gemm(args):
             "cpu_baseline": None}
 
 
+# Beside the listed cases of perf/operators.py: products of 64 to 512 rows, and fp32 activations and weights.
+MX_CASES = [{"name": "gemm-%dx%dx%d-%s" % (m, n, k, a), "op": "gemm", "m": m, "n": n, "k": k, "a": a}
+            for m, n, k in ((64, 3584, 8960), (128, 3584, 3584), (128, 3584, 18944), (256, 3584, 18944), (512, 3584, 3584))
+            for a in ("e4m3", "e2m1")] + [
+    {"name": "quantize-18944x3584-f32", "op": "quantize", "rows": 18944, "cols": 3584, "dtype": "f32", "rule": "floor"},
+    {"name": "transpose-18944x3584-bf16", "op": "transpose", "rows": 18944, "cols": 3584, "source": "bf16", "to": "e2m1",
+     "rule": "floor"},
+    {"name": "swiglu-4096x18944-f32", "op": "swiglu", "rows": 4096, "cols": 18944, "dtype": "f32", "pass": "train"},
+    {"name": "rmsnorm-8192x3584-f32", "op": "rmsnorm", "rows": 8192, "cols": 3584, "dtype": "f32", "pass": "train"}]
+
+
+def bench_mx_ops(args):
+    """The MX operators through their tensor functions, case by case: `warmup` passes and then
+    `steps` passes back to back between one event pair, over three sets of inputs in turn, in
+    three rounds (median; least and largest beside it).  A pass of the quantizers and of the
+    operators with 8-bit outputs holds the call that turns the codes back into values, as in
+    perf/operators.py, whose inputs and byte and operation counts these are.  `value` is the
+    listed cases' sum."""
+    import importlib.util
+    import torch
+    spec = importlib.util.spec_from_file_location("operators", os.path.join(HERE, "perf", "operators.py"))
+    ops = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ops)
+    ops.own = True
+    listed, res = ops.listed(), []
+    for case in listed + MX_CASES:
+        states = [ops.prepare(case, 100 + k) for k in range(3)]
+        times = []
+        for _ in range(3):
+            for i in range(args.warmup):
+                ops.run(states[i % 3])
+            torch.cuda.synchronize()
+            e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            e0.record()
+            for i in range(args.steps):
+                ops.run(states[i % 3])
+            e1.record()
+            torch.cuda.synchronize()
+            times.append(e0.elapsed_time(e1) * 1e3 / args.steps)
+        us, work = float(np.median(times)), ops.work(case)
+        res.append({"case": case["name"], "us": round(us, 2), "least_us": round(min(times), 2),
+                    "most_us": round(max(times), 2), "GB/s": round(work["bytes"] / us / 1e3, 1),
+                    "TFLOP/s": round(work["flops"] / us / 1e6, 1)})
+        del states
+    total = sum(r["us"] for r in res[:len(listed)])
+    return {"metric": "MX operators, sum over the listed cases", "value": round(total, 1), "unit": "us", "n_gpus": 1,
+            "steps": args.steps, "warmup": args.warmup, "ms_per_step": round(total / 1e3, 4),
+            "higher_is_better": False, "scaling": "weak", "vs_baseline": None, "dtype": "mxfp4/mxfp8",
+            "data": "synthetic", "config": {"workload": "mxops: the listed cases of perf/operators.py"},
+            "cases": res, "roofline": None, "cpu_baseline": None}
+
+
 def bench_copy(args):
     """A plain device copy of 256 MiB (torch's copy kernel): the reference point that scales
     profiler byte counters (FETCH_SIZE / WRITE_SIZE) to bytes, and a measured bandwidth."""
@@ -1078,6 +1131,8 @@ def main():
         line = bench_gemm_sweep(args)
     elif args.workload == "vendorgemm":
         line = bench_vendor_gemm(args)
+    elif args.workload == "mxops":
+        line = bench_mx_ops(args)
     else:
         line = bench_workload(args)
     print(json.dumps(line), flush=True)
