@@ -12,8 +12,10 @@
 //   SwiGLU   dg = dh * u~ * sigma * (1 + g~ * (1 - sigma)),  du = dh * g~ * sigma
 //   RMSNorm  c = dy * w,  xh = x~ * r,  dx = r * (c - xh * mean(c * xh)),
 //            dw = sum over rows of dy * xh
-// All arithmetic is in fp32; the codes and the gradients' own type are the
-// only roundings.  Each tensor is read and written once: HBM bounds all four.
+// Arithmetic is in fp32, RMSNorm's mean and root in 64 bits (and the squares of
+// rows that leave fp32's range); the codes and the gradients' own type are the
+// only roundings to fewer bits.  Each tensor is read and written once: HBM
+// bounds all four.
 #include "mx_common.hpp"
 #include "mx_launch.hpp"
 
@@ -148,10 +150,10 @@ __device__ __forceinline__ T wave_sum(T v) {
 }
 // Sum over the waves of one row, the same order in each of them.
 template <int WPR, typename T>
-__device__ __forceinline__ T row_sum(T v, uint32_t wave, double* shared) {
+__device__ __forceinline__ T row_sum(T v, uint32_t wave) {
   v = wave_sum(v);
   if constexpr (WPR > 1) {
-    T* red = reinterpret_cast<T*>(shared);
+    __shared__ T red[WPR];
     __syncthreads();  // red of the row before has been read
     if ((threadIdx.x & 63) == 0) red[wave] = v;
     __syncthreads();
@@ -206,7 +208,6 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_forward_kernel(
     uint8_t* __restrict__ ks, float* __restrict__ rstd) {
 #if defined(__HIP_DEVICE_COMPILE__)
   extern __shared__ nt_f32x4 lds[];
-  __shared__ double red[16];
   const uint32_t lane = threadIdx.x & 63;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   constexpr uint32_t RPW = WPR == 1 ? THREADS / 64 : 1;  // rows per workgroup and round
@@ -248,7 +249,7 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_forward_kernel(
       for (int j = 0; j < 8; ++j) sq[j] = __builtin_fmaf(f[j], f[j], sq[j]);
     }
     float ss = ((sq[0] + sq[1]) + (sq[2] + sq[3])) + ((sq[4] + sq[5]) + (sq[6] + sq[7]));
-    ss = row_sum<WPR>(ss, wave, red);
+    ss = row_sum<WPR>(ss, wave);
 #pragma unroll
     for (int i = 0; i < NU; ++i) again(raw[i]);
     double sum = ss;
@@ -264,7 +265,7 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_forward_kernel(
         for (int j = 0; j < 8; ++j) sum = __builtin_fma((double)f[j], (double)f[j], sum);
         again(raw[i]);
       }
-      sum = row_sum<WPR>(sum, wave, red);
+      sum = row_sum<WPR>(sum, wave);
     }
     const float r = (float)(1.0 / __builtin_sqrt(sum / (double)(upr * 8) + (double)eps));
     const mx_rsrc ry = mx_run(y + row * ldy), rys = mx_run(ys + row * nb);
@@ -307,7 +308,6 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(
     T* __restrict__ dx, int64_t lddx, float* __restrict__ part) {
 #if defined(__HIP_DEVICE_COMPILE__)
   extern __shared__ nt_f32x4 lds[];
-  __shared__ double red[16];
   const uint32_t lane = threadIdx.x & 63;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   constexpr uint32_t RPW = WPR == 1 ? THREADS / 64 : 1;
@@ -367,7 +367,7 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(
       dot += p;
       __builtin_amdgcn_sched_barrier(0);  // unit after unit: side by side they need every register
     }
-    const float k = row_sum<WPR>(dot, wave, red) * inv_cols;
+    const float k = row_sum<WPR>(dot, wave) * inv_cols;
     const mx_rsrc rx = mx_run(dx + row * lddx);
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
