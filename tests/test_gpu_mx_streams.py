@@ -9,8 +9,8 @@ import mx_block_scaled_x128_amd as mx
 pytestmark = pytest.mark.gpu
 
 
-def _busy(n=40):
-    """A few milliseconds of elementwise work on the current stream."""
+def _busy(n=400):
+    """Several milliseconds of elementwise work on the current stream, many times what a call takes the host."""
     t = torch.ones(16 << 20, device="cuda")
     for _ in range(n):
         t.mul_(1.0001)
@@ -81,7 +81,7 @@ def test_two_backward_passes_at_once():
     want = [mx.rmsnorm_mx_backward(kept, w, d) for d in dy]
     torch.cuda.synchronize()
     for _ in range(5):
-        hold = _busy(10)
+        hold = _busy(40)
         got = [mx.rmsnorm_mx_backward(kept, w, dy[0]), mx.rmsnorm_mx_backward(kept, w, dy[1], stream=side)]
         torch.cuda.synchronize()
         for g, e in zip(got, want):
