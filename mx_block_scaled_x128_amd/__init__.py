@@ -621,7 +621,8 @@ def gaussws(w, bitwidths, seed, stream_id=0, out=None, stream=None):
 # call.  E2M1 codes are uint8 tensors with two elements to a byte:
 # [rows][cols / 2].  With stream=, a call works as inside
 # torch.cuda.stream(stream): what it allocates is that stream's memory; what it
-# returns is marked as in use on the caller's current stream, too.
+# returns is marked as in use on the caller's current stream, too.  Inputs are
+# not marked: they stay until the stream is done with them.
 
 SwigluKept = collections.namedtuple("SwigluKept", "codes scales fmt")
 SwigluKept.__doc__ = "What swiglu_mx keeps of its input: codes [rows][2 cols], scales [rows][2 cols / 32], their format."

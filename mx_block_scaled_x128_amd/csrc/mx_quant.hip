@@ -8,7 +8,9 @@
 //   mx_dequantize    codes and scales back to values.
 // For a block with largest magnitude amax, e its exponent (mx_scale):
 //   scale byte = e + 127,  code = cast(x * 2^-e), to nearest even, saturating.
-// All four move each byte once; HBM bounds them.
+// All four move each byte once.  HBM bounds the row-wise ones; the transposers
+// come near it, held back by vector instructions and scattered scale lines
+// (from codes most) and by a launch's start and end.
 #include <type_traits>
 
 #include "mx_common.hpp"
