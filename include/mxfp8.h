@@ -443,6 +443,43 @@ int mx_rmsnorm_backward(const uint8_t* kept, int64_t ldk, const uint8_t* kept_sc
 /* Bytes of workspace; 0 for extents that mx_rmsnorm_backward refuses or that need none. */
 int64_t mx_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
 
+/*
+ * mx_layernorm_forward -- y = xh * w + b, xh = (x - mu) * r, mu the row's mean,
+ * r = 1 / sqrt(mean over the row of (x - mu)^2 + eps), computed in fp32 (the
+ * root in 64 bits; rows whose squares leave fp32's range throughout) and
+ * written as MX codes along rows.  x - mu is taken of the values as they are: a
+ * row far from zero loses nothing more.  r is an fp32 value: infinite for a row
+ * of equal values with eps = 0, which makes the row's blocks NaN.
+ *   x: [rows][ldx >= cols] fp32 or bf16;  w, b: [cols] fp32, 16-byte aligned;
+ *   w NULL: ones, and then b is NULL; b NULL: zeros.
+ *   eps >= 0 and finite (MXFP8_ERR_SHAPE otherwise).
+ *   y: [rows][ldy >= cols] codes of fmt (E4M3 or E5M2), y_scales [rows][cols / 32].
+ *   kept: [rows][ldk >= cols] codes of xh, kept_scales [rows][cols / 32], and
+ *         rstd: [rows] fp32 = r, for mx_layernorm_backward.  All three NULL:
+ *         nothing is kept (inference).
+ * Requires cols % 32 == 0 and cols <= 32768 (a row stays in registers).
+ */
+int mx_layernorm_forward(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const float* w,
+                         const float* b, float eps, int fmt, int rule, uint8_t* y, int64_t ldy, uint8_t* y_scales,
+                         uint8_t* kept, int64_t ldk, uint8_t* kept_scales, float* rstd, void* stream);
+
+/*
+ * mx_layernorm_backward -- the gradients of y at the kept values xh, r:
+ *   c = dy * w,  dx = r * (c - mean over the row of c - xh * mean over the row of c * xh),
+ *   dw = sum over rows of dy * xh,  db = sum over rows of dy.
+ *   dy: [rows][lddy >= cols], dx: [rows][lddx >= cols], both of `dtype`;
+ *   w as for the forward pass;  dw, db: [cols] fp32, or both NULL: not computed.
+ *   workspace: mx_layernorm_backward_workspace(rows, cols) bytes, 16-byte
+ *   aligned, used only during the call; NULL where dw is.
+ * dw and db are summed in a fixed order: the same inputs give the same bits.
+ * With rows == 0 they are set to zero.
+ */
+int mx_layernorm_backward(const uint8_t* kept, int64_t ldk, const uint8_t* kept_scales, const float* rstd, int fmt,
+                          const float* w, const void* dy, int dtype, int64_t lddy, int64_t rows, int64_t cols,
+                          void* dx, int64_t lddx, float* dw, float* db, void* workspace, void* stream);
+/* Bytes of workspace; 0 for extents that mx_layernorm_backward refuses or that need none. */
+int64_t mx_layernorm_backward_workspace(int64_t rows, int64_t cols);
+
 /* Static description of a status code (never NULL). */
 const char* mxfp8_status_string(int status);
 

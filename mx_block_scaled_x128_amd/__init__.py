@@ -12,14 +12,16 @@ Low-level entry points carry the C names and signatures (pointers as ints):
   mx_quantize, fp8_block_scaled_gemm, fp8_gemm_f32s, mx_gemm, gaussws_sample,
   mxfp4_quantize, mx_dequantize, mx_quantize_t, mx_requantize_t, mxfp4_gemm,
   mx_swiglu_forward, mx_swiglu_backward, mx_rmsnorm_forward,
-  mx_rmsnorm_backward, mx_rmsnorm_backward_workspace,
+  mx_rmsnorm_backward, mx_rmsnorm_backward_workspace, mx_layernorm_forward,
+  mx_layernorm_backward, mx_layernorm_backward_workspace,
   mxfp8_status_string, mxfp8_version.
 Tensor conveniences allocate outputs with torch and call them:
   quantize_token, quantize_block, quantize_token_dual, quantize_block_dual,
   quantize_token_f32s, quantize_block_f32s, quantize_mx, block_scaled_gemm,
   gemm_f32s, mx_scaled_gemm, gaussws, quantize_mxfp4, dequantize_mx,
   quantize_mx_t, requantize_mx_t, mxfp4_scaled_gemm, swiglu_mx,
-  swiglu_mx_backward, rmsnorm_mx, rmsnorm_mx_backward.
+  swiglu_mx_backward, rmsnorm_mx, rmsnorm_mx_backward, layernorm_mx,
+  layernorm_mx_backward.
 """
 import collections
 import ctypes
@@ -39,6 +41,8 @@ __all__ = [
     "mx_swiglu_backward", "mx_rmsnorm_forward", "mx_rmsnorm_backward", "mx_rmsnorm_backward_workspace",
     "quantize_mxfp4", "dequantize_mx", "quantize_mx_t", "requantize_mx_t", "mxfp4_scaled_gemm",
     "swiglu_mx", "swiglu_mx_backward", "SwigluKept", "rmsnorm_mx", "rmsnorm_mx_backward", "RmsnormKept",
+    "mx_layernorm_forward", "mx_layernorm_backward", "mx_layernorm_backward_workspace", "layernorm_mx",
+    "layernorm_mx_backward", "LayernormKept",
 ]
 
 # enum values of include/mxfp8.h
@@ -109,10 +113,15 @@ def load_library():
         lib.mx_rmsnorm_forward.argtypes = [P, I, I64, I64, I64, P, F, I, I, P, I64, P, P, I64, P, P, P]
         lib.mx_rmsnorm_backward.argtypes = [P, I64, P, P, I, P, P, I, I64, I64, I64, P, I64, P, P, P]
         lib.mx_rmsnorm_backward_workspace.argtypes = [I64, I64]
+        lib.mx_layernorm_forward.argtypes = [P, I, I64, I64, I64, P, P, F, I, I, P, I64, P, P, I64, P, P, P]
+        lib.mx_layernorm_backward.argtypes = [P, I64, P, P, I, P, P, I, I64, I64, I64, P, I64, P, P, P, P]
+        lib.mx_layernorm_backward_workspace.argtypes = [I64, I64]
         for f in (lib.mxfp4_quantize, lib.mx_dequantize, lib.mx_quantize_t, lib.mx_requantize_t, lib.mxfp4_gemm,
-                  lib.mx_swiglu_forward, lib.mx_swiglu_backward, lib.mx_rmsnorm_forward, lib.mx_rmsnorm_backward):
+                  lib.mx_swiglu_forward, lib.mx_swiglu_backward, lib.mx_rmsnorm_forward, lib.mx_rmsnorm_backward,
+                  lib.mx_layernorm_forward, lib.mx_layernorm_backward):
             f.restype = I
         lib.mx_rmsnorm_backward_workspace.restype = I64
+        lib.mx_layernorm_backward_workspace.restype = I64
         lib.mxfp8_status_string.argtypes = [I]
         lib.mxfp8_status_string.restype = ctypes.c_char_p
         lib.mxfp8_version.argtypes = []
@@ -221,6 +230,22 @@ def mx_rmsnorm_backward(kept, ldk, kept_scales, rstd, fmt, w, dy, dtype, lddy, r
 
 def mx_rmsnorm_backward_workspace(rows, cols):
     return load_library().mx_rmsnorm_backward_workspace(rows, cols)
+
+
+def mx_layernorm_forward(x, x_dtype, rows, cols, ldx, w, b, eps, fmt, rule, y, ldy, y_scales, kept, ldk, kept_scales,
+                         rstd, stream):
+    return load_library().mx_layernorm_forward(x, x_dtype, rows, cols, ldx, w, b, eps, fmt, rule, y, ldy, y_scales,
+                                               kept, ldk, kept_scales, rstd, stream)
+
+
+def mx_layernorm_backward(kept, ldk, kept_scales, rstd, fmt, w, dy, dtype, lddy, rows, cols, dx, lddx, dw, db, workspace,
+                          stream):
+    return load_library().mx_layernorm_backward(kept, ldk, kept_scales, rstd, fmt, w, dy, dtype, lddy, rows, cols, dx,
+                                                lddx, dw, db, workspace, stream)
+
+
+def mx_layernorm_backward_workspace(rows, cols):
+    return load_library().mx_layernorm_backward_workspace(rows, cols)
 
 
 def mxfp8_status_string(status):
@@ -629,6 +654,10 @@ SwigluKept.__doc__ = "What swiglu_mx keeps of its input: codes [rows][2 cols], s
 RmsnormKept = collections.namedtuple("RmsnormKept", "codes scales rstd fmt")
 RmsnormKept.__doc__ = "What rmsnorm_mx keeps: the input's codes and scales, 1 / rms of each row (fp32), the codes' format."
 
+LayernormKept = collections.namedtuple("LayernormKept", "codes scales rstd fmt")
+LayernormKept.__doc__ = "What layernorm_mx keeps: the normalised input's codes and scales, 1 / deviation of each row " \
+                        "(fp32), the codes' format."
+
 _tensors = None  # _mx_tensors once it is bound; not the submodule's name, which importing it would set
 
 
@@ -703,3 +732,16 @@ def rmsnorm_mx(x, w, eps, fmt=E4M3, rule=RULE_CEIL, keep=True, stream=None):
 def rmsnorm_mx_backward(kept, w, dy, stream=None):
     """(dx [rows][cols] of dy's dtype, dw [cols] float32) at the kept values."""
     return (_tensors or _ops()).rmsnorm_mx_backward(kept.codes, kept.scales, kept.rstd, kept.fmt, w, dy, stream)
+
+
+def layernorm_mx(x, w, b, eps, fmt=E4M3, rule=RULE_CEIL, keep=True, stream=None):
+    """y = xh * w + b, xh = (x - mean) / sqrt(var + eps) along rows, as MX codes: (y [rows][cols], scales
+    [rows][cols / 32], LayernormKept for layernorm_mx_backward, or None with keep=False).  b None: no bias;
+    w and b None: xh itself."""
+    r = (_tensors or _ops()).layernorm_mx(x, w, b, eps, fmt, rule, keep, stream)
+    return r[0], r[1], LayernormKept(r[2], r[3], r[4], fmt) if keep else None
+
+
+def layernorm_mx_backward(kept, w, dy, stream=None):
+    """(dx [rows][cols] of dy's dtype, dw and db [cols] float32) at the kept values; w None: (dx, None, None)."""
+    return (_tensors or _ops()).layernorm_mx_backward(kept.codes, kept.scales, kept.rstd, kept.fmt, w, dy, stream)

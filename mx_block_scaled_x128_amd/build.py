@@ -23,7 +23,7 @@ TENSORS = os.path.join(HERE, "_mx_tensors.so")
 ARCH = "gfx950"
 # (source, extra flags, object name)
 UNITS = [("api.cpp", [], "api"), ("mx_api.cpp", [], "mx_api"), ("mx_quant.hip", [], "mx_quant"),
-         ("mx_act.hip", [], "mx_act"),
+         ("mx_act.hip", [], "mx_act"), ("mx_layernorm.hip", [], "mx_layernorm"),
          ("mxfp4_gemm.hip", ["-DMXFP4_GEMM_FMT=-1"], "mxfp4_gemm_dispatch"),
          ("quant.hip", [], "quant"), ("gaussws.hip", [], "gaussws"),
          ("gemm.hip", ["-DMXFP8_GEMM_FMT=-1"], "gemm_dispatch")] + \

@@ -164,20 +164,6 @@ __device__ __forceinline__ T row_sum(T v, uint32_t wave) {
   return v;
 }
 
-// The row as read, once more: without this the compiler keeps the converted
-// values of the first pass for the second, twice the registers.
-__device__ __forceinline__ void again(MxRaw<uint16_t>& r) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("" : "+v"(r.v));
-#endif
-}
-__device__ __forceinline__ void again(MxRaw<float>&) {}
-__device__ __forceinline__ void again(uint2& c) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("" : "+v"(c.x), "+v"(c.y));
-#endif
-}
-
 // w in LDS as two planes, the first and the last four elements of each unit:
 // a wave's reads of a plane are 1 KB without a gap.
 struct WeightLds {

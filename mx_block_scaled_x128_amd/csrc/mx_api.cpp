@@ -210,4 +210,46 @@ int mx_rmsnorm_backward(const uint8_t* kept, int64_t ldk, const uint8_t* kept_sc
   return launch_status();
 }
 
+int mx_layernorm_forward(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const float* w,
+                         const float* b, float eps, int fmt, int rule, uint8_t* y, int64_t ldy, uint8_t* y_scales,
+                         uint8_t* kept, int64_t ldk, uint8_t* kept_scales, float* rstd, void* stream) {
+  if (!real(x_dtype) || !fp8(fmt) || !rule_ok(rule)) return MXFP8_ERR_ENUM;
+  if (!extents(rows, cols) || cols % 32 != 0 || cols > mxfp8::kMaxNormCols) return MXFP8_ERR_SHAPE;
+  if (!(eps >= 0.0f && eps <= 3.4e38f)) return MXFP8_ERR_SHAPE;
+  if (rows == 0 || cols == 0) return MXFP8_OK;
+  if (!x || !y || !y_scales || (b && !w) || (!kept != !kept_scales) || (!kept != !rstd)) return MXFP8_ERR_NULL;
+  if (!ld_ok(ldx, cols) || !ld_ok(ldy, cols) || (kept && !ld_ok(ldk, cols))) return MXFP8_ERR_LD;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(b) || !aligned16(y) || !aligned16(kept) || ((uintptr_t)rstd & 3))
+    return MXFP8_ERR_ALIGN;
+  if (shared({y, y_scales, kept, kept_scales, rstd}, {x, w, b})) return MXFP8_ERR_ALIAS;
+  (void)hipGetLastError();
+  mxfp8::launch_mx_layernorm_forward(x, x_dtype, rows, cols, ldx, w, b, eps, fmt, rule, y, ldy, y_scales, kept, ldk,
+                                     kept_scales, rstd, (hipStream_t)stream);
+  return launch_status();
+}
+
+int64_t mx_layernorm_backward_workspace(int64_t rows, int64_t cols) {
+  if (!extents(rows, cols) || cols % 32 != 0 || cols > mxfp8::kMaxNormCols || cols == 0) return 0;
+  return mxfp8::layernorm_backward_parts(rows, cols) * 2 * cols * (int64_t)sizeof(float);
+}
+
+int mx_layernorm_backward(const uint8_t* kept, int64_t ldk, const uint8_t* kept_scales, const float* rstd, int fmt,
+                          const float* w, const void* dy, int dtype, int64_t lddy, int64_t rows, int64_t cols,
+                          void* dx, int64_t lddx, float* dw, float* db, void* workspace, void* stream) {
+  if (!real(dtype) || !fp8(fmt)) return MXFP8_ERR_ENUM;
+  if (!extents(rows, cols) || cols % 32 != 0 || cols > mxfp8::kMaxNormCols) return MXFP8_ERR_SHAPE;
+  if (cols == 0) return MXFP8_OK;
+  if (!dw != !db || (rows > 0 && (!kept || !kept_scales || !rstd || !dy || !dx || (dw && !workspace))))
+    return MXFP8_ERR_NULL;
+  if (rows > 0 && (!ld_ok(ldk, cols) || !ld_ok(lddy, cols) || !ld_ok(lddx, cols))) return MXFP8_ERR_LD;
+  if (!aligned16(kept) || !aligned16(dy) || !aligned16(dx) || !aligned16(w) || !aligned16(dw) || !aligned16(db) ||
+      !aligned16(workspace) || ((uintptr_t)rstd & 3))
+    return MXFP8_ERR_ALIGN;
+  if (shared({dx, dw, db, workspace}, {kept, kept_scales, rstd, w, dy})) return MXFP8_ERR_ALIAS;
+  (void)hipGetLastError();
+  mxfp8::launch_mx_layernorm_backward(kept, ldk, kept_scales, rstd, fmt, w, dy, dtype, lddy, rows, cols, dx, lddx, dw,
+                                      db, static_cast<float*>(workspace), (hipStream_t)stream);
+  return launch_status();
+}
+
 }  // extern "C"

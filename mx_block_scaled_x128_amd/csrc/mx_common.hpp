@@ -215,6 +215,20 @@ __device__ __forceinline__ void mx_unpack(const MxRaw<float>& r, float (&f)[8]) 
   f[4] = r.b.x; f[5] = r.b.y; f[6] = r.b.z; f[7] = r.b.w;
 }
 
+// The words of a row as read, once more: without this the compiler keeps the converted
+// values of the first pass for the second, twice the registers.
+__device__ __forceinline__ void again(MxRaw<uint16_t>& r) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" : "+v"(r.v));
+#endif
+}
+__device__ __forceinline__ void again(MxRaw<float>&) {}
+__device__ __forceinline__ void again(uint2& c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" : "+v"(c.x), "+v"(c.y));
+#endif
+}
+
 // A row (or any run below 2 GiB) behind a buffer descriptor: accesses are a
 // lane's 32-bit offset plus a uniform one, so the offsets of a lane's units
 // cost one register per tensor and not two per unit.  A lane offset of

@@ -36,6 +36,16 @@ void launch_mx_rmsnorm_backward(const uint8_t* kept, int64_t ldk, const uint8_t*
                                 const float* w, const void* dy, int dtype, int64_t lddy, int64_t rows, int64_t cols,
                                 void* dx, int64_t lddx, float* dw, float* workspace, int64_t parts,
                                 hipStream_t stream);
+// LayerNorm; kept, b, or w and b may be null.  cols % 32 == 0, cols <= kMaxNormCols.
+void launch_mx_layernorm_forward(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ldx, const float* w,
+                                 const float* b, float eps, int fmt, int rule, uint8_t* y, int64_t ldy, uint8_t* ys,
+                                 uint8_t* kept, int64_t ldk, uint8_t* ks, float* rstd, hipStream_t stream);
+// Partial sums of dw and db that the backward pass leaves in its workspace (rows of 2 cols floats).
+int64_t layernorm_backward_parts(int64_t rows, int64_t cols);
+// dw and db may both be null.
+void launch_mx_layernorm_backward(const uint8_t* kept, int64_t ldk, const uint8_t* ks, const float* rstd, int fmt,
+                                  const float* w, const void* dy, int dtype, int64_t lddy, int64_t rows, int64_t cols,
+                                  void* dx, int64_t lddx, float* dw, float* db, float* workspace, hipStream_t stream);
 // C = A B^T, B in E2M1, scales per 32 of K.  K % 128 == 0, M, N >= 1, scale pointers 4-byte aligned.
 void launch_mxfp4_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, int a_fmt, const uint8_t* sa,
                        const uint8_t* b, int64_t ldb, const uint8_t* sb, void* c, int64_t ldc, int c_dtype,

@@ -28,6 +28,9 @@ struct Library {
   decltype(&::mx_rmsnorm_forward) mx_rmsnorm_forward;
   decltype(&::mx_rmsnorm_backward) mx_rmsnorm_backward;
   decltype(&::mx_rmsnorm_backward_workspace) mx_rmsnorm_backward_workspace;
+  decltype(&::mx_layernorm_forward) mx_layernorm_forward;
+  decltype(&::mx_layernorm_backward) mx_layernorm_backward;
+  decltype(&::mx_layernorm_backward_workspace) mx_layernorm_backward_workspace;
 } lib;
 
 bool bound = false;
@@ -52,6 +55,9 @@ void bind(const std::string& path) {
   MXFP8_FIND(mx_rmsnorm_forward);
   MXFP8_FIND(mx_rmsnorm_backward);
   MXFP8_FIND(mx_rmsnorm_backward_workspace);
+  MXFP8_FIND(mx_layernorm_forward);
+  MXFP8_FIND(mx_layernorm_backward);
+  MXFP8_FIND(mx_layernorm_backward_workspace);
 #undef MXFP8_FIND
   lib = all;
   bound = true;
@@ -135,10 +141,11 @@ void format(int fmt, const char* name, bool with_e2m1) {
           with_e2m1 ? ", E5M2 or E2M1" : " or E5M2", ", got ", fmt);
 }
 
-// All tensors on the current device; its index.
+// All tensors (null: none) on the current device; its index.
 int device_of(std::initializer_list<const at::Tensor*> all) {
   int dev = -1;
   for (const at::Tensor* t : all) {
+    if (!t) continue;
     REQUIRE(t->is_cuda(), "expected a CUDA tensor, got device ", t->device());
     const int i = t->get_device();
     REQUIRE(dev < 0 || i == dev, "tensors are on cuda:", dev, " and cuda:", i);
@@ -353,6 +360,58 @@ py::tuple rmsnorm_mx_backward(const at::Tensor& k, const at::Tensor& ks, const a
   return py::make_tuple(dx, dw);
 }
 
+const at::Tensor* given(const c10::optional<at::Tensor>& t) { return t.has_value() ? &*t : nullptr; }
+float* floats(const at::Tensor* t) { return t ? static_cast<float*>(t->data_ptr()) : nullptr; }
+
+py::tuple layernorm_mx(const at::Tensor& x, const c10::optional<at::Tensor>& w, const c10::optional<at::Tensor>& b,
+                       double eps, int fmt, int rule, bool keep, const py::object& stream) {
+  format(fmt, "fmt", false);
+  real_matrix(x, "x");
+  const int64_t rows = x.size(0), cols = x.size(1);
+  blocks32(cols, "x");
+  if (w) vector(*w, "w", cols);
+  REQUIRE(w || !b, "b without w");
+  if (b) vector(*b, "b", cols);
+  const Place on(stream, device_of({&x, given(w), given(b)}));
+  at::Tensor y = on.fresh({rows, cols}, at::kByte), ys = on.fresh({rows, cols / 32}, at::kByte), k, ks, r;
+  if (keep) {
+    k = on.fresh({rows, cols}, at::kByte);
+    ks = on.fresh({rows, cols / 32}, at::kByte);
+    r = on.fresh({rows}, at::kFloat);
+  }
+  status(lib.mx_layernorm_forward(ptr(x), real_type(x), rows, cols, ld(x), floats(given(w)), floats(given(b)),
+                                  (float)eps, fmt, rule, bytes(y), cols, bytes(ys), keep ? bytes(k) : nullptr, cols,
+                                  keep ? bytes(ks) : nullptr, keep ? floats(&r) : nullptr, on.stream()),
+         "mx_layernorm_forward");
+  if (!keep) return py::make_tuple(y, ys);
+  return py::make_tuple(y, ys, k, ks, r);
+}
+
+py::tuple layernorm_mx_backward(const at::Tensor& k, const at::Tensor& ks, const at::Tensor& r, int fmt,
+                                const c10::optional<at::Tensor>& w, const at::Tensor& dy, const py::object& stream) {
+  format(fmt, "kept.fmt", false);
+  const int64_t cols = codes(k, fmt, "kept.codes"), rows = k.size(0);
+  blocks32(cols, "kept.codes");
+  scales(ks, "kept.scales", rows, cols / 32);
+  vector(r, "kept.rstd", rows);
+  if (w) vector(*w, "w", cols);
+  real_matrix(dy, "dy");
+  shape(dy, "dy", rows, cols);
+  const Place on(stream, device_of({&k, &ks, &r, given(w), &dy}));
+  at::Tensor dx = on.fresh({rows, cols}, dy.scalar_type()), dw, db, work;
+  if (w) {
+    dw = on.fresh({cols}, at::kFloat);
+    db = on.fresh({cols}, at::kFloat);
+    work = on.scratch({lib.mx_layernorm_backward_workspace(rows, cols)}, at::kByte);
+  }
+  status(lib.mx_layernorm_backward(bytes(k), ld(k), bytes(ks), floats(&r), fmt, floats(given(w)), ptr(dy),
+                                   real_type(dy), ld(dy), rows, cols, ptr(dx), cols, w ? floats(&dw) : nullptr,
+                                   w ? floats(&db) : nullptr, w ? ptr(work) : nullptr, on.stream()),
+         "mx_layernorm_backward");
+  if (!w) return py::make_tuple(dx, py::none(), py::none());
+  return py::make_tuple(dx, dw, db);
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_mx_tensors, m) {
@@ -366,4 +425,6 @@ PYBIND11_MODULE(_mx_tensors, m) {
   m.def("swiglu_mx_backward", once_bound(&swiglu_mx_backward));
   m.def("rmsnorm_mx", once_bound(&rmsnorm_mx));
   m.def("rmsnorm_mx_backward", once_bound(&rmsnorm_mx_backward));
+  m.def("layernorm_mx", once_bound(&layernorm_mx));
+  m.def("layernorm_mx_backward", once_bound(&layernorm_mx_backward));
 }
