@@ -480,6 +480,70 @@ int mx_layernorm_backward(const uint8_t* kept, int64_t ldk, const uint8_t* kept_
 /* Bytes of workspace; 0 for extents that mx_layernorm_backward refuses or that need none. */
 int64_t mx_layernorm_backward_workspace(int64_t rows, int64_t cols);
 
+/*
+ * Low-rank adapters of many requests beside a shared MXFP4 product.  Adapter a
+ * adds up[a] (alpha[a] down[a] x) to W x; row m of the activations takes the
+ * adapter ids[m].  The three entry points below share these arguments:
+ *   ids:      [M] int32; an id outside 0 .. adapters - 1 (-1, say): no adapter.
+ *   rank:     a multiple of 8, 8 to 256; adapters of lower rank are filled up
+ *             with zeros.
+ *   down, up: bf16, adapter a's matrix at down + a * down_stride ([rank][ldd >= K])
+ *             and up + a * up_stride ([N][ldu >= rank]); strides and leading
+ *             dimensions in elements, multiples of 8, ldd and ldu <= 2^22.
+ *   alpha:    [adapters] fp32, or NULL: ones.
+ *   p:        [M][rank] fp32, dense, 16-byte aligned.
+ * M is at most 2^27 and adapters 2^30.  What an adapter's values or a row's are
+ * (infinities and NaN included) reaches no other adapter's rows.
+ *
+ * The data gradient of such a layer is the same product: dx = g W + down^T u,
+ * u = alpha up^T g.  It takes the transposed weight and, in the place of down and up, the
+ * transposed up ([rank][N]) and the transposed down ([K][rank]).
+ */
+
+/*
+ * mx_adapter_project -- p[m] = alpha[a] * down[a] x[m], a = ids[m]; zeros for a
+ * row without an adapter.
+ *   a: [M][lda] codes of a_fmt (E4M3, E5M2 or E2M1), a_scales [M][K / 32].
+ * Requires K % 128 == 0, 4-byte aligned a_scales, lda <= 2^22.  Products are
+ * exact and added up in fp32.
+ */
+int mx_adapter_project(int64_t M, int64_t K, const uint8_t* a, int64_t lda, int a_fmt, const uint8_t* a_scales,
+                       const int32_t* ids, int64_t adapters, int64_t rank, const uint16_t* down, int64_t ldd,
+                       int64_t down_stride, const float* alpha, float* p, void* stream);
+
+/*
+ * mxfp4_gemm_adapted -- mxfp4_gemm and each row's adapter:
+ *   p[m] = alpha[a] * down[a] x[m],  C[m] = W x[m] + up[a] p[m],  a = ids[m],
+ * x[m] row m of A and W = B.  p is an output too (the gradient of up needs it);
+ * its 24 bits enter the second product, which is added in fp32 before C is
+ * rounded.  All other arguments and requirements are those of mxfp4_gemm.
+ * With N == 0 p is computed alone.
+ */
+int mxfp4_gemm_adapted(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, int a_fmt,
+                       const uint8_t* a_scales, const uint8_t* b, int64_t ldb, const uint8_t* b_scales,
+                       const int32_t* ids, int64_t adapters, int64_t rank, const uint16_t* down, int64_t ldd,
+                       int64_t down_stride, const uint16_t* up, int64_t ldu, int64_t up_stride, const float* alpha,
+                       float* p, void* c, int64_t ldc, int c_dtype, void* stream);
+
+/*
+ * mx_adapter_grad -- grad[a] = the sum over the rows m with ids[m] == a of
+ * p[m] (x) z[m]: of down with the data gradient's u for p and the layer's input
+ * for z; of up, with transposed != 0, with the forward pass's p and the
+ * output's gradient for z.
+ *   z: [M][ldz] codes of z_fmt (E4M3, E5M2 or E2M1), z_scales [M][C / 32].
+ *   grad: [adapters][rank][C] fp32, or [adapters][C][rank] if transposed; zeros
+ *         for an adapter without rows.  16-byte aligned.
+ *   workspace: mx_adapter_grad_workspace(M, C, rank, adapters) bytes, 16-byte
+ *         aligned, used only during the call; may be NULL where that is 0.
+ * Requires C % 32 == 0 and ldz <= 2^22.  Sums are in fp32 and in a fixed order:
+ * the same inputs give the same bits.
+ */
+int mx_adapter_grad(int64_t M, int64_t C, const uint8_t* z, int64_t ldz, int z_fmt, const uint8_t* z_scales,
+                    const float* p, int64_t rank, const int32_t* ids, int64_t adapters, int transposed, float* grad,
+                    void* workspace, void* stream);
+/* Bytes of workspace; 0 for extents that mx_adapter_grad refuses or that need none. */
+int64_t mx_adapter_grad_workspace(int64_t M, int64_t C, int64_t rank, int64_t adapters);
+
 /* Static description of a status code (never NULL). */
 const char* mxfp8_status_string(int status);
 

@@ -13,7 +13,8 @@ Low-level entry points carry the C names and signatures (pointers as ints):
   mxfp4_quantize, mx_dequantize, mx_quantize_t, mx_requantize_t, mxfp4_gemm,
   mx_swiglu_forward, mx_swiglu_backward, mx_rmsnorm_forward,
   mx_rmsnorm_backward, mx_rmsnorm_backward_workspace, mx_layernorm_forward,
-  mx_layernorm_backward, mx_layernorm_backward_workspace,
+  mx_layernorm_backward, mx_layernorm_backward_workspace, mx_adapter_project,
+  mxfp4_gemm_adapted, mx_adapter_grad, mx_adapter_grad_workspace,
   mxfp8_status_string, mxfp8_version.
 Tensor conveniences allocate outputs with torch and call them:
   quantize_token, quantize_block, quantize_token_dual, quantize_block_dual,
@@ -21,7 +22,8 @@ Tensor conveniences allocate outputs with torch and call them:
   gemm_f32s, mx_scaled_gemm, gaussws, quantize_mxfp4, dequantize_mx,
   quantize_mx_t, requantize_mx_t, mxfp4_scaled_gemm, swiglu_mx,
   swiglu_mx_backward, rmsnorm_mx, rmsnorm_mx_backward, layernorm_mx,
-  layernorm_mx_backward.
+  layernorm_mx_backward, adapter_project_mx, mxfp4_adapted_gemm,
+  adapter_grad_mx.
 """
 import collections
 import ctypes
@@ -43,6 +45,8 @@ __all__ = [
     "swiglu_mx", "swiglu_mx_backward", "SwigluKept", "rmsnorm_mx", "rmsnorm_mx_backward", "RmsnormKept",
     "mx_layernorm_forward", "mx_layernorm_backward", "mx_layernorm_backward_workspace", "layernorm_mx",
     "layernorm_mx_backward", "LayernormKept",
+    "mx_adapter_project", "mxfp4_gemm_adapted", "mx_adapter_grad", "mx_adapter_grad_workspace", "adapter_project_mx",
+    "mxfp4_adapted_gemm", "adapter_grad_mx",
 ]
 
 # enum values of include/mxfp8.h
@@ -116,12 +120,19 @@ def load_library():
         lib.mx_layernorm_forward.argtypes = [P, I, I64, I64, I64, P, P, F, I, I, P, I64, P, P, I64, P, P, P]
         lib.mx_layernorm_backward.argtypes = [P, I64, P, P, I, P, P, I, I64, I64, I64, P, I64, P, P, P, P]
         lib.mx_layernorm_backward_workspace.argtypes = [I64, I64]
+        lib.mx_adapter_project.argtypes = [I64, I64, P, I64, I, P, P, I64, I64, P, I64, I64, P, P, P]
+        lib.mxfp4_gemm_adapted.argtypes = [I64, I64, I64, P, I64, I, P, P, I64, P, P, I64, I64, P, I64, I64, P, I64,
+                                           I64, P, P, P, I64, I, P]
+        lib.mx_adapter_grad.argtypes = [I64, I64, P, I64, I, P, P, I64, P, I64, I, P, P, P]
+        lib.mx_adapter_grad_workspace.argtypes = [I64, I64, I64, I64]
         for f in (lib.mxfp4_quantize, lib.mx_dequantize, lib.mx_quantize_t, lib.mx_requantize_t, lib.mxfp4_gemm,
                   lib.mx_swiglu_forward, lib.mx_swiglu_backward, lib.mx_rmsnorm_forward, lib.mx_rmsnorm_backward,
-                  lib.mx_layernorm_forward, lib.mx_layernorm_backward):
+                  lib.mx_layernorm_forward, lib.mx_layernorm_backward, lib.mx_adapter_project,
+                  lib.mxfp4_gemm_adapted, lib.mx_adapter_grad):
             f.restype = I
         lib.mx_rmsnorm_backward_workspace.restype = I64
         lib.mx_layernorm_backward_workspace.restype = I64
+        lib.mx_adapter_grad_workspace.restype = I64
         lib.mxfp8_status_string.argtypes = [I]
         lib.mxfp8_status_string.restype = ctypes.c_char_p
         lib.mxfp8_version.argtypes = []
@@ -246,6 +257,27 @@ def mx_layernorm_backward(kept, ldk, kept_scales, rstd, fmt, w, dy, dtype, lddy,
 
 def mx_layernorm_backward_workspace(rows, cols):
     return load_library().mx_layernorm_backward_workspace(rows, cols)
+
+
+def mx_adapter_project(M, K, a, lda, a_fmt, a_scales, ids, adapters, rank, down, ldd, down_stride, alpha, p, stream):
+    return load_library().mx_adapter_project(M, K, a, lda, a_fmt, a_scales, ids, adapters, rank, down, ldd, down_stride,
+                                             alpha, p, stream)
+
+
+def mxfp4_gemm_adapted(M, N, K, a, lda, a_fmt, a_scales, b, ldb, b_scales, ids, adapters, rank, down, ldd, down_stride,
+                       up, ldu, up_stride, alpha, p, c, ldc, c_dtype, stream):
+    return load_library().mxfp4_gemm_adapted(M, N, K, a, lda, a_fmt, a_scales, b, ldb, b_scales, ids, adapters, rank,
+                                             down, ldd, down_stride, up, ldu, up_stride, alpha, p, c, ldc, c_dtype,
+                                             stream)
+
+
+def mx_adapter_grad(M, C, z, ldz, z_fmt, z_scales, p, rank, ids, adapters, transposed, grad, workspace, stream):
+    return load_library().mx_adapter_grad(M, C, z, ldz, z_fmt, z_scales, p, rank, ids, adapters, transposed, grad,
+                                          workspace, stream)
+
+
+def mx_adapter_grad_workspace(M, C, rank, adapters):
+    return load_library().mx_adapter_grad_workspace(M, C, rank, adapters)
 
 
 def mxfp8_status_string(status):
@@ -745,3 +777,28 @@ def layernorm_mx(x, w, b, eps, fmt=E4M3, rule=RULE_CEIL, keep=True, stream=None)
 def layernorm_mx_backward(kept, w, dy, stream=None):
     """(dx [rows][cols] of dy's dtype, dw and db [cols] float32) at the kept values; w None: (dx, None, None)."""
     return (_tensors or _ops()).layernorm_mx_backward(kept.codes, kept.scales, kept.rstd, kept.fmt, w, dy, stream)
+
+
+# Low-rank adapters of many requests: down [adapters][rank][K] and up [adapters][N][rank] in bf16 (rows and
+# adapters may be strided: multiples of 8), rank a multiple of 8 up to 256; ids [rows] int32 names each row's
+# adapter, any id outside 0 .. adapters - 1 none; alpha [adapters] float32 or None (ones).
+
+def adapter_project_mx(a, a_scales, a_fmt, down, ids, alpha=None, stream=None):
+    """p [rows][rank] float32: row m is alpha[i] * down[i] @ a[m], i = ids[m], or zeros without an adapter.
+    a as for mxfp4_scaled_gemm."""
+    return (_tensors or _ops()).adapter_project_mx(a, a_scales, a_fmt, down, ids, alpha, stream)
+
+
+def mxfp4_adapted_gemm(a, a_scales, a_fmt, b, b_scales, down, up, ids, alpha=None, out_dtype=None, out=None, stream=None):
+    """(c, p): mxfp4_scaled_gemm's product with each row's adapter added, c[m] = a[m] B^T + p[m] up[ids[m]]^T, and p
+    as of adapter_project_mx.  The data gradient is the same call with the output's gradient for a, the transposed
+    weight for b, up^T for down and down^T for up; its second result is then what adapter_grad_mx takes for down."""
+    return (_tensors or _ops()).mxfp4_adapted_gemm(a, a_scales, a_fmt, b, b_scales, down, up, ids, alpha, out_dtype, out,
+                                                   stream)
+
+
+def adapter_grad_mx(p, z, z_scales, z_fmt, ids, adapters, transposed=False, stream=None):
+    """The sums of p[m]^T z[m] over each adapter's rows, float32 [adapters][rank][cols] ([cols][rank] if transposed):
+    the gradient of down from the data gradient's p and the layer's input z, and that of up (transposed) from
+    the forward pass's p and the output's gradient z.  z holds MX codes along rows."""
+    return (_tensors or _ops()).adapter_grad_mx(p, z, z_scales, z_fmt, ids, adapters, transposed, stream)

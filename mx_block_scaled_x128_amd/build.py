@@ -3,7 +3,7 @@ _mx_tensors.so, the Python extension with the MX operators' tensor functions.
 
 The sources compile to objects in parallel (the GEMM once per pair of operand
 formats, plus its host dispatch; the MXFP4 product once per format of its left
-operand), which hipcc then links into the library.
+operand, without and with adapters), which hipcc then links into the library.
 
 Usage: python -m mx_block_scaled_x128_amd.build   (always recompiles)
 """
@@ -23,12 +23,13 @@ TENSORS = os.path.join(HERE, "_mx_tensors.so")
 ARCH = "gfx950"
 # (source, extra flags, object name)
 UNITS = [("api.cpp", [], "api"), ("mx_api.cpp", [], "mx_api"), ("mx_quant.hip", [], "mx_quant"),
-         ("mx_act.hip", [], "mx_act"), ("mx_layernorm.hip", [], "mx_layernorm"),
+         ("mx_act.hip", [], "mx_act"), ("mx_layernorm.hip", [], "mx_layernorm"), ("mx_adapters.hip", [], "mx_adapters"),
          ("mxfp4_gemm.hip", ["-DMXFP4_GEMM_FMT=-1"], "mxfp4_gemm_dispatch"),
          ("quant.hip", [], "quant"), ("gaussws.hip", [], "gaussws"),
          ("gemm.hip", ["-DMXFP8_GEMM_FMT=-1"], "gemm_dispatch")] + \
         [("gemm.hip", ["-DMXFP8_GEMM_FMT=%d" % k], "gemm_fmt%d" % k) for k in range(4)] + \
-        [("mxfp4_gemm.hip", ["-DMXFP4_GEMM_FMT=%d" % k], "mxfp4_gemm_fmt%d" % k) for k in range(3)]
+        [("mxfp4_gemm.hip", ["-DMXFP4_GEMM_FMT=%d" % k, "-DMXFP4_GEMM_ADAPT=%d" % a],
+          "mxfp4_gemm_fmt%d%s" % (k, "_adapted" if a else "")) for k in range(3) for a in range(2)]
 
 FLAGS = [
     "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC",

@@ -41,6 +41,21 @@ bool shared(std::initializer_list<const void*> outs, std::initializer_list<const
 
 int launch_status() { return hipGetLastError() == hipSuccess ? MXFP8_OK : MXFP8_ERR_DEVICE; }
 
+// Rows, adapters and their rank.
+bool adapter_extents(int64_t M, int64_t adapters, int64_t rank) {
+  return M >= 0 && M <= mxfp8::kMaxAdapterRows && adapters >= 0 && adapters <= INT32_MAX / 2 && rank >= 8 &&
+         rank <= mxfp8::kMaxRank && rank % 8 == 0;
+}
+// Leading dimension of an adapter's matrix, and the stride from one to the next.
+bool adapter_ld(int64_t ld, int64_t row, int64_t stride) {
+  return ld >= row && ld % 8 == 0 && ld <= kMaxGemmLd && stride >= 0 && stride % 8 == 0;
+}
+bool grad_extents(int64_t M, int64_t C, int64_t rank, int64_t adapters) {
+  if (!adapter_extents(M, adapters, rank) || C < 0 || C > INT32_MAX / 2 || C % 32 != 0) return false;
+  // A launch takes fewer than 2^32 threads.
+  return C == 0 || adapters == 0 || mxfp8::adapter_grad_groups(M, C, rank, adapters) < (int64_t(1) << 24);
+}
+
 // Extents of the transposing quantizers.
 int transposed_extents(int64_t rows, int64_t cols, int64_t rows_out, int64_t multiple) {
   if (!extents(rows, cols) || rows_out < rows || rows_out > INT32_MAX) return MXFP8_ERR_SHAPE;
@@ -249,6 +264,81 @@ int mx_layernorm_backward(const uint8_t* kept, int64_t ldk, const uint8_t* kept_
   (void)hipGetLastError();
   mxfp8::launch_mx_layernorm_backward(kept, ldk, kept_scales, rstd, fmt, w, dy, dtype, lddy, rows, cols, dx, lddx, dw,
                                       db, static_cast<float*>(workspace), (hipStream_t)stream);
+  return launch_status();
+}
+
+int mx_adapter_project(int64_t M, int64_t K, const uint8_t* a, int64_t lda, int a_fmt, const uint8_t* a_scales,
+                       const int32_t* ids, int64_t adapters, int64_t rank, const uint16_t* down, int64_t ldd,
+                       int64_t down_stride, const float* alpha, float* p, void* stream) {
+  if (!element(a_fmt)) return MXFP8_ERR_ENUM;
+  if (!adapter_extents(M, adapters, rank) || K < 0 || K > INT32_MAX / 2 || K % 128 != 0) return MXFP8_ERR_SHAPE;
+  if (M == 0) return MXFP8_OK;
+  if (!p || !ids || (K > 0 && (!a || !a_scales || (adapters > 0 && !down)))) return MXFP8_ERR_NULL;
+  if (K > 0) {
+    if (!ld_ok(lda, code_bytes(K, a_fmt)) || lda > kMaxGemmLd) return MXFP8_ERR_LD;
+    if (adapters > 0 && !adapter_ld(ldd, K, down_stride)) return MXFP8_ERR_LD;
+  }
+  if (!aligned16(a) || !aligned16(down) || !aligned16(p) || (((uintptr_t)a_scales | (uintptr_t)ids | (uintptr_t)alpha) & 3))
+    return MXFP8_ERR_ALIGN;
+  if (shared({p}, {a, a_scales, ids, down, alpha})) return MXFP8_ERR_ALIAS;
+  (void)hipGetLastError();
+  mxfp8::launch_mx_adapter_project(M, K, a, lda, a_fmt, a_scales, ids, adapters, rank, down, ldd, down_stride, alpha, p,
+                                   (hipStream_t)stream);
+  return launch_status();
+}
+
+int mxfp4_gemm_adapted(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, int a_fmt,
+                       const uint8_t* a_scales, const uint8_t* b, int64_t ldb, const uint8_t* b_scales,
+                       const int32_t* ids, int64_t adapters, int64_t rank, const uint16_t* down, int64_t ldd,
+                       int64_t down_stride, const uint16_t* up, int64_t ldu, int64_t up_stride, const float* alpha,
+                       float* p, void* c, int64_t ldc, int c_dtype, void* stream) {
+  if (!element(a_fmt) || !real(c_dtype)) return MXFP8_ERR_ENUM;
+  if (!adapter_extents(M, adapters, rank) || N < 0 || K < 0) return MXFP8_ERR_SHAPE;
+  if (N > INT32_MAX / 2 || K > INT32_MAX / 2 || K % 128 != 0) return MXFP8_ERR_SHAPE;
+  if (M == 0) return MXFP8_OK;
+  if (!p || !ids || (N > 0 && !c)) return MXFP8_ERR_NULL;
+  if (K > 0 && (!a || !a_scales || (adapters > 0 && !down) || (N > 0 && (!b || !b_scales)))) return MXFP8_ERR_NULL;
+  if (N > 0 && adapters > 0 && !up) return MXFP8_ERR_NULL;
+  if (N > 0 && !ld_ok(ldc, N)) return MXFP8_ERR_LD;
+  if (K > 0) {
+    if (!ld_ok(lda, code_bytes(K, a_fmt)) || lda > kMaxGemmLd) return MXFP8_ERR_LD;
+    if (N > 0 && (!ld_ok(ldb, K / 2) || ldb > kMaxGemmLd)) return MXFP8_ERR_LD;
+    if (adapters > 0 && !adapter_ld(ldd, K, down_stride)) return MXFP8_ERR_LD;
+  }
+  if (N > 0 && adapters > 0 && !adapter_ld(ldu, rank, up_stride)) return MXFP8_ERR_LD;
+  if (!aligned16(a) || !aligned16(b) || !aligned16(down) || !aligned16(up) || !aligned16(p) || !aligned16(c))
+    return MXFP8_ERR_ALIGN;
+  if (((uintptr_t)a_scales | (uintptr_t)b_scales | (uintptr_t)ids | (uintptr_t)alpha) & 3) return MXFP8_ERR_ALIGN;
+  if (shared({c, p}, {a, b, a_scales, b_scales, ids, down, up, alpha})) return MXFP8_ERR_ALIAS;
+  (void)hipGetLastError();
+  mxfp8::launch_mx_adapter_project(M, K, a, lda, a_fmt, a_scales, ids, adapters, rank, down, ldd, down_stride, alpha, p,
+                                   (hipStream_t)stream);
+  if (N > 0)
+    mxfp8::launch_mxfp4_gemm_adapted(M, N, K, a, lda, a_fmt, a_scales, b, ldb, b_scales, ids, adapters, rank, p, up, ldu,
+                                     up_stride, c, ldc, c_dtype, (hipStream_t)stream);
+  return launch_status();
+}
+
+int64_t mx_adapter_grad_workspace(int64_t M, int64_t C, int64_t rank, int64_t adapters) {
+  if (!grad_extents(M, C, rank, adapters) || M == 0 || C == 0 || adapters == 0) return 0;
+  return mxfp8::adapter_grad_workspace(M, C, rank, adapters);
+}
+
+int mx_adapter_grad(int64_t M, int64_t C, const uint8_t* z, int64_t ldz, int z_fmt, const uint8_t* z_scales,
+                    const float* p, int64_t rank, const int32_t* ids, int64_t adapters, int transposed, float* grad,
+                    void* workspace, void* stream) {
+  if (!element(z_fmt)) return MXFP8_ERR_ENUM;
+  if (!grad_extents(M, C, rank, adapters)) return MXFP8_ERR_SHAPE;
+  if (C == 0 || adapters == 0) return MXFP8_OK;
+  const bool work = M > 0 && mxfp8::adapter_grad_workspace(M, C, rank, adapters) > 0;
+  if (!grad || (M > 0 && (!z || !z_scales || !p || !ids)) || (work && !workspace)) return MXFP8_ERR_NULL;
+  if (M > 0 && (!ld_ok(ldz, code_bytes(C, z_fmt)) || ldz > kMaxGemmLd)) return MXFP8_ERR_LD;
+  if (!aligned16(z) || !aligned16(p) || !aligned16(grad) || !aligned16(workspace) || ((uintptr_t)ids & 3))
+    return MXFP8_ERR_ALIGN;
+  if (shared({grad, work ? workspace : nullptr}, {z, z_scales, p, ids})) return MXFP8_ERR_ALIAS;
+  (void)hipGetLastError();
+  mxfp8::launch_mx_adapter_grad(M, C, z, ldz, z_fmt, z_scales, p, rank, ids, adapters, transposed, grad, workspace,
+                                (hipStream_t)stream);
   return launch_status();
 }
 

@@ -148,6 +148,66 @@ __device__ __forceinline__ void mx_decode8(uint2 w, float factor, float (&f)[8])
 #endif
 }
 
+// Eight codes -> bf16 values under scale byte `byte`, exactly (values below
+// bf16's least subnormal, 2^-133, aside): the conversions take the scale as a
+// float of which they use the exponent field, 0 standing for 2^-127 and 255
+// giving NaN.
+typedef __bf16 mx_bf8 __attribute__((ext_vector_type(8)));
+template <int FMT>
+__device__ __forceinline__ mx_bf8 mx_bf16x8(uint32_t lo, uint32_t hi, uint32_t byte) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const float s = __uint_as_float(byte << 23);
+  nt_u32x4 o;
+  if constexpr (FMT == kE2M1) {
+    o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(lo, s, 0));
+    o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(lo, s, 1));
+    o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(lo, s, 2));
+    o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(lo, s, 3));
+  } else if constexpr (FMT == 0) {
+    o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false));
+    o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true));
+    o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, false));
+    o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, true));
+  } else {
+    o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, s, false));
+    o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, s, true));
+    o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, s, false));
+    o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, s, true));
+  }
+  return __builtin_bit_cast(mx_bf8, o);
+#else
+  return mx_bf8{};
+#endif
+}
+
+// Eight fp32 values as three bf16 parts whose sum they are: each part takes the
+// next eight bits (cut off, not rounded, so that no part overflows), so a
+// product with the three is one with all 24 bits.  An infinity gives NaN.
+struct MxParts {
+  mx_bf8 part[3];
+};
+__device__ __forceinline__ MxParts mx_parts(const float (&f)[8]) {
+  MxParts o;
+#if defined(__HIP_DEVICE_COMPILE__)
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = f[j];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    nt_u32x4 w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // the upper halves of both words
+      w[j] = __builtin_amdgcn_perm(__float_as_uint(v[2 * j + 1]), __float_as_uint(v[2 * j]), 0x07060302u);
+      v[2 * j] -= __uint_as_float(__float_as_uint(v[2 * j]) & 0xFFFF0000u);
+      v[2 * j + 1] -= __uint_as_float(__float_as_uint(v[2 * j + 1]) & 0xFFFF0000u);
+    }
+    o.part[k] = __builtin_bit_cast(mx_bf8, w);
+  }
+#endif
+  return o;
+}
+
 // Eight codes of one lane from memory: 8 bytes of FP8, 4 of E2M1.
 template <int FMT>
 __device__ __forceinline__ uint2 mx_load_codes8(const uint8_t* p) {
@@ -214,6 +274,29 @@ __device__ __forceinline__ void mx_unpack(const MxRaw<float>& r, float (&f)[8]) 
   f[0] = r.a.x; f[1] = r.a.y; f[2] = r.a.z; f[3] = r.a.w;
   f[4] = r.b.x; f[5] = r.b.y; f[6] = r.b.z; f[7] = r.b.w;
 }
+
+#if defined(__HIP_DEVICE_COMPILE__)
+template <int CTRL>
+__device__ __forceinline__ float dpp_sum(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+// Sums over 16 and over all 64 lanes, the same bits in every lane.
+__device__ __forceinline__ float sum16(float v) {
+  v = dpp_sum<DPP_QUAD_XOR1>(v);
+  v = dpp_sum<DPP_QUAD_XOR2>(v);
+  v = dpp_sum<DPP_ROW_ROR4>(v);
+  return dpp_sum<DPP_ROW_ROR8>(v);
+}
+__device__ __forceinline__ float sum64(float v) {
+  v = sum16(v);
+  const uint32_t a = __float_as_uint(v);
+  const auto p = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+  v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  const uint32_t b = __float_as_uint(v);
+  const auto q = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+}
+#endif
 
 // The words of a row as read, once more: without this the compiler keeps the converted
 // values of the first pass for the second, twice the registers.

@@ -29,27 +29,6 @@ namespace mxfp8 {
 namespace mx_layernorm_detail {
 
 #if defined(__HIP_DEVICE_COMPILE__)
-template <int CTRL>
-__device__ __forceinline__ float dpp_sum(float v) {
-  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
-}
-// Sums over 16 and over all 64 lanes, the same bits in every lane.
-__device__ __forceinline__ float sum16(float v) {
-  v = dpp_sum<DPP_QUAD_XOR1>(v);
-  v = dpp_sum<DPP_QUAD_XOR2>(v);
-  v = dpp_sum<DPP_ROW_ROR4>(v);
-  return dpp_sum<DPP_ROW_ROR8>(v);
-}
-__device__ __forceinline__ float sum64(float v) {
-  v = sum16(v);
-  const uint32_t a = __float_as_uint(v);
-  const auto p = __builtin_amdgcn_permlane16_swap(a, a, false, false);
-  v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
-  const uint32_t b = __float_as_uint(v);
-  const auto q = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-  return __uint_as_float(q[0]) + __uint_as_float(q[1]);
-}
-
 // LDS written before is read after, by all waves; loads from memory stay in flight.
 __device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 

@@ -12,23 +12,40 @@
 // result's rms in fp32 (an fp32 product of the same values 3 to 6e-8), a
 // three-hundredth of what bf16 rounds off; products in 16 bits would avoid it at
 // half the rate at most.  E2M1 pairs lose nothing.
+//
+// With adapters, row m of C starts from up[a] p[m], a = ids[m], in place of zero:
+// a few bf16 matrix instructions per tile (p in three parts, all 24 bits) while
+// the first operands are on their way.
 #include "mx_common.hpp"
 #include "mx_launch.hpp"
 
 // One translation unit can hold everything (MXFP4_GEMM_FMT undefined), or the
-// build compiles this file once per format of A in parallel (0, 1, 2) and once
-// with -1 for the host dispatch alone.
+// build compiles this file once per format of A in parallel (0, 1, 2), without
+// and with adapters (MXFP4_GEMM_ADAPT 0, 1), and once with -1 for the host
+// dispatch alone.
 #ifndef MXFP4_GEMM_FMT
 #define MXFP4_GEMM_FMT 3
 #endif
+
+#include <type_traits>
 
 namespace mxfp8 {
 
 namespace mxfp4_detail {
 
-template <int AFMT>
+struct NoAdapters {};
+// Row m gets up[ids[m]] p[m]; ids outside 0 .. adapters - 1 nothing.
+struct Adapters {
+  const int32_t* ids;
+  const float* p;       // [M][rank]
+  const uint16_t* up;   // [adapters] at `stride`, each [N][ldu] bf16
+  int64_t ldu, stride;
+  int adapters, rank;
+};
+
+template <int AFMT, typename AD>
 void gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const uint8_t* sa, const uint8_t* b,
-          int64_t ldb, const uint8_t* sb, void* c, int64_t ldc, int c_dtype, hipStream_t stream);
+          int64_t ldb, const uint8_t* sb, void* c, int64_t ldc, int c_dtype, AD ad, hipStream_t stream);
 
 #if MXFP4_GEMM_FMT >= 0
 
@@ -152,12 +169,81 @@ __host__ __device__ inline int few_rows_lds(int rows, int K) {
   return in > out ? in : out;
 }
 
-template <int AFMT, int MT, int NT, int WAVES, int U, bool ALDS, typename OutT>
+#if defined(__HIP_DEVICE_COMPILE__)
+// The next adapter that any lane's rows name, or -1; its rows are crossed off
+// with `id[i] = -1` where id[i] is it.
+template <int MT>
+__device__ __forceinline__ int next_adapter(const int (&id)[MT]) {
+  int a = -1;
+#pragma unroll
+  for (int i = MT - 1; i >= 0; --i) {
+    const uint64_t some = __ballot(id[i] >= 0);
+    if (some) a = __builtin_amdgcn_readlane(id[i], __builtin_ctzll(some));
+  }
+  return a;
+}
+// Eight values of p, zeros where `in` is false.
+__device__ __forceinline__ MxParts adapter_parts(__amdgpu_buffer_rsrc_t rp, bool in, uint32_t off) {
+  MxRaw<float> v;
+  mx_get(rp, in ? off : kOutside, 0, v);
+  float f[8];
+  mx_unpack(v, f);
+  return mx_parts(f);
+}
+
+// up p in the few-row kernel's accumulators: pieces of 32 ranks of each adapter
+// that the workgroup's rows name, dealt to the waves in turn.  A lane's four
+// results belong to one row, so rows of other adapters keep what they had,
+// whatever this one's values are.
+template <int MT, int NT, int WAVES>
+__device__ __forceinline__ void add_adapters(const Adapters& ad, int m0, int n0, int rows_a, int rows_b, int wave,
+                                             int lane, v4f (&acc)[MT][NT]) {
+  const int r = lane & 15, g = lane >> 4;
+  int id[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    id[i] = 16 * i + r < rows_a ? ad.ids[m0 + 16 * i + r] : -1;
+    if (id[i] >= ad.adapters) id[i] = -1;
+  }
+  const __amdgpu_buffer_rsrc_t rp = descriptor(reinterpret_cast<const uint8_t*>(ad.p + (int64_t)m0 * ad.rank));
+  int turn = 0;
+  for (int a = next_adapter(id); a >= 0; a = next_adapter(id)) {
+    const __amdgpu_buffer_rsrc_t ru =
+        descriptor(reinterpret_cast<const uint8_t*>(ad.up + a * ad.stride + (int64_t)n0 * ad.ldu));
+    for (int k = 8 * g; k - 8 * g < ad.rank; k += 32) {
+      if (turn++ % WAVES != wave) continue;
+      mx_bf8 u[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        u[j] = __builtin_bit_cast(mx_bf8, load16(ru, 16 * j + r < rows_b && k < ad.rank
+                                                         ? (uint32_t)((16 * j + r) * ad.ldu + k) * 2 : kOutside, 0));
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const bool mine = id[i] == a;
+        const MxParts p = adapter_parts(rp, mine && k < ad.rank, (uint32_t)((16 * i + r) * ad.rank + k) * 4);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          v4f s = acc[i][j];
+#pragma unroll
+          for (int part = 2; part >= 0; --part) s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u[j], p.part[part], s, 0, 0, 0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = mine ? s[e] : acc[i][j][e];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+      if (id[i] == a) id[i] = -1;
+  }
+}
+#endif
+
+template <int AFMT, int MT, int NT, int WAVES, int U, bool ALDS, typename OutT, typename AD>
 __global__ __launch_bounds__(WAVES * 64) void few_rows_kernel(int M, int N, int K, const uint8_t* __restrict__ A,
                                                               int64_t lda, const uint8_t* __restrict__ SA,
                                                               const uint8_t* __restrict__ B, int64_t ldb,
                                                               const uint8_t* __restrict__ SB, OutT* __restrict__ C,
-                                                              int64_t ldc) {
+                                                              int64_t ldc, AD ad) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int PARTS = AFMT == kE2M1 ? 1 : 2;  // 16-byte parts of A per lane and chunk
   constexpr int AB = 64 * PARTS;                // bytes of a chunk of a row of A
@@ -256,6 +342,10 @@ __global__ __launch_bounds__(WAVES * 64) void few_rows_kernel(int M, int N, int 
   Batch x, y;
   load(c0, x);
   load(c0 + U, y);
+  if constexpr (std::is_same_v<AD, Adapters>) {
+    add_adapters<MT, NT, WAVES>(ad, m0, n0, rows_a, rows_b, wave, lane, acc);
+    mfma_retire_pad();
+  }
   auto pin = [](Batch& v) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -313,17 +403,17 @@ __global__ __launch_bounds__(WAVES * 64) void few_rows_kernel(int M, int N, int 
 
 constexpr int kFewRowsLds = 150 * 1024;
 
-template <int AFMT, int MT, int NT, int WAVES, int U, bool ALDS>
+template <int AFMT, int MT, int NT, int WAVES, int U, bool ALDS, typename AD>
 void few_rows(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const uint8_t* sa, const uint8_t* b,
-              int64_t ldb, const uint8_t* sb, void* c, int64_t ldc, int c_dtype, hipStream_t stream) {
+              int64_t ldb, const uint8_t* sb, void* c, int64_t ldc, int c_dtype, AD ad, hipStream_t stream) {
   const dim3 grid((uint32_t)(((N + 16 * NT - 1) / (16 * NT)) * ((M + 16 * MT - 1) / (16 * MT))));
   const int lds = few_rows_lds<AFMT, MT, NT, WAVES, ALDS>((int)(M < 16 * MT ? M : 16 * MT), (int)K);
   if (c_dtype == 0)
-    hipLaunchKernelGGL((few_rows_kernel<AFMT, MT, NT, WAVES, U, ALDS, float>), grid, dim3(WAVES * 64), lds, stream,
-                       (int)M, (int)N, (int)K, a, lda, sa, b, ldb, sb, static_cast<float*>(c), ldc);
+    hipLaunchKernelGGL((few_rows_kernel<AFMT, MT, NT, WAVES, U, ALDS, float, AD>), grid, dim3(WAVES * 64), lds, stream,
+                       (int)M, (int)N, (int)K, a, lda, sa, b, ldb, sb, static_cast<float*>(c), ldc, ad);
   else
-    hipLaunchKernelGGL((few_rows_kernel<AFMT, MT, NT, WAVES, U, ALDS, uint16_t>), grid, dim3(WAVES * 64), lds, stream,
-                       (int)M, (int)N, (int)K, a, lda, sa, b, ldb, sb, static_cast<uint16_t*>(c), ldc);
+    hipLaunchKernelGGL((few_rows_kernel<AFMT, MT, NT, WAVES, U, ALDS, uint16_t, AD>), grid, dim3(WAVES * 64), lds, stream,
+                       (int)M, (int)N, (int)K, a, lda, sa, b, ldb, sb, static_cast<uint16_t*>(c), ldc, ad);
 }
 
 // ---------------------------------------------------------------------------
@@ -374,15 +464,73 @@ __device__ __forceinline__ uint32_t opaque(uint32_t x) {
   return x;
 }
 
+#if defined(__HIP_DEVICE_COMPILE__)
+// up p in a tile's accumulators (v_mfma_f32_32x32x16_bf16, whose results lie as
+// the scaled instruction's do): 16 ranks at a time of each adapter that the
+// wave's rows name.  m0, n0: the wave's first row and column.  Strips whose rows
+// all have the adapter (or lie past M) take the results as they are, others row
+// by row, so that no adapter's values reach another's rows.
+template <int MT, int NT>
+__device__ __forceinline__ void add_adapters(const Adapters& ad, int M, int N, int m0, int n0, int lane,
+                                             v16f (&acc)[MT][NT]) {
+  const int r = lane & 31, g = lane >> 5;
+  int id[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    id[i] = m0 + 32 * i + r < M ? ad.ids[m0 + 32 * i + r] : -1;
+    if (id[i] >= ad.adapters) id[i] = -1;
+  }
+  const __amdgpu_buffer_rsrc_t rp = descriptor(reinterpret_cast<const uint8_t*>(ad.p + (int64_t)m0 * ad.rank));
+  for (int a = next_adapter(id); a >= 0; a = next_adapter(id)) {
+    const __amdgpu_buffer_rsrc_t ru =
+        descriptor(reinterpret_cast<const uint8_t*>(ad.up + a * ad.stride + (int64_t)n0 * ad.ldu));
+#pragma nounroll
+    for (int k = 8 * g; k - 8 * g < ad.rank; k += 16) {
+      mx_bf8 u[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        u[j] = __builtin_bit_cast(mx_bf8, load16(ru, n0 + 32 * j + r < N && k < ad.rank
+                                                         ? (uint32_t)((32 * j + r) * ad.ldu + k) * 2 : kOutside, 0));
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const bool mine = id[i] == a;
+        const uint64_t have = __ballot(mine);
+        if (!have) continue;
+        const MxParts p = adapter_parts(rp, mine && k < ad.rank, (uint32_t)((32 * i + r) * ad.rank + k) * 4);
+        if (have == __ballot(m0 + 32 * i + r < M)) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int part = 2; part >= 0; --part)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u[j], p.part[part], acc[i][j], 0, 0, 0);
+        } else {
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            v16f s = acc[i][j];
+#pragma unroll
+            for (int part = 2; part >= 0; --part) s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u[j], p.part[part], s, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = mine ? s[e] : acc[i][j][e];
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+      if (id[i] == a) id[i] = -1;
+  }
+}
+#endif
+
 // SW: scale rows that start on 16-byte boundaries are loaded 16 bytes a lane,
 // others 4.
-template <int BM, int BN, int AFMT, bool SW, int RING, typename OutT>
+template <int BM, int BN, int AFMT, bool SW, int RING, typename OutT, typename AD>
 __device__ __forceinline__ void gemm_tile(int M, int N, int K, const uint8_t* __restrict__ A, int64_t lda,
                                           const uint8_t* __restrict__ SA, const uint8_t* __restrict__ B, int64_t ldb,
                                           const uint8_t* __restrict__ SB, OutT* __restrict__ C, int64_t ldc,
                                           int tiles_m, int tiles_n, int tile_first, int sm, int sn, int wg, int nwg,
                                           uint8_t* kbuf0, uint8_t* kbuf1, uint8_t* kbuf2, uint8_t* kbuf3,
-                                          uint8_t* sgrp) {
+                                          uint8_t* sgrp, const AD& ad) {
 #if defined(__HIP_DEVICE_COMPILE__)
   typedef Tile<BM, BN, AFMT> T;
   constexpr bool A4 = T::A4;
@@ -660,6 +808,10 @@ __device__ __forceinline__ void gemm_tile(int M, int N, int K, const uint8_t* __
   for (int q = 0; q < RING; ++q)
 #pragma unroll
     for (int item = 0; item < DMA_ITEMS; ++item) dma_item(q, q, item);
+  if constexpr (std::is_same_v<AD, Adapters>) {
+    add_adapters<MT, NT>(ad, M, N, m0 + wm * WM, n0 + wn * WN, lane, acc);
+    mfma_retire_pad();
+  }
   wait_loads_and_meet<(RING - 1) * DMA_ITEMS>();
 #pragma unroll
   for (int item = 0; item < DS_ITEMS; ++item) ds_item(0, 0, item, f0);
@@ -726,11 +878,11 @@ __device__ __forceinline__ void gemm_tile(int M, int N, int K, const uint8_t* __
 #endif
 }
 
-template <int BM, int BN, int AFMT, bool SW, int RING, typename OutT>
+template <int BM, int BN, int AFMT, bool SW, int RING, typename OutT, typename AD>
 __global__ __launch_bounds__(kTileThreads, BM == 128 && RING == 2 ? 2 : 1) void tile_kernel(
     int M, int N, int K, const uint8_t* __restrict__ A, int64_t lda, const uint8_t* __restrict__ SA,
     const uint8_t* __restrict__ B, int64_t ldb, const uint8_t* __restrict__ SB, OutT* __restrict__ C, int64_t ldc,
-    int tiles_m, int tiles_n) {
+    int tiles_m, int tiles_n, AD ad) {
 #if defined(__HIP_DEVICE_COMPILE__)
   typedef Tile<BM, BN, AFMT> T;
   __shared__ __attribute__((aligned(1024))) uint8_t kbuf0[T::PB];
@@ -739,22 +891,22 @@ __global__ __launch_bounds__(kTileThreads, BM == 128 && RING == 2 ? 2 : 1) void 
   if constexpr (RING == 4) {
     __shared__ __attribute__((aligned(1024))) uint8_t kbuf2[T::PB];
     __shared__ __attribute__((aligned(1024))) uint8_t kbuf3[T::PB];
-    gemm_tile<BM, BN, AFMT, SW, RING, OutT>(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, tiles_m, tiles_n, 0, 0, 0,
-                                            blockIdx.x, gridDim.x, kbuf0, kbuf1, kbuf2, kbuf3, sgrp);
+    gemm_tile<BM, BN, AFMT, SW, RING, OutT, AD>(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, tiles_m, tiles_n, 0, 0, 0,
+                                            blockIdx.x, gridDim.x, kbuf0, kbuf1, kbuf2, kbuf3, sgrp, ad);
   } else {
-    gemm_tile<BM, BN, AFMT, SW, RING, OutT>(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, tiles_m, tiles_n, 0, 0, 0,
-                                            blockIdx.x, gridDim.x, kbuf0, kbuf1, nullptr, nullptr, sgrp);
+    gemm_tile<BM, BN, AFMT, SW, RING, OutT, AD>(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, tiles_m, tiles_n, 0, 0, 0,
+                                            blockIdx.x, gridDim.x, kbuf0, kbuf1, nullptr, nullptr, sgrp, ad);
   }
 #endif
 }
 
 // The 256 x 256 cells past the last full round of the chip as 128 x 128
 // quadrants (first in launch order), the full rounds after them.
-template <int AFMT, bool SW, typename OutT>
+template <int AFMT, bool SW, typename OutT, typename AD>
 __global__ __launch_bounds__(kTileThreads, 1) void tail_kernel(
     int M, int N, int K, const uint8_t* __restrict__ A, int64_t lda, const uint8_t* __restrict__ SA,
     const uint8_t* __restrict__ B, int64_t ldb, const uint8_t* __restrict__ SB, OutT* __restrict__ C, int64_t ldc,
-    int tiles_m, int tiles_n, int big) {
+    int tiles_m, int tiles_n, int big, AD ad) {
 #if defined(__HIP_DEVICE_COMPILE__)
   typedef Tile<256, 256, AFMT> T;
   __shared__ __attribute__((aligned(1024))) uint8_t kbuf0[T::PB];
@@ -762,17 +914,17 @@ __global__ __launch_bounds__(kTileThreads, 1) void tail_kernel(
   __shared__ __attribute__((aligned(1024))) uint8_t sgrp[T::SGRP];
   const int nq = (int)gridDim.x - big, b = blockIdx.x;
   if (b >= nq)
-    gemm_tile<256, 256, AFMT, SW, 2, OutT>(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, tiles_m, tiles_n, 0, 0, 0, b - nq,
-                                        big, kbuf0, kbuf1, nullptr, nullptr, sgrp);
+    gemm_tile<256, 256, AFMT, SW, 2, OutT, AD>(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, tiles_m, tiles_n, 0, 0, 0, b - nq,
+                                        big, kbuf0, kbuf1, nullptr, nullptr, sgrp, ad);
   else
-    gemm_tile<128, 128, AFMT, SW, 2, OutT>(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, tiles_m, tiles_n, big, 1, 1, b, nq,
-                                        kbuf0, kbuf1, nullptr, nullptr, sgrp);
+    gemm_tile<128, 128, AFMT, SW, 2, OutT, AD>(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, tiles_m, tiles_n, big, 1, 1, b, nq,
+                                        kbuf0, kbuf1, nullptr, nullptr, sgrp, ad);
 #endif
 }
 
-template <int AFMT, bool SW, typename OutT>
+template <int AFMT, bool SW, typename OutT, typename AD>
 void tiles(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const uint8_t* sa, const uint8_t* b,
-           int64_t ldb, const uint8_t* sb, OutT* c, int64_t ldc, hipStream_t stream) {
+           int64_t ldb, const uint8_t* sb, OutT* c, int64_t ldc, AD ad, hipStream_t stream) {
   const int bm = (int)((M + 255) / 256), bn = (int)((N + 255) / 256), big = bm * bn;
   const int sm = (int)((M + 127) / 128), sn = (int)((N + 127) / 128), cus = device_cus();
   // 128 x 128 tiles while they fit on the CUs at two per CU.  At one per CU
@@ -781,27 +933,27 @@ void tiles(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const
   // pairs 38 / 57, 11.6 / 13.4); a short K is over before that pays
   // (1000x1024x1024 6.4 / 6.1, 5.8 / 5.2; 512x8960x1536 12.8 / 12.7, 9.6 / 9.8).
   if (sm * sn <= cus && K >= 1536) {
-    hipLaunchKernelGGL((tile_kernel<128, 128, AFMT, SW, 4, OutT>), dim3(sm * sn), dim3(kTileThreads), 0, stream, (int)M,
-                       (int)N, (int)K, a, lda, sa, b, ldb, sb, c, ldc, sm, sn);
+    hipLaunchKernelGGL((tile_kernel<128, 128, AFMT, SW, 4, OutT, AD>), dim3(sm * sn), dim3(kTileThreads), 0, stream, (int)M,
+                       (int)N, (int)K, a, lda, sa, b, ldb, sb, c, ldc, sm, sn, ad);
     return;
   }
   if (sm * sn <= 2 * cus) {
-    hipLaunchKernelGGL((tile_kernel<128, 128, AFMT, SW, 2, OutT>), dim3(sm * sn), dim3(kTileThreads), 0, stream, (int)M,
-                       (int)N, (int)K, a, lda, sa, b, ldb, sb, c, ldc, sm, sn);
+    hipLaunchKernelGGL((tile_kernel<128, 128, AFMT, SW, 2, OutT, AD>), dim3(sm * sn), dim3(kTileThreads), 0, stream, (int)M,
+                       (int)N, (int)K, a, lda, sa, b, ldb, sb, c, ldc, sm, sn, ad);
     return;
   }
   const int tail = big % cus;
   if (big > cus && tail > 0 && 4 * tail <= cus)
-    hipLaunchKernelGGL((tail_kernel<AFMT, SW, OutT>), dim3(big + 3 * tail), dim3(kTileThreads), 0, stream, (int)M,
-                       (int)N, (int)K, a, lda, sa, b, ldb, sb, c, ldc, bm, bn, big - tail);
+    hipLaunchKernelGGL((tail_kernel<AFMT, SW, OutT, AD>), dim3(big + 3 * tail), dim3(kTileThreads), 0, stream, (int)M,
+                       (int)N, (int)K, a, lda, sa, b, ldb, sb, c, ldc, bm, bn, big - tail, ad);
   else
-    hipLaunchKernelGGL((tile_kernel<256, 256, AFMT, SW, 2, OutT>), dim3(big), dim3(kTileThreads), 0, stream, (int)M,
-                       (int)N, (int)K, a, lda, sa, b, ldb, sb, c, ldc, bm, bn);
+    hipLaunchKernelGGL((tile_kernel<256, 256, AFMT, SW, 2, OutT, AD>), dim3(big), dim3(kTileThreads), 0, stream, (int)M,
+                       (int)N, (int)K, a, lda, sa, b, ldb, sb, c, ldc, bm, bn, ad);
 }
 
-template <int AFMT>
+template <int AFMT, typename AD>
 void gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const uint8_t* sa, const uint8_t* b,
-          int64_t ldb, const uint8_t* sb, void* c, int64_t ldc, int c_dtype, hipStream_t stream) {
+          int64_t ldb, const uint8_t* sb, void* c, int64_t ldc, int c_dtype, AD ad, hipStream_t stream) {
   // Few rows or tiles.  Up to 16 rows B crosses a CU's load path once however
   // wide it is.  Beyond, the few-row kernel is the faster one while its
   // workgroups all fit on the chip, one to a CU, since it has four times or
@@ -820,8 +972,8 @@ void gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const 
                                             : few_rows_lds<AFMT, 2, 4, 4, false>(0, (int)K)) <= kFewRowsLds;
 #define MXFP4_FEW(MT, NT, WAVES, U)                                                                           \
   (few_rows_lds<AFMT, MT, NT, WAVES, true>((int)(M < 16 * MT ? M : 16 * MT), (int)K) <= kFewRowsLds           \
-       ? few_rows<AFMT, MT, NT, WAVES, U, true>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, stream)     \
-       : few_rows<AFMT, MT, NT, WAVES, U, false>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, stream))
+       ? few_rows<AFMT, MT, NT, WAVES, U, true>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, ad, stream) \
+       : few_rows<AFMT, MT, NT, WAVES, U, false>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, ad, stream))
   if (few) {
     if (M <= 16) {
       // Two waves a workgroup where a run of K is short or the workgroups are
@@ -833,7 +985,7 @@ void gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const 
       const bool wide_a = M * (AFMT == kE2M1 ? K / 2 : K) > 32 * 1024 && n16 >= 512;
       if (wide_a) MXFP4_FEW(1, 2, 8, 2);
       else if (chunks <= 16 || (n16 >= 512 && M <= 8))  // A, 32 KB at most, always fits
-        few_rows<AFMT, 1, 1, 2, 4, true>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, stream);
+        few_rows<AFMT, 1, 1, 2, 4, true>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, ad, stream);
       else MXFP4_FEW(1, 1, 4, 4);
     } else if (pairs < 128 && M <= 48) {
       // Few workgroups of 32 x 32 (us, 16x16, 16x32 and 32x32 ones, E4M3 x
@@ -855,24 +1007,29 @@ void gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const 
     float* cf = static_cast<float*>(c);
     uint16_t* cb = static_cast<uint16_t*>(c);
     if (c_dtype == 0)
-      sw ? tiles<AFMT, true>(M, N, K, a, lda, sa, b, ldb, sb, cf, ldc, stream)
-         : tiles<AFMT, false>(M, N, K, a, lda, sa, b, ldb, sb, cf, ldc, stream);
+      sw ? tiles<AFMT, true>(M, N, K, a, lda, sa, b, ldb, sb, cf, ldc, ad, stream)
+         : tiles<AFMT, false>(M, N, K, a, lda, sa, b, ldb, sb, cf, ldc, ad, stream);
     else
-      sw ? tiles<AFMT, true>(M, N, K, a, lda, sa, b, ldb, sb, cb, ldc, stream)
-         : tiles<AFMT, false>(M, N, K, a, lda, sa, b, ldb, sb, cb, ldc, stream);
+      sw ? tiles<AFMT, true>(M, N, K, a, lda, sa, b, ldb, sb, cb, ldc, ad, stream)
+         : tiles<AFMT, false>(M, N, K, a, lda, sa, b, ldb, sb, cb, ldc, ad, stream);
   }
 #undef MXFP4_FEW
 }
 
-#define MXFP4_GEMM(FMT)                                                                                      \
-  template void gemm<FMT>(int64_t, int64_t, int64_t, const uint8_t*, int64_t, const uint8_t*, const uint8_t*, \
-                          int64_t, const uint8_t*, void*, int64_t, int, hipStream_t);
+#define MXFP4_GEMM(FMT, AD)                                                                                     \
+  template void gemm<FMT, AD>(int64_t, int64_t, int64_t, const uint8_t*, int64_t, const uint8_t*, const uint8_t*, \
+                              int64_t, const uint8_t*, void*, int64_t, int, AD, hipStream_t);
 #if MXFP4_GEMM_FMT == 3
-MXFP4_GEMM(0)
-MXFP4_GEMM(1)
-MXFP4_GEMM(2)
+MXFP4_GEMM(0, NoAdapters)
+MXFP4_GEMM(1, NoAdapters)
+MXFP4_GEMM(2, NoAdapters)
+MXFP4_GEMM(0, Adapters)
+MXFP4_GEMM(1, Adapters)
+MXFP4_GEMM(2, Adapters)
+#elif MXFP4_GEMM_ADAPT
+MXFP4_GEMM(MXFP4_GEMM_FMT, Adapters)
 #else
-MXFP4_GEMM(MXFP4_GEMM_FMT)
+MXFP4_GEMM(MXFP4_GEMM_FMT, NoAdapters)
 #endif
 #undef MXFP4_GEMM
 
@@ -881,13 +1038,30 @@ MXFP4_GEMM(MXFP4_GEMM_FMT)
 }  // namespace mxfp4_detail
 
 #if MXFP4_GEMM_FMT == 3 || MXFP4_GEMM_FMT < 0
+namespace {
+template <typename AD>
+void any_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, int a_fmt, const uint8_t* sa,
+              const uint8_t* b, int64_t ldb, const uint8_t* sb, void* c, int64_t ldc, int c_dtype, AD ad,
+              hipStream_t stream) {
+  using mxfp4_detail::gemm;
+  if (a_fmt == 0) gemm<0, AD>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, ad, stream);
+  else if (a_fmt == 1) gemm<1, AD>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, ad, stream);
+  else gemm<kE2M1, AD>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, ad, stream);
+}
+}  // namespace
+
 void launch_mxfp4_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, int a_fmt, const uint8_t* sa,
                        const uint8_t* b, int64_t ldb, const uint8_t* sb, void* c, int64_t ldc, int c_dtype,
                        hipStream_t stream) {
-  using namespace mxfp4_detail;
-  if (a_fmt == 0) gemm<0>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, stream);
-  else if (a_fmt == 1) gemm<1>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, stream);
-  else gemm<kE2M1>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, stream);
+  any_gemm(M, N, K, a, lda, a_fmt, sa, b, ldb, sb, c, ldc, c_dtype, mxfp4_detail::NoAdapters{}, stream);
+}
+
+void launch_mxfp4_gemm_adapted(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, int a_fmt,
+                               const uint8_t* sa, const uint8_t* b, int64_t ldb, const uint8_t* sb, const int32_t* ids,
+                               int64_t adapters, int64_t rank, const float* p, const uint16_t* up, int64_t ldu,
+                               int64_t stride, void* c, int64_t ldc, int c_dtype, hipStream_t stream) {
+  const mxfp4_detail::Adapters ad{ids, p, up, ldu, stride, (int)adapters, (int)rank};
+  any_gemm(M, N, K, a, lda, a_fmt, sa, b, ldb, sb, c, ldc, c_dtype, ad, stream);
 }
 
 #endif

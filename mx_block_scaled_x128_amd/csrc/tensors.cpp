@@ -31,6 +31,10 @@ struct Library {
   decltype(&::mx_layernorm_forward) mx_layernorm_forward;
   decltype(&::mx_layernorm_backward) mx_layernorm_backward;
   decltype(&::mx_layernorm_backward_workspace) mx_layernorm_backward_workspace;
+  decltype(&::mx_adapter_project) mx_adapter_project;
+  decltype(&::mxfp4_gemm_adapted) mxfp4_gemm_adapted;
+  decltype(&::mx_adapter_grad) mx_adapter_grad;
+  decltype(&::mx_adapter_grad_workspace) mx_adapter_grad_workspace;
 } lib;
 
 bool bound = false;
@@ -58,6 +62,10 @@ void bind(const std::string& path) {
   MXFP8_FIND(mx_layernorm_forward);
   MXFP8_FIND(mx_layernorm_backward);
   MXFP8_FIND(mx_layernorm_backward_workspace);
+  MXFP8_FIND(mx_adapter_project);
+  MXFP8_FIND(mxfp4_gemm_adapted);
+  MXFP8_FIND(mx_adapter_grad);
+  MXFP8_FIND(mx_adapter_grad_workspace);
 #undef MXFP8_FIND
   lib = all;
   bound = true;
@@ -412,6 +420,100 @@ py::tuple layernorm_mx_backward(const at::Tensor& k, const at::Tensor& ks, const
   return py::make_tuple(dx, dw, db);
 }
 
+// Adapters' matrices [adapters][rows][cols] in bf16, rows and adapters padded or not.
+void adapter_matrices(const at::Tensor& t, const char* name, int64_t adapters, int64_t rows, int64_t cols) {
+  REQUIRE(t.dim() == 3 && t.size(0) == adapters && t.size(1) == rows && t.size(2) == cols, name, " must have shape (",
+          adapters, ", ", rows, ", ", cols, "), got ", t.sizes());
+  REQUIRE(t.scalar_type() == at::kBFloat16, name, " must be bfloat16, got ", t.scalar_type());
+  REQUIRE(cols <= 1 || t.stride(2) == 1, name, " must have unit column stride");
+  REQUIRE(rows <= 1 || t.stride(1) >= cols, name, " rows must not overlap");
+}
+// One row, or one adapter, has no stride: the least that the C functions take.
+int64_t adapter_ld(const at::Tensor& t) { return t.size(1) > 1 ? t.stride(1) : (t.size(2) + 7) / 8 * 8; }
+int64_t adapter_stride(const at::Tensor& t) { return t.size(0) > 1 ? t.stride(0) : 0; }
+const uint16_t* bf16(const at::Tensor& t) { return static_cast<const uint16_t*>(t.data_ptr()); }
+void adapter_ids(const at::Tensor& ids, int64_t rows) {
+  REQUIRE(ids.dim() == 1 && ids.size(0) == rows && ids.scalar_type() == at::kInt && ids.is_contiguous(),
+          "ids must be a contiguous int32 vector of ", rows);
+}
+const int32_t* ints(const at::Tensor& t) { return static_cast<const int32_t*>(t.data_ptr()); }
+void adapter_rank(int64_t rank) {
+  REQUIRE(rank % 8 == 0 && rank >= 8 && rank <= 256, "the rank must be a multiple of 8 from 8 to 256, got ", rank);
+}
+// down's rank, checked with the arguments that go with it.
+int64_t adapters_of(const at::Tensor& down, int64_t K, const at::Tensor& ids, int64_t rows,
+                    const c10::optional<at::Tensor>& alpha) {
+  REQUIRE(down.dim() == 3, "down must be 3-D, got ", down.dim(), "-D");
+  adapter_rank(down.size(1));
+  adapter_matrices(down, "down", down.size(0), down.size(1), K);
+  adapter_ids(ids, rows);
+  if (alpha) vector(*alpha, "alpha", down.size(0));
+  return down.size(1);
+}
+
+at::Tensor adapter_project_mx(const at::Tensor& a, const at::Tensor& sa, int a_fmt, const at::Tensor& down,
+                              const at::Tensor& ids, const c10::optional<at::Tensor>& alpha, const py::object& stream) {
+  format(a_fmt, "a_fmt", true);
+  const int64_t K = codes(a, a_fmt, "a"), M = a.size(0);
+  REQUIRE(K % 128 == 0, "adapter_project_mx: K must be a multiple of 128, got ", K);
+  scales(sa, "a_scales", M, K / 32);
+  const int64_t rank = adapters_of(down, K, ids, M, alpha);
+  const Place on(stream, device_of({&a, &sa, &down, &ids, given(alpha)}));
+  at::Tensor p = on.fresh({M, rank}, at::kFloat);
+  status(lib.mx_adapter_project(M, K, bytes(a), ld(a), a_fmt, bytes(sa), ints(ids), down.size(0), rank, bf16(down),
+                                adapter_ld(down), adapter_stride(down), floats(given(alpha)), floats(&p), on.stream()),
+         "mx_adapter_project");
+  return p;
+}
+
+py::tuple mxfp4_adapted_gemm(const at::Tensor& a, const at::Tensor& sa, int a_fmt, const at::Tensor& b,
+                             const at::Tensor& sb, const at::Tensor& down, const at::Tensor& up, const at::Tensor& ids,
+                             const c10::optional<at::Tensor>& alpha, const c10::optional<at::ScalarType>& out_dtype,
+                             const c10::optional<at::Tensor>& out, const py::object& stream) {
+  format(a_fmt, "a_fmt", true);
+  const int64_t K = codes(a, a_fmt, "a"), kb = codes(b, MXFP8_E2M1, "b"), M = a.size(0), N = b.size(0);
+  REQUIRE(kb == K, "a has K = ", K, " but b has K = ", kb);
+  REQUIRE(K % 128 == 0, "mxfp4_adapted_gemm: K must be a multiple of 128, got ", K);
+  scales(sa, "a_scales", M, K / 32);
+  scales(sb, "b_scales", N, K / 32);
+  const int64_t rank = adapters_of(down, K, ids, M, alpha);
+  adapter_matrices(up, "up", down.size(0), N, rank);
+  if (out.has_value()) {
+    real_matrix(*out, "out");
+    shape(*out, "out", M, N);
+  }
+  const at::ScalarType type = out_dtype.value_or(at::kFloat);
+  REQUIRE(out.has_value() || type == at::kFloat || type == at::kBFloat16,
+          "out_dtype must be float32 or bfloat16, got ", type);
+  const Place on(stream, device_of({&a, &sa, &b, &sb, &down, &up, &ids, given(alpha), given(out)}));
+  at::Tensor c = out.has_value() ? *out : on.pitched(M, N, type), p = on.fresh({M, rank}, at::kFloat);
+  status(lib.mxfp4_gemm_adapted(M, N, K, bytes(a), ld(a), a_fmt, bytes(sa), bytes(b), ld(b), bytes(sb), ints(ids),
+                                down.size(0), rank, bf16(down), adapter_ld(down), adapter_stride(down), bf16(up),
+                                adapter_ld(up), adapter_stride(up), floats(given(alpha)), floats(&p), ptr(c), ld(c),
+                                real_type(c), on.stream()), "mxfp4_gemm_adapted");
+  return py::make_tuple(c, p);
+}
+
+at::Tensor adapter_grad_mx(const at::Tensor& p, const at::Tensor& z, const at::Tensor& sz, int z_fmt,
+                           const at::Tensor& ids, int64_t adapters, bool transposed, const py::object& stream) {
+  format(z_fmt, "z_fmt", true);
+  const int64_t C = codes(z, z_fmt, "z"), M = z.size(0);
+  blocks32(C, "z");
+  scales(sz, "z_scales", M, C / 32);
+  REQUIRE(p.dim() == 2 && p.size(0) == M && p.scalar_type() == at::kFloat && p.is_contiguous(),
+          "p must be a contiguous float32 matrix of ", M, " rows");
+  const int64_t rank = p.size(1);
+  adapter_rank(rank);
+  adapter_ids(ids, M);
+  REQUIRE(adapters >= 0, "adapters must not be negative, got ", adapters);
+  const Place on(stream, device_of({&p, &z, &sz, &ids}));
+  at::Tensor grad = transposed ? on.fresh({adapters, C, rank}, at::kFloat) : on.fresh({adapters, rank, C}, at::kFloat);
+  at::Tensor work = on.scratch({lib.mx_adapter_grad_workspace(M, C, rank, adapters)}, at::kByte);
+  status(lib.mx_adapter_grad(M, C, bytes(z), ld(z), z_fmt, bytes(sz), floats(&p), rank, ints(ids), adapters, transposed,
+                             floats(&grad), ptr(work), on.stream()), "mx_adapter_grad");
+  return grad;
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_mx_tensors, m) {
@@ -427,4 +529,7 @@ PYBIND11_MODULE(_mx_tensors, m) {
   m.def("rmsnorm_mx_backward", once_bound(&rmsnorm_mx_backward));
   m.def("layernorm_mx", once_bound(&layernorm_mx));
   m.def("layernorm_mx_backward", once_bound(&layernorm_mx_backward));
+  m.def("adapter_project_mx", once_bound(&adapter_project_mx));
+  m.def("mxfp4_adapted_gemm", once_bound(&mxfp4_adapted_gemm));
+  m.def("adapter_grad_mx", once_bound(&adapter_grad_mx));
 }
