@@ -492,6 +492,8 @@ int64_t mx_layernorm_backward_workspace(int64_t rows, int64_t cols);
  *             dimensions in elements, multiples of 8, ldd and ldu <= 2^22.
  *   alpha:    [adapters] fp32, or NULL: ones.
  *   p:        [M][rank] fp32, dense, 16-byte aligned.
+ *   workspace: mx_adapter_project_workspace(M, K, rank) bytes, 16-byte aligned,
+ *             used only during the call; may be NULL where that is 0.
  * M is at most 2^27 and adapters 2^30.  What an adapter's values or a row's are
  * (infinities and NaN included) reaches no other adapter's rows.
  *
@@ -509,7 +511,9 @@ int64_t mx_layernorm_backward_workspace(int64_t rows, int64_t cols);
  */
 int mx_adapter_project(int64_t M, int64_t K, const uint8_t* a, int64_t lda, int a_fmt, const uint8_t* a_scales,
                        const int32_t* ids, int64_t adapters, int64_t rank, const uint16_t* down, int64_t ldd,
-                       int64_t down_stride, const float* alpha, float* p, void* stream);
+                       int64_t down_stride, const float* alpha, float* p, void* workspace, void* stream);
+/* Bytes of workspace; 0 for extents that mx_adapter_project refuses or that need none. */
+int64_t mx_adapter_project_workspace(int64_t M, int64_t K, int64_t rank);
 
 /*
  * mxfp4_gemm_adapted -- mxfp4_gemm and each row's adapter:
@@ -523,7 +527,7 @@ int mxfp4_gemm_adapted(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_
                        const uint8_t* a_scales, const uint8_t* b, int64_t ldb, const uint8_t* b_scales,
                        const int32_t* ids, int64_t adapters, int64_t rank, const uint16_t* down, int64_t ldd,
                        int64_t down_stride, const uint16_t* up, int64_t ldu, int64_t up_stride, const float* alpha,
-                       float* p, void* c, int64_t ldc, int c_dtype, void* stream);
+                       float* p, void* c, int64_t ldc, int c_dtype, void* workspace, void* stream);
 
 /*
  * mx_adapter_grad -- grad[a] = the sum over the rows m with ids[m] == a of

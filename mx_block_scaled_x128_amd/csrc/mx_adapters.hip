@@ -36,7 +36,8 @@ __global__ __launch_bounds__(256) void project_rows_kernel(int K, const uint8_t*
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ float red[4][JT];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int groups = rank / JT, t = blockIdx.x / groups, j0 = (int)(blockIdx.x % groups) * JT;
+  const int groups = rank / JT, t = __builtin_amdgcn_readfirstlane((int)blockIdx.x / groups);
+  const int j0 = ((int)blockIdx.x - t * groups) * JT;
   float* to = p + (int64_t)t * rank + j0;
   const int a = ids[t];
   if ((uint32_t)a >= (uint32_t)adapters) {
@@ -98,111 +99,200 @@ __global__ __launch_bounds__(256) void project_rows_kernel(int K, const uint8_t*
 }
 
 // ---------------------------------------------------------------------------
-// Projection of many rows.  A workgroup takes 16 TG rows and 16 JC ranks; its
-// eight waves split K into runs of 128-wide chunks and add up through LDS in a
-// fixed order.  v_mfma_f32_16x16x32_bf16 with the adapter first: lane l holds
-// rank, or row, l & 15 and, with g = l >> 4, eight of 32 k.  Which k these are
-// is free as long as both sides agree, so a lane takes 16 (E2M1: 32) of a row in
-// one load: FP8 k = 64 s + 16 g + 8 h + i of the chunk, E2M1 32 g + 8 h + i.
+// Projection of many rows.  A workgroup takes 128 rows, 16 JC ranks and a run of
+// K's 128-wide chunks.  Chunks go straight to LDS, three buffers deep: the rows'
+// codes and scales and the adapter's ranks, 1 KB of whole row segments an
+// instruction (gathering 16 rows x 64 bytes a time costs the load path more than
+// twice as much for the same bytes), and the adapter's once for all four waves,
+// which take 32 rows each.  The runs' sums go to `part` and are joined in order.
 //
-// The rows of a tile may name several adapters: one pass over K for each, of
-// which only its own rows are stored.  Other rows' values, infinities and NaN
+// v_mfma_f32_16x16x32_bf16 with the adapter first: lane l holds rank, or row,
+// l & 15 and, with g = l >> 4, eight of 32 k.  Which k these are is free as long
+// as both sides agree, so a lane reads 16 bytes of a row at once: FP8
+// k = 64 s + 16 g + 8 h + i of the chunk, E2M1 32 g + 8 h + i.
+//
+// The rows of a tile may name several adapters: one pass over the run for each,
+// of which only its own rows are stored.  Other rows' values, infinities and NaN
 // among them, stay in columns that are dropped.
 // ---------------------------------------------------------------------------
-constexpr int kProjectWaves = 8;
-template <int FMT, int JC, int TG>
-__global__ __launch_bounds__(64 * kProjectWaves) void project_tile_kernel(
-    int M, int K, const uint8_t* __restrict__ A, int64_t lda, const uint8_t* __restrict__ SA,
-    const int32_t* __restrict__ ids, int adapters, int rank, const uint16_t* __restrict__ down, int64_t ldd,
-    int64_t stride, const float* __restrict__ alpha, float* __restrict__ p) {
+constexpr int kTileRows = 128;
+template <int FMT, int JC>
+struct ProjectTile {
+  static constexpr int XB = FMT == kE2M1 ? 64 : 128;            // bytes of a row per chunk
+  static constexpr int X = kTileRows * XB, D = 16 * JC * 256, S = 1024;  // scales: 512 bytes, and as many that nobody reads
+  static constexpr int STAGE = X + D + S;
+};
+
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int W = kProjectWaves, ROWS = 16 * TG, XL = FMT == kE2M1 ? 1 : 2;
-  __shared__ v4f red[W][JC * TG][64];
+typedef __attribute__((address_space(3))) void lds_void;
+template <int BYTES>
+__device__ __forceinline__ void load_lds(mx_rsrc r, uint8_t* to, uint32_t lane_off, uint32_t off) {
+  if constexpr (BYTES == 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)to, 16, lane_off, off, 0, 0);
+  else __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)to, 4, lane_off, off, 0, 0);
+}
+// All but the last N of this wave's loads have landed, and its LDS reads; then
+// all waves meet.
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+  static_assert(N >= 0 && N <= 63, "vmcnt");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+  asm volatile("s_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+// The next adapter that a lane's two ids name, or -1.
+__device__ __forceinline__ int next_of(int id0, int id1) {
+  const uint64_t a = __ballot(id0 >= 0), b = __ballot(id1 >= 0);
+  return a ? __builtin_amdgcn_readlane(id0, __builtin_ctzll(a)) : b ? __builtin_amdgcn_readlane(id1, __builtin_ctzll(b)) : -1;
+}
+#endif
+
+// part: [runs][M][rank]; runs == 1: p itself.
+template <int FMT, int JC>
+__global__ __launch_bounds__(256) void project_tile_kernel(int M, int K, int runs, const uint8_t* __restrict__ A,
+                                                           int64_t lda, const uint8_t* __restrict__ SA,
+                                                           const int32_t* __restrict__ ids, int adapters, int rank,
+                                                           const uint16_t* __restrict__ down, int64_t ldd,
+                                                           int64_t stride, const float* __restrict__ alpha,
+                                                           float* __restrict__ part) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef ProjectTile<FMT, JC> T;
+  // Three arrays, so that the compiler's waits for what is on its way to one do
+  // not hold up reads of another.
+  __shared__ __attribute__((aligned(1024))) uint8_t ring0[T::STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring1[T::STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring2[T::STAGE];
+  constexpr int XI = T::X / 4096, DI = T::D / 4096;  // loads of a wave and chunk; scales: one more
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int t0 = (int)blockIdx.x * ROWS, j0 = (int)blockIdx.y * (16 * JC), rows = min(ROWS, M - t0);
+  // Quotients come from the vector unit: back to scalar registers, for the descriptors.
+  const int tile = __builtin_amdgcn_readfirstlane((int)blockIdx.x / runs), run = (int)blockIdx.x - tile * runs;
+  const int t0 = tile * kTileRows, j0 = (int)blockIdx.y * (16 * JC), rows = min(kTileRows, M - t0);
   const int chunks = K >> 7, sk = K >> 5;
-  const int c0 = (int)((int64_t)chunks * wave / W), c1 = (int)((int64_t)chunks * (wave + 1) / W);
-  int id = lane < rows ? ids[t0 + lane] : -1;
-  if ((uint32_t)id >= (uint32_t)adapters) id = -1;
-  // Rows without an adapter: zeros.
-  for (int i = threadIdx.x; i < ROWS * 16 * JC; i += 64 * W) {
-    const int t = i / (16 * JC), j = j0 + i % (16 * JC);
-    if (t < rows && j < rank && (uint32_t)ids[t0 + t] >= (uint32_t)adapters) p[(int64_t)(t0 + t) * rank + j] = 0.0f;
-  }
-  const mx_rsrc rx = mx_run(A + (int64_t)t0 * lda), rs = mx_run(SA + (int64_t)t0 * sk);
-  uint32_t xo[TG], so[TG], dof[JC];
-#pragma unroll
-  for (int t = 0; t < TG; ++t) {
-    const bool in = 16 * t + r < rows;
-    xo[t] = in ? (uint32_t)((16 * t + r) * lda) + 16 * g : kNowhere;
-    so[t] = in ? (uint32_t)((16 * t + r) * sk) : kNowhere;
-  }
-#pragma unroll
-  for (int j = 0; j < JC; ++j)
-    dof[j] = j0 + 16 * j + r < rank ? (uint32_t)((16 * j + r) * ldd * 2) + (FMT == kE2M1 ? 64 : 32) * g : kNowhere;
-  struct In {
-    nt_u32x4 x[TG][XL], d[JC][4];
-    uint32_t s[TG];
+  const int per = (chunks + runs - 1) / runs, c0 = min(run * per, chunks), c1 = min(c0 + per, chunks);
+  auto id_of = [&](int t) __attribute__((always_inline)) {
+    const int id = t < rows ? ids[t0 + t] : -1;
+    return (uint32_t)id < (uint32_t)adapters ? id : -1;
   };
-  for (uint64_t todo = __ballot(id >= 0); todo;) {
-    const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-    todo &= ~__ballot(id == a);
+  int id0 = id_of(lane), id1 = id_of(64 + lane);
+  // The rows whose results this lane holds.
+  const int own[2] = {id_of(wave * 32 + r), id_of(wave * 32 + 16 + r)};
+  float* to = part + ((int64_t)run * M + t0) * rank;
+  if (runs == 1) {
+    for (int i = threadIdx.x; i < rows * 16 * JC; i += 256) {
+      const int t = i / (16 * JC), j = j0 + i % (16 * JC);
+      if (j < rank && (uint32_t)ids[t0 + t] >= (uint32_t)adapters) to[(int64_t)t * rank + j] = 0.0f;
+    }
+  }
+  int first = t0;
+  asm volatile("" : "+s"(first));  // in a scalar register: what the loop above made of t0 is not
+  const mx_rsrc rx = mx_run(A + (int64_t)first * lda), rs = mx_run(SA + (int64_t)first * sk);
+  // 16-byte units of a row sit at unit ^ swizzle(row), so that 16 rows read at
+  // one unit spread over the banks.
+  auto swz_x = [](int row) { return FMT == kE2M1 ? row >> 2 & 3 : row >> 1 & 7; };
+  auto swz_d = [](int row) { return row & 15; };
+  uint32_t xo[XI], dof[DI];
+#pragma unroll
+  for (int i = 0; i < XI; ++i) {
+    constexpr int UPR = T::XB / 16;
+    const int row = (i * 4 + wave) * (64 / UPR) + lane / UPR;
+    xo[i] = row < rows ? (uint32_t)(row * lda) + ((lane % UPR) ^ swz_x(row)) * 16 : kNowhere;
+  }
+#pragma unroll
+  for (int i = 0; i < DI; ++i) {
+    const int row = (i * 4 + wave) * 4 + (lane >> 4);
+    dof[i] = j0 + row < rank ? (uint32_t)(row * ldd * 2) + ((lane & 15) ^ swz_d(row)) * 16 : kNowhere;
+  }
+  // Scales: waves 0 and 1 take 64 rows each, the others zeros (their loads count all the same).
+  const uint32_t so = wave < 2 && wave * 64 + lane < rows ? (uint32_t)((wave * 64 + lane) * sk) : kNowhere;
+  constexpr int LOADS = XI + DI + 1;
+  for (int a = next_of(id0, id1); a >= 0; a = next_of(id0, id1)) {
     const mx_rsrc rd = mx_run(down + a * stride + j0 * ldd);
-    auto load = [&](int c, In& v) __attribute__((always_inline)) {
+    auto load = [&](uint8_t* to, int c) __attribute__((always_inline)) {
       const bool in = c < c1;
 #pragma unroll
-      for (int t = 0; t < TG; ++t) {
-        v.s[t] = __builtin_amdgcn_raw_buffer_load_b32(rs, in ? so[t] : kNowhere, c * 4, 0);
+      for (int i = 0; i < XI; ++i) load_lds<16>(rx, to + (i * 4 + wave) * 1024, in ? xo[i] : kNowhere, c * T::XB);
 #pragma unroll
-        for (int s = 0; s < XL; ++s) v.x[t][s] = get16(rx, in ? xo[t] : kNowhere, c * (64 * XL) + 64 * s);
-      }
+      for (int i = 0; i < DI; ++i) load_lds<16>(rd, to + T::X + (i * 4 + wave) * 1024, in ? dof[i] : kNowhere, c * 256);
+      load_lds<4>(rs, to + T::X + T::D + wave * 256, in ? so : kNowhere, c * 4);
+    };
+    v4f acc[JC][2];
+#pragma unroll
+    for (int j = 0; j < JC; ++j)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) acc[j][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    auto chunk = [&](const uint8_t* at) __attribute__((always_inline)) {
+      nt_u32x4 d[JC][4];
 #pragma unroll
       for (int j = 0; j < JC; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          v.d[j][q] = get16(rd, in ? dof[j] : kNowhere, c * 256 + (FMT == kE2M1 ? 16 * q : 128 * (q >> 1) + 16 * (q & 1)));
-    };
-    v4f acc[JC][TG];
+        for (int q = 0; q < 4; ++q) {
+          const int unit = FMT == kE2M1 ? 4 * g + q : 8 * (q >> 1) + 2 * g + (q & 1);
+          d[j][q] = *reinterpret_cast<const nt_u32x4*>(at + T::X + (16 * j + r) * 256 + (unit ^ swz_d(r)) * 16);
+        }
 #pragma unroll
-    for (int j = 0; j < JC; ++j)
-#pragma unroll
-      for (int t = 0; t < TG; ++t) acc[j][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    In v;
-    load(c0, v);
-    for (int c = c0; c < c1; ++c) {
-      In next;
-      load(c + 1, next);
-#pragma unroll
-      for (int t = 0; t < TG; ++t)
+      for (int t = 0; t < 2; ++t) {
+        const int row = wave * 32 + 16 * t + r;
+        const uint32_t s = *reinterpret_cast<const uint32_t*>(at + T::X + T::D + row * 4);
+        nt_u32x4 x[2];
+        x[0] = *reinterpret_cast<const nt_u32x4*>(at + row * T::XB + (g ^ swz_x(row)) * 16);
+        if constexpr (FMT != kE2M1) x[1] = *reinterpret_cast<const nt_u32x4*>(at + row * T::XB + ((4 + g) ^ swz_x(row)) * 16);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const uint32_t byte = (v.s[t] >> (FMT == kE2M1 ? 8 * g : 16 * (q >> 1) + 8 * (g >> 1))) & 255u;
-          const mx_bf8 x = FMT == kE2M1 ? mx_bf16x8<FMT>(v.x[t][0][q], 0, byte)
-                                        : mx_bf16x8<FMT>(v.x[t][(q >> 1) % XL][2 * (q & 1)],
-                                                         v.x[t][(q >> 1) % XL][2 * (q & 1) + 1], byte);
+          const uint32_t byte = (s >> (FMT == kE2M1 ? 8 * g : 16 * (q >> 1) + 8 * (g >> 1))) & 255u;
+          const mx_bf8 v = FMT == kE2M1 ? mx_bf16x8<FMT>(x[0][q], 0, byte)
+                                        : mx_bf16x8<FMT>(x[q >> 1][2 * (q & 1)], x[q >> 1][2 * (q & 1) + 1], byte);
 #pragma unroll
           for (int j = 0; j < JC; ++j)
-            acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(mx_bf8, v.d[j][q]), x, acc[j][t], 0, 0, 0);
+            acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(mx_bf8, d[j][q]), v, acc[j][t], 0, 0, 0);
         }
-      v = next;
+      }
+    };
+    // Chunk c is there when all but the chunk after it has landed; the buffer
+    // that c + 2 goes to, that of c - 1, has then been read by everybody.
+    load(ring0, c0);
+    load(ring1, c0 + 1);
+    for (int c = c0; c < c1; c += 3) {
+      wait_and_meet<LOADS>();
+      load(ring2, c + 2);
+      chunk(ring0);
+      if (c + 1 >= c1) break;
+      wait_and_meet<LOADS>();
+      load(ring0, c + 3);
+      chunk(ring1);
+      if (c + 2 >= c1) break;
+      wait_and_meet<LOADS>();
+      load(ring1, c + 4);
+      chunk(ring2);
     }
+    wait_and_meet<0>();  // nothing is on its way, nobody reads: the ring may start again
+    const float f = runs == 1 && alpha ? alpha[a] : 1.0f;
 #pragma unroll
-    for (int j = 0; j < JC; ++j)
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int t = 0; t < TG; ++t) red[wave][j * TG + t][lane] = acc[j][t];
-    __syncthreads();
-    for (int f = wave; f < JC * TG; f += W) {
-      v4f s = red[0][f][lane];
-#pragma unroll
-      for (int w = 1; w < W; ++w) s += red[w][f][lane];
-      const int t = f % TG * 16 + r, j = j0 + f / TG * 16 + 4 * g;
-      if (__shfl(id, t) == a && j < rank)
-        *reinterpret_cast<v4f*>(p + (int64_t)(t0 + t) * rank + j) = s * (alpha ? alpha[a] : 1.0f);
-    }
-    __syncthreads();
+      for (int j = 0; j < JC; ++j)
+        if (own[t] == a && j0 + 16 * j + 4 * g < rank)
+          *reinterpret_cast<v4f*>(to + (int64_t)(wave * 32 + 16 * t + r) * rank + j0 + 16 * j + 4 * g) = acc[j][t] * f;
+    if (id0 == a) id0 = -1;
+    if (id1 == a) id1 = -1;
   }
 #endif
+}
+
+// p = alpha times the runs' sums, in order; four ranks a thread.
+__global__ __launch_bounds__(256) void project_join_kernel(const nt_f32x4* __restrict__ part, int runs, int64_t units,
+                                                           int upr, const int32_t* __restrict__ ids, int adapters,
+                                                           const float* __restrict__ alpha, nt_f32x4* __restrict__ p) {
+  const int64_t step = (int64_t)gridDim.x * 256;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < units; i += step) {
+    const int a = ids[i / upr];
+    const bool some = (uint32_t)a < (uint32_t)adapters;
+    nt_f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int r = 0; r < runs; ++r) s += part[r * units + i];
+    const float f = some && alpha ? alpha[a] : 1.0f;
+    p[i] = some ? s * f : nt_f32x4{0.0f, 0.0f, 0.0f, 0.0f};  // rows without an adapter: nothing was written
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -213,7 +303,10 @@ __global__ __launch_bounds__(64 * kProjectWaves) void project_tile_kernel(
 // read.  v_mfma_f32_16x16x32_bf16 with z first: lane l = (m, g) loads NF columns
 // from column NF m of the rows 8 g .. 8 g + 7 of the 32, and column i of each
 // lane's makes fragment i, eight rows deep: the transposition is the choice of
-// bytes at the conversion.  p, as three parts, is the other operand.
+// bytes at the conversion.  p, as three parts, is the other operand: a lane loads
+// the JT ranks from JT m of its rows, rank i of each lane's for fragment i.  The
+// scales of the 32 rows come with one load and go to their lanes from there.
+// What bounds it is the count of load instructions, 17 for 32 rows.
 //
 // The runs' sums go to `part` and are joined in order; with one run they are
 // the result.
@@ -241,8 +334,21 @@ __device__ __forceinline__ mx_f2 two_codes(uint32_t w, float scale, int pair) {
 #endif
 }
 
+#if defined(__HIP_DEVICE_COMPILE__)
+// Four scale bytes, `left` of them in the row: as a dword where rows start on
+// one, else one by one.
+__device__ __forceinline__ uint32_t load_scales(mx_rsrc r, uint32_t off, int left, bool dword) {
+  if (dword) return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+  uint32_t w = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w |= mx_get_byte(r, k < left ? off : kNowhere, k) << (8 * k);
+  return w;
+}
+#endif
+
 struct GradArgs {
   int M, C, rank, adapters, runs, jgroups, ctiles;
+  int per;  // rows of a run
   int transposed;
   int64_t ldz;
   float* out;    // one run: the gradients; else [runs] of them
@@ -261,26 +367,30 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(GradArgs q, const
   __shared__ v4f red[2][NF * JT][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m = lane & 15, g = lane >> 4;
-  int b = (int)blockIdx.x;
-  const int ct = b % q.ctiles;
-  b /= q.ctiles;
-  const int jg = b % q.jgroups;
-  b /= q.jgroups;
-  const int a = b % q.adapters, run = b / q.adapters;
-  const int first = (int)((int64_t)q.M * run / q.runs), end = (int)((int64_t)q.M * (run + 1) / q.runs);
+  // Quotients come from the vector unit: back to scalar registers, for the descriptors.
+  const int b1 = __builtin_amdgcn_readfirstlane((int)blockIdx.x / q.ctiles), ct = (int)blockIdx.x - b1 * q.ctiles;
+  const int b2 = __builtin_amdgcn_readfirstlane(b1 / q.jgroups), jg = b1 - b2 * q.jgroups;
+  const int run = __builtin_amdgcn_readfirstlane(b2 / q.adapters), a = b2 - run * q.adapters;
+  const int first = min(run * q.per, q.M), end = min(first + q.per, q.M);
   const int c0 = ct * (16 * NF), j0 = jg * (16 * JT), sk = q.C >> 5;
   const int col = c0 + NF * m;
   const bool col_in = col < q.C;
   const uint32_t zo = FMT == kE2M1 ? col >> 1 : col;
+  const bool s_dword = ((uintptr_t)SZ & 3) == 0 && (sk & 3) == 0;
   v4f acc[NF][JT];
 #pragma unroll
   for (int f = 0; f < NF; ++f)
 #pragma unroll
     for (int j = 0; j < JT; ++j) acc[f][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  constexpr int SB = NF / 2;                      // scale bytes of a row: its 16 NF columns
+  constexpr int LPR = SB / 4;                     // lanes that load them, four each
   struct In {
-    uint32_t z[8][WORDS], s[8];
-    float p[JT][8];
+    uint32_t z[8][WORDS], s;
+    float p[8][JT];
   };
+  // Which lane has the scale of row 8 g + i, and which byte it is there.
+  const int s_from = (8 * g * LPR + m * NF / 128) * 4, s_shift = 8 * (m * NF / 32 % 4);
+  const uint32_t s_col = (uint32_t)(c0 >> 5) + 4 * (lane % LPR);
   int total = 0;
   for (int w0 = first; w0 < end; w0 += kWindow) {
     // This adapter's rows of the window, in order.
@@ -305,12 +415,13 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(GradArgs q, const
     const mx_rsrc rz = mx_run(Z + (int64_t)w0 * q.ldz), rs = mx_run(SZ + (int64_t)w0 * sk);
     const mx_rsrc rp = mx_run(p + (int64_t)w0 * q.rank);
     auto load = [&](int at, In& v) __attribute__((always_inline)) {
+      const int rk = j0 + JT * m;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int e = at + 8 * g + i;
         const bool in = e < n;
         const uint32_t t = in ? (uint32_t)list[e] : 0;
-        const uint32_t off = in && col_in ? t * (uint32_t)q.ldz + zo : kNowhere;
+        const uint32_t off = in && col_in ? __umul24(t, (uint32_t)q.ldz) + zo : kNowhere;
         if constexpr (WORDS == 4) {
           const nt_u32x4 w = get16(rz, off, 0);
 #pragma unroll
@@ -322,44 +433,60 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(GradArgs q, const
         } else {
           v.z[i][0] = __builtin_amdgcn_raw_buffer_load_b32(rz, off, 0, 0);
         }
-        v.s[i] = mx_get_byte(rs, in && col_in ? t * (uint32_t)sk + (col >> 5) : kNowhere, 0);
+        const uint32_t po = in && rk < q.rank ? (__umul24(t, (uint32_t)q.rank) + rk) * 4 : kNowhere;
+        if constexpr (JT == 4) {
+          const nt_u32x4 w = get16(rp, po, 0);
 #pragma unroll
-        for (int j = 0; j < JT; ++j) {
-          const int rk = j0 + 16 * j + m;
-          v.p[j][i] = __uint_as_float(
-              __builtin_amdgcn_raw_buffer_load_b32(rp, in && rk < q.rank ? (t * (uint32_t)q.rank + rk) * 4 : kNowhere, 0, 0));
+          for (int j = 0; j < 4; ++j) v.p[i][j] = __uint_as_float(w[j]);
+        } else if constexpr (JT == 2) {
+          const uint2 w = mx_get_codes(rp, po, 0);
+          v.p[i][0] = __uint_as_float(w.x);
+          v.p[i][1] = __uint_as_float(w.y);
+        } else {
+          v.p[i][0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rp, po, 0, 0));
         }
       }
+      // Row lane / LPR of the 32; bytes past the row's end are of columns that nobody stores.
+      const int e = at + lane / LPR;
+      const bool in = lane < 32 * LPR && e < n && s_col < (uint32_t)sk;
+      const uint32_t t = in ? (uint32_t)list[e] : 0;
+      v.s = load_scales(rs, in ? __umul24(t, (uint32_t)sk) + s_col : kNowhere, sk - (int)s_col, s_dword);
     };
     In v;
     load(wave * 32, v);
     for (int at = wave * 32; at < n; at += 128) {
       In next;
       load(at + 128, next);
-      MxParts pp[JT];
+      float scale[8];
 #pragma unroll
-      for (int j = 0; j < JT; ++j) pp[j] = mx_parts(v.p[j]);
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t w = (uint32_t)__builtin_amdgcn_ds_bpermute(s_from + 4 * LPR * i, (int)v.s);
+        scale[i] = __uint_as_float((w >> s_shift & 255u) << 23);
+      }
+      nt_u32x4 zf[NF];
 #pragma unroll
       for (int k = 0; k < WORDS; ++k)
 #pragma unroll
-        for (int h = 0; h < PER / 2; ++h) {
-          nt_u32x4 even, odd;
+        for (int h = 0; h < PER / 2; ++h)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const mx_f2 x = two_codes<FMT>(v.z[2 * i][k], __uint_as_float(v.s[2 * i] << 23), h);
-            const mx_f2 y = two_codes<FMT>(v.z[2 * i + 1][k], __uint_as_float(v.s[2 * i + 1] << 23), h);
-            even[i] = mx_bf16x2(x.x, y.x);
-            odd[i] = mx_bf16x2(x.y, y.y);
+            const mx_f2 x = two_codes<FMT>(v.z[2 * i][k], scale[2 * i], h);
+            const mx_f2 y = two_codes<FMT>(v.z[2 * i + 1][k], scale[2 * i + 1], h);
+            zf[k * PER + 2 * h][i] = mx_bf16x2(x.x, y.x);
+            zf[k * PER + 2 * h + 1][i] = mx_bf16x2(x.y, y.y);
           }
-          const int f = k * PER + 2 * h;
 #pragma unroll
-          for (int j = 0; j < JT; ++j)
+      for (int j = 0; j < JT; ++j) {
+        float f[8];
 #pragma unroll
-            for (int part = 2; part >= 0; --part) {
-              acc[f][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(mx_bf8, even), pp[j].part[part], acc[f][j], 0, 0, 0);
-              acc[f + 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(mx_bf8, odd), pp[j].part[part], acc[f + 1][j], 0, 0, 0);
-            }
-        }
+        for (int i = 0; i < 8; ++i) f[i] = v.p[i][j];
+        const MxParts pp = mx_parts(f);
+#pragma unroll
+        for (int part = 2; part >= 0; --part)
+#pragma unroll
+          for (int k = 0; k < NF; ++k)
+            acc[k][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(mx_bf8, zf[k]), pp.part[part], acc[k][j], 0, 0, 0);
+      }
       v = next;
     }
     __syncthreads();  // the list has been read
@@ -385,25 +512,26 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(GradArgs q, const
     __syncthreads();
   }
   if (wave != 0) return;
-  // A lane holds rank m and, of fragment f, the columns NF (4 g + i) + f.
+  // A lane holds ranks JT m + j and, of fragment f, the columns NF (4 g + i) + f.
   float* out = q.out + ((int64_t)run * q.adapters + a) * q.rank * q.C;
+  const int rk = j0 + JT * m;
+  if (rk >= q.rank) return;
 #pragma unroll
-  for (int j = 0; j < JT; ++j) {
-    const int rk = j0 + 16 * j + m;
-    if (rk >= q.rank) continue;
+  for (int i = 0; i < 4; ++i) {
+    const int c = c0 + NF * (4 * g + i);
+    if (c >= q.C) continue;
+    if (q.transposed) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = c0 + NF * (4 * g + i);
-      if (c >= q.C) continue;
-      if (q.transposed) {
+      for (int f = 0; f < NF; ++f)
 #pragma unroll
-        for (int f = 0; f < NF; ++f) out[(int64_t)(c + f) * q.rank + rk] = acc[f][j][i];
-      } else {
+        for (int j = 0; j < JT; ++j) out[(int64_t)(c + f) * q.rank + rk + j] = acc[f][j][i];
+    } else {
+#pragma unroll
+      for (int j = 0; j < JT; ++j)
 #pragma unroll
         for (int f = 0; f < NF; f += 4)
-          *reinterpret_cast<v4f*>(out + (int64_t)rk * q.C + c + f) =
+          *reinterpret_cast<v4f*>(out + (int64_t)(rk + j) * q.C + c + f) =
               v4f{acc[f][j][i], acc[f + 1][j][i], acc[f + 2][j][i], acc[f + 3][j][i]};
-      }
     }
   }
 #endif
@@ -416,17 +544,33 @@ __global__ __launch_bounds__(256) void grad_join_kernel(const nt_f32x4* __restri
   const int64_t step = (int64_t)gridDim.x * 256;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
     nt_f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int r = 0; r < runs; ++r)
-      if (counts[r * adapters + a]) s += part[((int64_t)r * adapters + a) * n + i];
+#pragma unroll 4
+    for (int r = 0; r < runs; ++r) {
+      const nt_f32x4 v = part[((int64_t)r * adapters + a) * n + i];  // read in any case, used if it was written
+      const bool some = counts[r * adapters + a] != 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[k] += some ? v[k] : 0.0f;
+    }
     out[a * n + i] = s;
   }
+}
+
+// Rows taken one by one up to this many, and the runs of K beyond.
+constexpr int64_t kFewRows = 256;
+int project_runs(int64_t M, int64_t K, int64_t rank) {
+  if (M <= kFewRows) return 1;
+  const int64_t tiles = (M + kTileRows - 1) / kTileRows * ((rank + 63) / 64), chunks = K / 128;
+  // Two workgroups to each of 256 compute units, runs of four chunks at least.
+  int64_t runs = 512 / tiles;
+  if (runs > chunks / 4) runs = chunks / 4;
+  return (int)(runs < 1 ? 1 : runs);
 }
 
 template <int FMT>
 void project(int64_t M, int64_t K, const uint8_t* a, int64_t lda, const uint8_t* sa, const int32_t* ids,
              int64_t adapters, int64_t rank, const uint16_t* down, int64_t ldd, int64_t stride, const float* alpha,
-             float* p, hipStream_t stream) {
-  if (M <= 256) {
+             float* p, float* workspace, hipStream_t stream) {
+  if (M <= kFewRows) {
     // One rank a workgroup until four fill the chip.
 #define MXFP8_PR(JT)                                                                                            \
   hipLaunchKernelGGL((project_rows_kernel<FMT, JT>), dim3((uint32_t)(M * (rank / JT))), dim3(256), 0, stream,   \
@@ -436,15 +580,23 @@ void project(int64_t M, int64_t K, const uint8_t* a, int64_t lda, const uint8_t*
 #undef MXFP8_PR
     return;
   }
-#define MXFP8_PT(JC, TG)                                                                                        \
-  hipLaunchKernelGGL((project_tile_kernel<FMT, JC, TG>),                                                        \
-                     dim3((uint32_t)((M + 16 * TG - 1) / (16 * TG)), (uint32_t)((rank + 16 * JC - 1) / (16 * JC))), \
-                     dim3(64 * kProjectWaves), 0, stream, (int)M, (int)K, a, lda, sa, ids, (int)adapters,       \
-                     (int)rank, down, ldd, stride, alpha, p)
-  if (rank <= 16) MXFP8_PT(1, 2);
-  else if (rank <= 32) MXFP8_PT(2, 2);
-  else MXFP8_PT(4, 2);
+  const int runs = project_runs(M, K, rank);
+  float* to = runs == 1 ? p : workspace;
+#define MXFP8_PT(JC)                                                                                              \
+  hipLaunchKernelGGL((project_tile_kernel<FMT, JC>),                                                              \
+                     dim3((uint32_t)((M + kTileRows - 1) / kTileRows * runs), (uint32_t)((rank + 16 * JC - 1) / (16 * JC))), \
+                     dim3(256), 0, stream, (int)M, (int)K, runs, a, lda, sa, ids, (int)adapters, (int)rank, down, ldd, \
+                     stride, alpha, to)
+  if (rank <= 16) MXFP8_PT(1);
+  else if (rank <= 32) MXFP8_PT(2);
+  else MXFP8_PT(4);
 #undef MXFP8_PT
+  if (runs > 1) {
+    const int64_t units = M * rank / 4, need = (units + 255) / 256;
+    hipLaunchKernelGGL(project_join_kernel, dim3((uint32_t)(need < 4096 ? need : 4096)), dim3(256), 0, stream,
+                       reinterpret_cast<const nt_f32x4*>(workspace), runs, units, (int)(rank / 4), ids, (int)adapters,
+                       alpha, reinterpret_cast<nt_f32x4*>(p));
+  }
 }
 
 // Ranks and columns of a workgroup, and the runs that the rows are split into.
@@ -454,13 +606,13 @@ struct GradShape {
 GradShape grad_shape(int64_t M, int64_t C, int64_t rank, int64_t adapters) {
   GradShape s;
   s.jt = rank <= 16 ? 1 : rank <= 32 ? 2 : 4;
-  s.nf = s.jt == 4 ? 8 : 16;
+  s.nf = s.jt == 1 ? 16 : 8;
   s.jgroups = (int)((rank + 16 * s.jt - 1) / (16 * s.jt));
   s.ctiles = (int)((C + 16 * s.nf - 1) / (16 * s.nf));
-  // Workgroups for the chip twice over, runs of 256 rows at least, and at most
-  // 256 MB of partial sums.
+  // Two workgroups to each of 256 compute units, runs of 256 rows at least, and
+  // at most 256 MB of partial sums.
   const int64_t wgs = (int64_t)s.ctiles * s.jgroups * adapters;
-  int64_t runs = (1024 + wgs - 1) / wgs;
+  int64_t runs = 512 / wgs;
   const int64_t most = (M + 255) / 256, bytes = adapters * rank * C * 4;
   if (runs > most) runs = most;
   if (runs * bytes > (int64_t(256) << 20)) runs = (int64_t(256) << 20) / bytes;
@@ -473,7 +625,7 @@ void grad(const GradShape& s, const GradArgs& q, const uint8_t* z, const uint8_t
           const int32_t* ids, hipStream_t stream) {
   const dim3 grid((uint32_t)s.ctiles * (uint32_t)s.jgroups * (uint32_t)q.adapters * (uint32_t)s.runs);
   if (s.jt == 1) hipLaunchKernelGGL((grad_kernel<FMT, 1, 16>), grid, dim3(kGradThreads), 0, stream, q, z, sz, p, ids);
-  else if (s.jt == 2) hipLaunchKernelGGL((grad_kernel<FMT, 2, 16>), grid, dim3(kGradThreads), 0, stream, q, z, sz, p, ids);
+  else if (s.jt == 2) hipLaunchKernelGGL((grad_kernel<FMT, 2, 8>), grid, dim3(kGradThreads), 0, stream, q, z, sz, p, ids);
   else hipLaunchKernelGGL((grad_kernel<FMT, 4, 8>), grid, dim3(kGradThreads), 0, stream, q, z, sz, p, ids);
 }
 
@@ -483,10 +635,15 @@ using namespace mx_adapters_detail;
 
 void launch_mx_adapter_project(int64_t M, int64_t K, const uint8_t* a, int64_t lda, int a_fmt, const uint8_t* sa,
                                const int32_t* ids, int64_t adapters, int64_t rank, const uint16_t* down, int64_t ldd,
-                               int64_t stride, const float* alpha, float* p, hipStream_t stream) {
-  if (a_fmt == 0) project<0>(M, K, a, lda, sa, ids, adapters, rank, down, ldd, stride, alpha, p, stream);
-  else if (a_fmt == 1) project<1>(M, K, a, lda, sa, ids, adapters, rank, down, ldd, stride, alpha, p, stream);
-  else project<kE2M1>(M, K, a, lda, sa, ids, adapters, rank, down, ldd, stride, alpha, p, stream);
+                               int64_t stride, const float* alpha, float* p, float* workspace, hipStream_t stream) {
+  if (a_fmt == 0) project<0>(M, K, a, lda, sa, ids, adapters, rank, down, ldd, stride, alpha, p, workspace, stream);
+  else if (a_fmt == 1) project<1>(M, K, a, lda, sa, ids, adapters, rank, down, ldd, stride, alpha, p, workspace, stream);
+  else project<kE2M1>(M, K, a, lda, sa, ids, adapters, rank, down, ldd, stride, alpha, p, workspace, stream);
+}
+
+int64_t adapter_project_workspace(int64_t M, int64_t K, int64_t rank) {
+  const int64_t runs = project_runs(M, K, rank);
+  return runs == 1 ? 0 : runs * M * rank * (int64_t)sizeof(float);
 }
 
 int64_t adapter_grad_workspace(int64_t M, int64_t C, int64_t rank, int64_t adapters) {
@@ -506,6 +663,7 @@ void launch_mx_adapter_grad(int64_t M, int64_t C, const uint8_t* z, int64_t ldz,
   const GradShape s = grad_shape(M, C, rank, adapters);
   GradArgs q;
   q.M = (int)M, q.C = (int)C, q.rank = (int)rank, q.adapters = (int)adapters;
+  q.per = (int)((M + s.runs - 1) / s.runs + 31) / 32 * 32;
   q.runs = s.runs, q.jgroups = s.jgroups, q.ctiles = s.ctiles, q.transposed = transposed, q.ldz = ldz;
   q.out = s.runs == 1 ? out : static_cast<float*>(workspace);
   q.counts = s.runs == 1 ? nullptr : reinterpret_cast<int*>(q.out + s.runs * adapters * rank * C);

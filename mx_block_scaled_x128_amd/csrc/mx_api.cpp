@@ -269,21 +269,23 @@ int mx_layernorm_backward(const uint8_t* kept, int64_t ldk, const uint8_t* kept_
 
 int mx_adapter_project(int64_t M, int64_t K, const uint8_t* a, int64_t lda, int a_fmt, const uint8_t* a_scales,
                        const int32_t* ids, int64_t adapters, int64_t rank, const uint16_t* down, int64_t ldd,
-                       int64_t down_stride, const float* alpha, float* p, void* stream) {
+                       int64_t down_stride, const float* alpha, float* p, void* workspace, void* stream) {
   if (!element(a_fmt)) return MXFP8_ERR_ENUM;
   if (!adapter_extents(M, adapters, rank) || K < 0 || K > INT32_MAX / 2 || K % 128 != 0) return MXFP8_ERR_SHAPE;
   if (M == 0) return MXFP8_OK;
   if (!p || !ids || (K > 0 && (!a || !a_scales || (adapters > 0 && !down)))) return MXFP8_ERR_NULL;
+  const bool work = mxfp8::adapter_project_workspace(M, K, rank) > 0;
+  if (work && !workspace) return MXFP8_ERR_NULL;
   if (K > 0) {
     if (!ld_ok(lda, code_bytes(K, a_fmt)) || lda > kMaxGemmLd) return MXFP8_ERR_LD;
     if (adapters > 0 && !adapter_ld(ldd, K, down_stride)) return MXFP8_ERR_LD;
   }
-  if (!aligned16(a) || !aligned16(down) || !aligned16(p) || (((uintptr_t)a_scales | (uintptr_t)ids | (uintptr_t)alpha) & 3))
-    return MXFP8_ERR_ALIGN;
-  if (shared({p}, {a, a_scales, ids, down, alpha})) return MXFP8_ERR_ALIAS;
+  if (!aligned16(a) || !aligned16(down) || !aligned16(p) || !aligned16(workspace)) return MXFP8_ERR_ALIGN;
+  if (((uintptr_t)a_scales | (uintptr_t)ids | (uintptr_t)alpha) & 3) return MXFP8_ERR_ALIGN;
+  if (shared({p, work ? workspace : nullptr}, {a, a_scales, ids, down, alpha})) return MXFP8_ERR_ALIAS;
   (void)hipGetLastError();
   mxfp8::launch_mx_adapter_project(M, K, a, lda, a_fmt, a_scales, ids, adapters, rank, down, ldd, down_stride, alpha, p,
-                                   (hipStream_t)stream);
+                                   static_cast<float*>(workspace), (hipStream_t)stream);
   return launch_status();
 }
 
@@ -291,14 +293,15 @@ int mxfp4_gemm_adapted(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_
                        const uint8_t* a_scales, const uint8_t* b, int64_t ldb, const uint8_t* b_scales,
                        const int32_t* ids, int64_t adapters, int64_t rank, const uint16_t* down, int64_t ldd,
                        int64_t down_stride, const uint16_t* up, int64_t ldu, int64_t up_stride, const float* alpha,
-                       float* p, void* c, int64_t ldc, int c_dtype, void* stream) {
+                       float* p, void* c, int64_t ldc, int c_dtype, void* workspace, void* stream) {
   if (!element(a_fmt) || !real(c_dtype)) return MXFP8_ERR_ENUM;
   if (!adapter_extents(M, adapters, rank) || N < 0 || K < 0) return MXFP8_ERR_SHAPE;
   if (N > INT32_MAX / 2 || K > INT32_MAX / 2 || K % 128 != 0) return MXFP8_ERR_SHAPE;
   if (M == 0) return MXFP8_OK;
   if (!p || !ids || (N > 0 && !c)) return MXFP8_ERR_NULL;
   if (K > 0 && (!a || !a_scales || (adapters > 0 && !down) || (N > 0 && (!b || !b_scales)))) return MXFP8_ERR_NULL;
-  if (N > 0 && adapters > 0 && !up) return MXFP8_ERR_NULL;
+  const bool work = mxfp8::adapter_project_workspace(M, K, rank) > 0;
+  if ((N > 0 && adapters > 0 && !up) || (work && !workspace)) return MXFP8_ERR_NULL;
   if (N > 0 && !ld_ok(ldc, N)) return MXFP8_ERR_LD;
   if (K > 0) {
     if (!ld_ok(lda, code_bytes(K, a_fmt)) || lda > kMaxGemmLd) return MXFP8_ERR_LD;
@@ -306,17 +309,24 @@ int mxfp4_gemm_adapted(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_
     if (adapters > 0 && !adapter_ld(ldd, K, down_stride)) return MXFP8_ERR_LD;
   }
   if (N > 0 && adapters > 0 && !adapter_ld(ldu, rank, up_stride)) return MXFP8_ERR_LD;
-  if (!aligned16(a) || !aligned16(b) || !aligned16(down) || !aligned16(up) || !aligned16(p) || !aligned16(c))
+  if (!aligned16(a) || !aligned16(b) || !aligned16(down) || !aligned16(up) || !aligned16(p) || !aligned16(c) ||
+      !aligned16(workspace))
     return MXFP8_ERR_ALIGN;
   if (((uintptr_t)a_scales | (uintptr_t)b_scales | (uintptr_t)ids | (uintptr_t)alpha) & 3) return MXFP8_ERR_ALIGN;
-  if (shared({c, p}, {a, b, a_scales, b_scales, ids, down, up, alpha})) return MXFP8_ERR_ALIAS;
+  if (shared({c, p, work ? workspace : nullptr}, {a, b, a_scales, b_scales, ids, down, up, alpha}))
+    return MXFP8_ERR_ALIAS;
   (void)hipGetLastError();
   mxfp8::launch_mx_adapter_project(M, K, a, lda, a_fmt, a_scales, ids, adapters, rank, down, ldd, down_stride, alpha, p,
-                                   (hipStream_t)stream);
+                                   static_cast<float*>(workspace), (hipStream_t)stream);
   if (N > 0)
     mxfp8::launch_mxfp4_gemm_adapted(M, N, K, a, lda, a_fmt, a_scales, b, ldb, b_scales, ids, adapters, rank, p, up, ldu,
                                      up_stride, c, ldc, c_dtype, (hipStream_t)stream);
   return launch_status();
+}
+
+int64_t mx_adapter_project_workspace(int64_t M, int64_t K, int64_t rank) {
+  if (!adapter_extents(M, 0, rank) || K < 0 || K > INT32_MAX / 2 || K % 128 != 0 || M == 0) return 0;
+  return mxfp8::adapter_project_workspace(M, K, rank);
 }
 
 int64_t mx_adapter_grad_workspace(int64_t M, int64_t C, int64_t rank, int64_t adapters) {

@@ -57,11 +57,12 @@ void launch_mxfp4_gemm_adapted(int64_t M, int64_t N, int64_t K, const uint8_t* a
                                int64_t adapters, int64_t rank, const float* p, const uint16_t* up, int64_t ldu,
                                int64_t stride, void* c, int64_t ldc, int c_dtype, hipStream_t stream);
 // p[m] = alpha[a] down[a] x[m], zeros without an adapter; adapter a's [rank][ldd] bf16 from down + a stride, alpha
-// may be null (ones).  K % 128 == 0, scale pointers 4-byte aligned, M <= kMaxAdapterRows.
+// may be null (ones).  K % 128 == 0, scale pointers 4-byte aligned, M <= kMaxAdapterRows.  Bytes of workspace.
 constexpr int64_t kMaxAdapterRows = int64_t(1) << 27, kMaxRank = 256;
 void launch_mx_adapter_project(int64_t M, int64_t K, const uint8_t* a, int64_t lda, int a_fmt, const uint8_t* sa,
                                const int32_t* ids, int64_t adapters, int64_t rank, const uint16_t* down, int64_t ldd,
-                               int64_t stride, const float* alpha, float* p, hipStream_t stream);
+                               int64_t stride, const float* alpha, float* p, float* workspace, hipStream_t stream);
+int64_t adapter_project_workspace(int64_t M, int64_t K, int64_t rank);
 // out[a] = the sum over the rows m of adapter a of p[m] (x) z[m], [rank][C], or [C][rank] if transposed.  C % 32 ==
 // 0, all extents >= 1.  Bytes of workspace, and workgroups (fewer than 2^24).
 int64_t adapter_grad_workspace(int64_t M, int64_t C, int64_t rank, int64_t adapters);

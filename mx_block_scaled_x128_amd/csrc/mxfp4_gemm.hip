@@ -182,58 +182,79 @@ __device__ __forceinline__ int next_adapter(const int (&id)[MT]) {
   }
   return a;
 }
-// Eight values of p, zeros where `in` is false.
-__device__ __forceinline__ MxParts adapter_parts(__amdgpu_buffer_rsrc_t rp, bool in, uint32_t off) {
-  MxRaw<float> v;
-  mx_get(rp, in ? off : kOutside, 0, v);
-  float f[8];
-  mx_unpack(v, f);
-  return mx_parts(f);
-}
-
 // up p in the few-row kernel's accumulators: pieces of 32 ranks of each adapter
-// that the workgroup's rows name, dealt to the waves in turn.  A lane's four
-// results belong to one row, so rows of other adapters keep what they had,
-// whatever this one's values are.
+// that the workgroup's rows name, dealt to the waves in turn, DEPTH of them on
+// their way at once.  A lane's four results belong to one row, so rows of other
+// adapters keep what they had, whatever this one's values are.
 template <int MT, int NT, int WAVES>
 __device__ __forceinline__ void add_adapters(const Adapters& ad, int m0, int n0, int rows_a, int rows_b, int wave,
                                              int lane, v4f (&acc)[MT][NT]) {
+  constexpr int DEPTH = 2;
   const int r = lane & 15, g = lane >> 4;
-  int id[MT];
+  int id[MT], left[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     id[i] = 16 * i + r < rows_a ? ad.ids[m0 + 16 * i + r] : -1;
     if (id[i] >= ad.adapters) id[i] = -1;
+    left[i] = id[i];
   }
-  const __amdgpu_buffer_rsrc_t rp = descriptor(reinterpret_cast<const uint8_t*>(ad.p + (int64_t)m0 * ad.rank));
-  int turn = 0;
-  for (int a = next_adapter(id); a >= 0; a = next_adapter(id)) {
-    const __amdgpu_buffer_rsrc_t ru =
-        descriptor(reinterpret_cast<const uint8_t*>(ad.up + a * ad.stride + (int64_t)n0 * ad.ldu));
-    for (int k = 8 * g; k - 8 * g < ad.rank; k += 32) {
-      if (turn++ % WAVES != wave) continue;
-      mx_bf8 u[NT];
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        u[j] = __builtin_bit_cast(mx_bf8, load16(ru, 16 * j + r < rows_b && k < ad.rank
-                                                         ? (uint32_t)((16 * j + r) * ad.ldu + k) * 2 : kOutside, 0));
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const bool mine = id[i] == a;
-        const MxParts p = adapter_parts(rp, mine && k < ad.rank, (uint32_t)((16 * i + r) * ad.rank + k) * 4);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          v4f s = acc[i][j];
-#pragma unroll
-          for (int part = 2; part >= 0; --part) s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u[j], p.part[part], s, 0, 0, 0);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = mine ? s[e] : acc[i][j][e];
-        }
-      }
-    }
+  // Lane n of `names` holds the n-th adapter.
+  int names = -1, count = 0;
+  for (int a = next_adapter(left); a >= 0; a = next_adapter(left)) {
+    if (lane == count) names = a;
+    ++count;
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-      if (id[i] == a) id[i] = -1;
+      if (left[i] == a) left[i] = -1;
+  }
+  const int per = (ad.rank + 31) >> 5, pieces = count * per;
+  const __amdgpu_buffer_rsrc_t rp = descriptor(reinterpret_cast<const uint8_t*>(ad.p + (int64_t)m0 * ad.rank));
+  struct Piece {
+    int a;
+    mx_bf8 u[NT];
+    MxRaw<float> p[MT];
+  };
+  auto load = [&](int n, Piece& v) __attribute__((always_inline)) {
+    const bool in = n < pieces;
+    const int which = in ? n / per : 0;
+    v.a = __builtin_amdgcn_readlane(names, which);
+    const int k = (n - which * per) * 32 + 8 * g;
+    const __amdgpu_buffer_rsrc_t ru = descriptor(
+        reinterpret_cast<const uint8_t*>(ad.up + (in ? v.a * ad.stride + (int64_t)n0 * ad.ldu : 0)));
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      v.u[j] = __builtin_bit_cast(mx_bf8, load16(ru, in && 16 * j + r < rows_b && k < ad.rank
+                                                         ? (uint32_t)((16 * j + r) * ad.ldu + k) * 2 : kOutside, 0));
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+      mx_get(rp, in && id[i] == v.a && k < ad.rank ? (uint32_t)((16 * i + r) * ad.rank + k) * 4 : kOutside, 0, v.p[i]);
+  };
+  auto add = [&](const Piece& v) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      float f[8];
+      mx_unpack(v.p[i], f);
+      const MxParts p = mx_parts(f);
+      const bool mine = id[i] == v.a;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        v4f s = acc[i][j];
+#pragma unroll
+        for (int part = 2; part >= 0; --part) s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v.u[j], p.part[part], s, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = mine ? s[e] : acc[i][j][e];
+      }
+    }
+  };
+  Piece v[DEPTH];
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d) load(wave + d * WAVES, v[d]);
+  for (int n = wave; n < pieces; n += DEPTH * WAVES) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      if (n + d * WAVES < pieces) add(v[d]);
+      load(n + (d + DEPTH) * WAVES, v[d]);
+    }
   }
 }
 #endif
@@ -465,60 +486,91 @@ __device__ __forceinline__ uint32_t opaque(uint32_t x) {
 }
 
 #if defined(__HIP_DEVICE_COMPILE__)
-// up p in a tile's accumulators (v_mfma_f32_32x32x16_bf16, whose results lie as
-// the scaled instruction's do): 16 ranks at a time of each adapter that the
-// wave's rows name.  m0, n0: the wave's first row and column.  Strips whose rows
-// all have the adapter (or lie past M) take the results as they are, others row
-// by row, so that no adapter's values reach another's rows.
-template <int MT, int NT>
-__device__ __forceinline__ void add_adapters(const Adapters& ad, int M, int N, int m0, int n0, int lane,
-                                             v16f (&acc)[MT][NT]) {
+// up p as a tile's first accumulators (v_mfma_f32_32x32x16_bf16, whose results
+// lie as the scaled instruction's do): 16 ranks at a time of each adapter that
+// the wave's rows name, zeros for p in the rows of others.  m0, n0: the wave's
+// first row and column.
+//
+// Zeros times an infinity or a NaN would not be zero.  So such values of up are
+// taken out, and `spoilt` keeps, for each of a lane's rows, the columns that
+// they leave without a result; true if there are any.  (Choosing row by row what
+// to add would take the accumulators through the vector registers.)
+template <int PARTS, int MT, int NT>
+__device__ __forceinline__ bool first_adapters(const Adapters& ad, int M, int N, int m0, int n0, int lane,
+                                               v16f (&acc)[MT][NT], uint32_t (&spoilt)[MT][NT]) {
   const int r = lane & 31, g = lane >> 5;
   int id[MT];
+  bool any = false;
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     id[i] = m0 + 32 * i + r < M ? ad.ids[m0 + 32 * i + r] : -1;
     if (id[i] >= ad.adapters) id[i] = -1;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) spoilt[i][j] = 0;
   }
   const __amdgpu_buffer_rsrc_t rp = descriptor(reinterpret_cast<const uint8_t*>(ad.p + (int64_t)m0 * ad.rank));
+  struct In {
+    u32x4 u[NT];
+    MxRaw<float> p[MT];
+  };
   for (int a = next_adapter(id); a >= 0; a = next_adapter(id)) {
     const __amdgpu_buffer_rsrc_t ru =
         descriptor(reinterpret_cast<const uint8_t*>(ad.up + a * ad.stride + (int64_t)n0 * ad.ldu));
-#pragma nounroll
-    for (int k = 8 * g; k - 8 * g < ad.rank; k += 16) {
-      mx_bf8 u[NT];
+    auto load = [&](int k0, In& v) __attribute__((always_inline)) {
+      const int k = k0 + 8 * g;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-        u[j] = __builtin_bit_cast(mx_bf8, load16(ru, n0 + 32 * j + r < N && k < ad.rank
-                                                         ? (uint32_t)((32 * j + r) * ad.ldu + k) * 2 : kOutside, 0));
+        v.u[j] = __builtin_bit_cast(u32x4, load16(ru, n0 + 32 * j + r < N && k < ad.rank
+                                                          ? (uint32_t)((32 * j + r) * ad.ldu + k) * 2 : kOutside, 0));
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const bool mine = id[i] == a;
-        const uint64_t have = __ballot(mine);
-        if (!have) continue;
-        const MxParts p = adapter_parts(rp, mine && k < ad.rank, (uint32_t)((32 * i + r) * ad.rank + k) * 4);
-        if (have == __ballot(m0 + 32 * i + r < M)) {
+      for (int i = 0; i < MT; ++i)
+        mx_get(rp, id[i] == a && k < ad.rank ? (uint32_t)((32 * i + r) * ad.rank + k) * 4 : kOutside, 0, v.p[i]);
+    };
+    In v;
+    load(0, v);
+#pragma nounroll
+    for (int k0 = 0; k0 < ad.rank; k0 += 16) {
+      In next;
+      load(k0 + 16, next);
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
+      for (int j = 0; j < NT; ++j) {
+        bool bad = false;
 #pragma unroll
-            for (int part = 2; part >= 0; --part)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u[j], p.part[part], acc[i][j], 0, 0, 0);
-        } else {
+        for (int w = 0; w < 4; ++w)
+          bad |= (v.u[j][w] & 0x7F80u) == 0x7F80u || (v.u[j][w] & 0x7F800000u) == 0x7F800000u;
+        const uint64_t where = __ballot(bad);
+        if (where) {
+          any = true;
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            v16f s = acc[i][j];
-#pragma unroll
-            for (int part = 2; part >= 0; --part) s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u[j], p.part[part], s, 0, 0, 0);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[i][j][e] = mine ? s[e] : acc[i][j][e];
+          for (int w = 0; w < 4; ++w) {
+            if ((v.u[j][w] & 0x7F80u) == 0x7F80u) v.u[j][w] &= 0xFFFF0000u;
+            if ((v.u[j][w] & 0x7F800000u) == 0x7F800000u) v.u[j][w] &= 0x0000FFFFu;
           }
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            if (id[i] == a) spoilt[i][j] |= (uint32_t)where | (uint32_t)(where >> 32);
         }
       }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        if (!__ballot(id[i] == a)) continue;
+        float f[8];
+        mx_unpack(v.p[i], f);
+        const MxParts p = mx_parts(f);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int part = PARTS - 1; part >= 0; --part)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(mx_bf8, v.u[j]), p.part[part],
+                                                                acc[i][j], 0, 0, 0);
+      }
+      v = next;
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i)
       if (id[i] == a) id[i] = -1;
   }
+  return any;
 }
 #endif
 
@@ -756,6 +808,9 @@ __device__ __forceinline__ void gemm_tile(int M, int N, int K, const uint8_t* __
     stage(p, 1, kb, next, (p + 1) % RING, 0, next, dma, sg, f1, f0, sa, sb, nsa, nsb);
   };
 
+  [[maybe_unused]] uint32_t spoilt[MT][NT];
+  [[maybe_unused]] bool spoils = false;
+
   // Epilogue: each wave stages a 32-row strip at a time in its own part of a
   // buffer nobody reads any more and writes whole row segments, past the
   // caches (C is written once).  A lane holds, of each 32 x 32 block, row
@@ -773,7 +828,14 @@ __device__ __forceinline__ void gemm_tile(int M, int N, int K, const uint8_t* __
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const v4f v = v4f{acc[mt][nt][4 * q], acc[mt][nt][4 * q + 1], acc[mt][nt][4 * q + 2], acc[mt][nt][4 * q + 3]};
+          v4f v = v4f{acc[mt][nt][4 * q], acc[mt][nt][4 * q + 1], acc[mt][nt][4 * q + 2], acc[mt][nt][4 * q + 3]};
+          if constexpr (std::is_same_v<AD, Adapters>) {
+            if (spoils) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (spoilt[mt][nt] >> (8 * q + 4 * g + i) & 1) v[i] = __builtin_nanf("");
+            }
+          }
           if constexpr (F32)
             *reinterpret_cast<v4f*>(stg + (lane & 31) * P + (((nt * 8 + 2 * q + g) ^ (lane & 15)) * 16)) = v;
           else
@@ -809,7 +871,8 @@ __device__ __forceinline__ void gemm_tile(int M, int N, int K, const uint8_t* __
 #pragma unroll
     for (int item = 0; item < DMA_ITEMS; ++item) dma_item(q, q, item);
   if constexpr (std::is_same_v<AD, Adapters>) {
-    add_adapters<MT, NT>(ad, M, N, m0 + wm * WM, n0 + wn * WN, lane, acc);
+    // p's leading 16 bits are 2^-16 of it off, 24 none; bf16 results round by 2^-8.
+    spoils = first_adapters<sizeof(OutT) == 2 ? 2 : 3, MT, NT>(ad, M, N, m0 + wm * WM, n0 + wn * WN, lane, acc, spoilt);
     mfma_retire_pad();
   }
   wait_loads_and_meet<(RING - 1) * DMA_ITEMS>();

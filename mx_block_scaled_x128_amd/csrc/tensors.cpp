@@ -32,6 +32,7 @@ struct Library {
   decltype(&::mx_layernorm_backward) mx_layernorm_backward;
   decltype(&::mx_layernorm_backward_workspace) mx_layernorm_backward_workspace;
   decltype(&::mx_adapter_project) mx_adapter_project;
+  decltype(&::mx_adapter_project_workspace) mx_adapter_project_workspace;
   decltype(&::mxfp4_gemm_adapted) mxfp4_gemm_adapted;
   decltype(&::mx_adapter_grad) mx_adapter_grad;
   decltype(&::mx_adapter_grad_workspace) mx_adapter_grad_workspace;
@@ -63,6 +64,7 @@ void bind(const std::string& path) {
   MXFP8_FIND(mx_layernorm_backward);
   MXFP8_FIND(mx_layernorm_backward_workspace);
   MXFP8_FIND(mx_adapter_project);
+  MXFP8_FIND(mx_adapter_project_workspace);
   MXFP8_FIND(mxfp4_gemm_adapted);
   MXFP8_FIND(mx_adapter_grad);
   MXFP8_FIND(mx_adapter_grad_workspace);
@@ -460,8 +462,9 @@ at::Tensor adapter_project_mx(const at::Tensor& a, const at::Tensor& sa, int a_f
   const int64_t rank = adapters_of(down, K, ids, M, alpha);
   const Place on(stream, device_of({&a, &sa, &down, &ids, given(alpha)}));
   at::Tensor p = on.fresh({M, rank}, at::kFloat);
+  at::Tensor work = on.scratch({lib.mx_adapter_project_workspace(M, K, rank)}, at::kByte);
   status(lib.mx_adapter_project(M, K, bytes(a), ld(a), a_fmt, bytes(sa), ints(ids), down.size(0), rank, bf16(down),
-                                adapter_ld(down), adapter_stride(down), floats(given(alpha)), floats(&p), on.stream()),
+                                adapter_ld(down), adapter_stride(down), floats(given(alpha)), floats(&p), ptr(work), on.stream()),
          "mx_adapter_project");
   return p;
 }
@@ -487,10 +490,11 @@ py::tuple mxfp4_adapted_gemm(const at::Tensor& a, const at::Tensor& sa, int a_fm
           "out_dtype must be float32 or bfloat16, got ", type);
   const Place on(stream, device_of({&a, &sa, &b, &sb, &down, &up, &ids, given(alpha), given(out)}));
   at::Tensor c = out.has_value() ? *out : on.pitched(M, N, type), p = on.fresh({M, rank}, at::kFloat);
+  at::Tensor work = on.scratch({lib.mx_adapter_project_workspace(M, K, rank)}, at::kByte);
   status(lib.mxfp4_gemm_adapted(M, N, K, bytes(a), ld(a), a_fmt, bytes(sa), bytes(b), ld(b), bytes(sb), ints(ids),
                                 down.size(0), rank, bf16(down), adapter_ld(down), adapter_stride(down), bf16(up),
                                 adapter_ld(up), adapter_stride(up), floats(given(alpha)), floats(&p), ptr(c), ld(c),
-                                real_type(c), on.stream()), "mxfp4_gemm_adapted");
+                                real_type(c), ptr(work), on.stream()), "mxfp4_gemm_adapted");
   return py::make_tuple(c, p);
 }
 

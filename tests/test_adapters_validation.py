@@ -76,8 +76,8 @@ U, V = 0xB00000, 0xC00000
 
 
 def test_mx_adapter_project():
-    def f(M=64, K=256, a=X, lda=256, fmt=0, sa=S, ids=B, n=4, rank=16, down=W, ldd=256, stride=4096, alpha=R, p=C):
-        return mx.mx_adapter_project(M, K, a, lda, fmt, sa, ids, n, rank, down, ldd, stride, alpha, p, None)
+    def f(M=64, K=256, a=X, lda=256, fmt=0, sa=S, ids=B, n=4, rank=16, down=W, ldd=256, stride=4096, alpha=R, p=C, work=V):
+        return mx.mx_adapter_project(M, K, a, lda, fmt, sa, ids, n, rank, down, ldd, stride, alpha, p, work, None)
     assert f(fmt=3) == ENUM and f(fmt=-1) == ENUM
     assert f(M=-1) == SHAPE and f(M=2 ** 27 + 1) == SHAPE and f(K=192) == SHAPE and f(K=-128) == SHAPE
     assert f(n=-1) == SHAPE and f(n=2 ** 30 + 1) == SHAPE
@@ -87,7 +87,10 @@ def test_mx_adapter_project():
         assert f(**{name: None}) == NULL, name
     assert f(lda=240) == LD and f(lda=264) == LD and f(lda=2 ** 22 + 16) == LD
     assert f(ldd=248) == LD and f(ldd=260) == LD and f(ldd=2 ** 22 + 8) == LD and f(stride=4) == LD and f(stride=-8) == LD
-    for name in ("a", "down", "p"):
+    assert mx.mx_adapter_project_workspace(2000, 4096, 16) > 0
+    large = dict(M=2000, K=4096, lda=4096, ldd=4096, stride=65536)
+    assert f(work=None, **large) == NULL and f(work=X, **large) == ALIAS and f(work=C, **large) == ALIAS
+    for name in ("a", "down", "p", "work"):
         assert f(**{name: MIS}) == ALIGN, name
     assert f(sa=S + 2) == ALIGN and f(ids=B + 2) == ALIGN and f(alpha=R + 1) == ALIGN
     for other in (X, S, B, W, R):
@@ -96,9 +99,9 @@ def test_mx_adapter_project():
 
 def test_mxfp4_gemm_adapted():
     def f(M=64, N=96, K=256, a=X, lda=256, fmt=0, sa=S, b=Q, ldb=128, sb=P, ids=B, n=4, rank=16, down=W, ldd=256, ds=4096,
-          up=U, ldu=16, us=1536, alpha=R, p=V, c=C, ldc=96, dt=0):
+          up=U, ldu=16, us=1536, alpha=R, p=V, c=C, ldc=96, dt=0, work=0xD00000):
         return mx.mxfp4_gemm_adapted(M, N, K, a, lda, fmt, sa, b, ldb, sb, ids, n, rank, down, ldd, ds, up, ldu, us, alpha,
-                                     p, c, ldc, dt, None)
+                                     p, c, ldc, dt, work, None)
     assert f(fmt=3) == ENUM and f(dt=2) == ENUM
     assert f(M=-1) == SHAPE and f(N=-1) == SHAPE and f(K=100) == SHAPE and f(rank=20) == SHAPE and f(n=-2) == SHAPE
     assert f(M=2 ** 27 + 1) == SHAPE and f(N=2 ** 30) == SHAPE and f(K=2 ** 30) == SHAPE
@@ -108,7 +111,9 @@ def test_mxfp4_gemm_adapted():
     assert f(lda=128) == LD and f(ldb=136) == LD and f(ldc=80) == LD and f(ldc=104) == LD
     assert f(lda=2 ** 22 + 16) == LD and f(ldb=2 ** 22 + 16) == LD
     assert f(ldd=128) == LD and f(ldu=8) == LD and f(ldu=20) == LD and f(us=1540) == LD and f(ds=-8) == LD
-    for name in ("a", "b", "down", "up", "p", "c"):
+    large = dict(M=2000, K=4096, lda=4096, ldb=2048, ldd=4096, ds=65536)
+    assert f(work=None, **large) == NULL and f(work=U, **large) == ALIAS and f(work=V, **large) == ALIAS
+    for name in ("a", "b", "down", "up", "p", "c", "work"):
         assert f(**{name: MIS}) == ALIGN, name
     assert f(sa=S + 1) == ALIGN and f(sb=P + 2) == ALIGN and f(ids=B + 1) == ALIGN and f(alpha=R + 2) == ALIGN
     for other in (X, Q, S, P, B, W, U, R):
@@ -133,6 +138,13 @@ def test_mx_adapter_grad():
     for other in (X, S, P, B):
         assert f(grad=other) == ALIAS and f(M=8192, n=1, work=other) == ALIAS, other
     assert f(M=8192, n=1, work=C) == ALIAS
+
+
+def test_adapter_project_workspace():
+    for bad in ((-1, 256, 16), (64, 200, 16), (64, 256, 9), (0, 256, 16), (2 ** 27 + 1, 256, 16), (256, 18944, 64)):
+        assert mx.mx_adapter_project_workspace(*bad) == 0, bad
+    for M, K, rank in ((257, 1 << 22, 256), (65536, 18944, 256), (8192, 18944, 16), (1 << 27, 128, 8)):
+        assert mx.mx_adapter_project_workspace(M, K, rank) <= 512 * 128 * rank * 4
 
 
 def test_adapter_grad_workspace():
