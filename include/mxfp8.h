@@ -492,8 +492,9 @@ int64_t mx_layernorm_backward_workspace(int64_t rows, int64_t cols);
  *             dimensions in elements, multiples of 8, ldd and ldu <= 2^22.
  *   alpha:    [adapters] fp32, or NULL: ones.
  *   p:        [M][rank] fp32, dense, 16-byte aligned.
- *   workspace: mx_adapter_project_workspace(M, K, rank) bytes, 16-byte aligned,
- *             used only during the call; may be NULL where that is 0.
+ *   workspace: the bytes that the entry point's own ..._workspace function
+ *             gives, 16-byte aligned, used only during the call; may be NULL
+ *             where that is 0.
  * M is at most 2^27 and adapters 2^30.  What an adapter's values or a row's are
  * (infinities and NaN included) reaches no other adapter's rows.
  *
@@ -528,6 +529,8 @@ int mxfp4_gemm_adapted(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_
                        const int32_t* ids, int64_t adapters, int64_t rank, const uint16_t* down, int64_t ldd,
                        int64_t down_stride, const uint16_t* up, int64_t ldu, int64_t up_stride, const float* alpha,
                        float* p, void* c, int64_t ldc, int c_dtype, void* workspace, void* stream);
+/* Bytes of workspace; 0 for extents that mxfp4_gemm_adapted refuses or that need none. */
+int64_t mxfp4_gemm_adapted_workspace(int64_t M, int64_t N, int64_t K, int64_t rank);
 
 /*
  * mx_adapter_grad -- grad[a] = the sum over the rows m with ids[m] == a of
@@ -537,8 +540,6 @@ int mxfp4_gemm_adapted(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_
  *   z: [M][ldz] codes of z_fmt (E4M3, E5M2 or E2M1), z_scales [M][C / 32].
  *   grad: [adapters][rank][C] fp32, or [adapters][C][rank] if transposed; zeros
  *         for an adapter without rows.  16-byte aligned.
- *   workspace: mx_adapter_grad_workspace(M, C, rank, adapters) bytes, 16-byte
- *         aligned, used only during the call; may be NULL where that is 0.
  * Requires C % 32 == 0 and ldz <= 2^22.  Sums are in fp32 and in a fixed order:
  * the same inputs give the same bits.
  */

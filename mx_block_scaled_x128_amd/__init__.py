@@ -14,8 +14,8 @@ Low-level entry points carry the C names and signatures (pointers as ints):
   mx_swiglu_forward, mx_swiglu_backward, mx_rmsnorm_forward,
   mx_rmsnorm_backward, mx_rmsnorm_backward_workspace, mx_layernorm_forward,
   mx_layernorm_backward, mx_layernorm_backward_workspace, mx_adapter_project,
-  mx_adapter_project_workspace, mxfp4_gemm_adapted, mx_adapter_grad,
-  mx_adapter_grad_workspace,
+  mx_adapter_project_workspace, mxfp4_gemm_adapted,
+  mxfp4_gemm_adapted_workspace, mx_adapter_grad, mx_adapter_grad_workspace,
   mxfp8_status_string, mxfp8_version.
 Tensor conveniences allocate outputs with torch and call them:
   quantize_token, quantize_block, quantize_token_dual, quantize_block_dual,
@@ -46,7 +46,8 @@ __all__ = [
     "swiglu_mx", "swiglu_mx_backward", "SwigluKept", "rmsnorm_mx", "rmsnorm_mx_backward", "RmsnormKept",
     "mx_layernorm_forward", "mx_layernorm_backward", "mx_layernorm_backward_workspace", "layernorm_mx",
     "layernorm_mx_backward", "LayernormKept",
-    "mx_adapter_project", "mx_adapter_project_workspace", "mxfp4_gemm_adapted", "mx_adapter_grad", "mx_adapter_grad_workspace", "adapter_project_mx",
+    "mx_adapter_project", "mx_adapter_project_workspace", "mxfp4_gemm_adapted", "mxfp4_gemm_adapted_workspace",
+    "mx_adapter_grad", "mx_adapter_grad_workspace", "adapter_project_mx",
     "mxfp4_adapted_gemm", "adapter_grad_mx",
 ]
 
@@ -123,6 +124,7 @@ def load_library():
         lib.mx_layernorm_backward_workspace.argtypes = [I64, I64]
         lib.mx_adapter_project.argtypes = [I64, I64, P, I64, I, P, P, I64, I64, P, I64, I64, P, P, P, P]
         lib.mx_adapter_project_workspace.argtypes = [I64, I64, I64]
+        lib.mxfp4_gemm_adapted_workspace.argtypes = [I64, I64, I64, I64]
         lib.mxfp4_gemm_adapted.argtypes = [I64, I64, I64, P, I64, I, P, P, I64, P, P, I64, I64, P, I64, I64, P, I64,
                                            I64, P, P, P, I64, I, P, P]
         lib.mx_adapter_grad.argtypes = [I64, I64, P, I64, I, P, P, I64, P, I64, I, P, P, P]
@@ -135,6 +137,7 @@ def load_library():
         lib.mx_rmsnorm_backward_workspace.restype = I64
         lib.mx_layernorm_backward_workspace.restype = I64
         lib.mx_adapter_project_workspace.restype = I64
+        lib.mxfp4_gemm_adapted_workspace.restype = I64
         lib.mx_adapter_grad_workspace.restype = I64
         lib.mxfp8_status_string.argtypes = [I]
         lib.mxfp8_status_string.restype = ctypes.c_char_p
@@ -277,6 +280,10 @@ def mxfp4_gemm_adapted(M, N, K, a, lda, a_fmt, a_scales, b, ldb, b_scales, ids, 
     return load_library().mxfp4_gemm_adapted(M, N, K, a, lda, a_fmt, a_scales, b, ldb, b_scales, ids, adapters, rank,
                                              down, ldd, down_stride, up, ldu, up_stride, alpha, p, c, ldc, c_dtype,
                                              workspace, stream)
+
+
+def mxfp4_gemm_adapted_workspace(M, N, K, rank):
+    return load_library().mxfp4_gemm_adapted_workspace(M, N, K, rank)
 
 
 def mx_adapter_grad(M, C, z, ldz, z_fmt, z_scales, p, rank, ids, adapters, transposed, grad, workspace, stream):

@@ -21,6 +21,23 @@ __device__ __forceinline__ nt_u32x4 get16(mx_rsrc r, uint32_t lane, uint32_t at)
 }
 #endif
 
+#if defined(__HIP_DEVICE_COMPILE__)
+// Four ranks of a row of p into its packed parts.
+__device__ __forceinline__ void put_packed(const MxPacked& packed, int64_t t, int j, v4f v) {
+  uint16_t* to = packed.place(t, j);
+#pragma unroll
+  for (int part = 0; part < 3; ++part) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      w[k] = __float_as_uint(v[k]) & 0xFFFF0000u;
+      v[k] -= __uint_as_float(w[k]);
+    }
+    *reinterpret_cast<nt_u32x2*>(to + part * 512) = nt_u32x2{w[0] >> 16 | w[1], w[2] >> 16 | w[3]};
+  }
+}
+#endif
+
 // ---------------------------------------------------------------------------
 // Projection, a row at a time: a workgroup takes JT ranks of one row, its 256
 // threads 8 elements of K each, step after step.  Each row reads its adapter for
@@ -32,7 +49,7 @@ __global__ __launch_bounds__(256) void project_rows_kernel(int K, const uint8_t*
                                                            const int32_t* __restrict__ ids, int adapters, int rank,
                                                            const uint16_t* __restrict__ down, int64_t ldd,
                                                            int64_t stride, const float* __restrict__ alpha,
-                                                           float* __restrict__ p) {
+                                                           float* __restrict__ p, MxPacked packed) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ float red[4][JT];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -94,7 +111,19 @@ __global__ __launch_bounds__(256) void project_rows_kernel(int K, const uint8_t*
     for (int j = 0; j < JT; ++j) red[wave][j] = sum[j];
   }
   __syncthreads();
-  if (tid < JT) to[tid] = (alpha ? alpha[a] : 1.0f) * ((red[0][tid] + red[1][tid]) + (red[2][tid] + red[3][tid]));
+  if (tid < JT) {
+    float v = (alpha ? alpha[a] : 1.0f) * ((red[0][tid] + red[1][tid]) + (red[2][tid] + red[3][tid]));
+    to[tid] = v;
+    if (packed.at) {
+      uint16_t* one = packed.place(t, (j0 + tid) & ~3) + ((j0 + tid) & 3);
+#pragma unroll
+      for (int part = 0; part < 3; ++part) {
+        const uint32_t w = __float_as_uint(v) & 0xFFFF0000u;
+        one[part * 512] = (uint16_t)(w >> 16);
+        v -= __uint_as_float(w);
+      }
+    }
+  }
 #endif
 }
 
@@ -147,14 +176,14 @@ __device__ __forceinline__ int next_of(int id0, int id1) {
 }
 #endif
 
-// part: [runs][M][rank]; runs == 1: p itself.
+// part: [runs][M][rank]; runs == 1: p itself, and its packed parts.
 template <int FMT, int JC>
 __global__ __launch_bounds__(256) void project_tile_kernel(int M, int K, int runs, const uint8_t* __restrict__ A,
                                                            int64_t lda, const uint8_t* __restrict__ SA,
                                                            const int32_t* __restrict__ ids, int adapters, int rank,
                                                            const uint16_t* __restrict__ down, int64_t ldd,
                                                            int64_t stride, const float* __restrict__ alpha,
-                                                           float* __restrict__ part) {
+                                                           float* __restrict__ part, MxPacked packed) {
 #if defined(__HIP_DEVICE_COMPILE__)
   typedef ProjectTile<FMT, JC> T;
   // Three arrays, so that the compiler's waits for what is on its way to one do
@@ -271,8 +300,12 @@ __global__ __launch_bounds__(256) void project_tile_kernel(int M, int K, int run
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int j = 0; j < JC; ++j)
-        if (own[t] == a && j0 + 16 * j + 4 * g < rank)
-          *reinterpret_cast<v4f*>(to + (int64_t)(wave * 32 + 16 * t + r) * rank + j0 + 16 * j + 4 * g) = acc[j][t] * f;
+        if (own[t] == a && j0 + 16 * j + 4 * g < rank) {
+          const int row = wave * 32 + 16 * t + r, rk = j0 + 16 * j + 4 * g;
+          const v4f v = acc[j][t] * f;
+          *reinterpret_cast<v4f*>(to + (int64_t)row * rank + rk) = v;
+          if (runs == 1 && packed.at) put_packed(packed, t0 + row, rk, v);
+        }
     if (id0 == a) id0 = -1;
     if (id1 == a) id1 = -1;
   }
@@ -282,7 +315,8 @@ __global__ __launch_bounds__(256) void project_tile_kernel(int M, int K, int run
 // p = alpha times the runs' sums, in order; four ranks a thread.
 __global__ __launch_bounds__(256) void project_join_kernel(const nt_f32x4* __restrict__ part, int runs, int64_t units,
                                                            int upr, const int32_t* __restrict__ ids, int adapters,
-                                                           const float* __restrict__ alpha, nt_f32x4* __restrict__ p) {
+                                                           const float* __restrict__ alpha, nt_f32x4* __restrict__ p,
+                                                           MxPacked packed) {
   const int64_t step = (int64_t)gridDim.x * 256;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < units; i += step) {
     const int a = ids[i / upr];
@@ -292,6 +326,9 @@ __global__ __launch_bounds__(256) void project_join_kernel(const nt_f32x4* __res
     for (int r = 0; r < runs; ++r) s += part[r * units + i];
     const float f = some && alpha ? alpha[a] : 1.0f;
     p[i] = some ? s * f : nt_f32x4{0.0f, 0.0f, 0.0f, 0.0f};  // rows without an adapter: nothing was written
+#if defined(__HIP_DEVICE_COMPILE__)
+    if (some && packed.at) put_packed(packed, i / upr, (int)(i % upr) * 4, s * f);
+#endif
   }
 }
 
@@ -569,12 +606,12 @@ int project_runs(int64_t M, int64_t K, int64_t rank) {
 template <int FMT>
 void project(int64_t M, int64_t K, const uint8_t* a, int64_t lda, const uint8_t* sa, const int32_t* ids,
              int64_t adapters, int64_t rank, const uint16_t* down, int64_t ldd, int64_t stride, const float* alpha,
-             float* p, float* workspace, hipStream_t stream) {
+             float* p, MxPacked packed, float* workspace, hipStream_t stream) {
   if (M <= kFewRows) {
     // One rank a workgroup until four fill the chip.
 #define MXFP8_PR(JT)                                                                                            \
   hipLaunchKernelGGL((project_rows_kernel<FMT, JT>), dim3((uint32_t)(M * (rank / JT))), dim3(256), 0, stream,   \
-                     (int)K, a, lda, sa, ids, (int)adapters, (int)rank, down, ldd, stride, alpha, p)
+                     (int)K, a, lda, sa, ids, (int)adapters, (int)rank, down, ldd, stride, alpha, p, packed)
     if (M * rank < 4 * 256) MXFP8_PR(1);
     else MXFP8_PR(4);
 #undef MXFP8_PR
@@ -586,7 +623,7 @@ void project(int64_t M, int64_t K, const uint8_t* a, int64_t lda, const uint8_t*
   hipLaunchKernelGGL((project_tile_kernel<FMT, JC>),                                                              \
                      dim3((uint32_t)((M + kTileRows - 1) / kTileRows * runs), (uint32_t)((rank + 16 * JC - 1) / (16 * JC))), \
                      dim3(256), 0, stream, (int)M, (int)K, runs, a, lda, sa, ids, (int)adapters, (int)rank, down, ldd, \
-                     stride, alpha, to)
+                     stride, alpha, to, packed)
   if (rank <= 16) MXFP8_PT(1);
   else if (rank <= 32) MXFP8_PT(2);
   else MXFP8_PT(4);
@@ -595,7 +632,7 @@ void project(int64_t M, int64_t K, const uint8_t* a, int64_t lda, const uint8_t*
     const int64_t units = M * rank / 4, need = (units + 255) / 256;
     hipLaunchKernelGGL(project_join_kernel, dim3((uint32_t)(need < 4096 ? need : 4096)), dim3(256), 0, stream,
                        reinterpret_cast<const nt_f32x4*>(workspace), runs, units, (int)(rank / 4), ids, (int)adapters,
-                       alpha, reinterpret_cast<nt_f32x4*>(p));
+                       alpha, reinterpret_cast<nt_f32x4*>(p), packed);
   }
 }
 
@@ -635,16 +672,20 @@ using namespace mx_adapters_detail;
 
 void launch_mx_adapter_project(int64_t M, int64_t K, const uint8_t* a, int64_t lda, int a_fmt, const uint8_t* sa,
                                const int32_t* ids, int64_t adapters, int64_t rank, const uint16_t* down, int64_t ldd,
-                               int64_t stride, const float* alpha, float* p, float* workspace, hipStream_t stream) {
-  if (a_fmt == 0) project<0>(M, K, a, lda, sa, ids, adapters, rank, down, ldd, stride, alpha, p, workspace, stream);
-  else if (a_fmt == 1) project<1>(M, K, a, lda, sa, ids, adapters, rank, down, ldd, stride, alpha, p, workspace, stream);
-  else project<kE2M1>(M, K, a, lda, sa, ids, adapters, rank, down, ldd, stride, alpha, p, workspace, stream);
+                               int64_t stride, const float* alpha, float* p, uint16_t* packed, float* workspace,
+                               hipStream_t stream) {
+  const MxPacked to{packed, (int)((rank + 15) / 16)};
+  if (a_fmt == 0) project<0>(M, K, a, lda, sa, ids, adapters, rank, down, ldd, stride, alpha, p, to, workspace, stream);
+  else if (a_fmt == 1) project<1>(M, K, a, lda, sa, ids, adapters, rank, down, ldd, stride, alpha, p, to, workspace, stream);
+  else project<kE2M1>(M, K, a, lda, sa, ids, adapters, rank, down, ldd, stride, alpha, p, to, workspace, stream);
 }
 
 int64_t adapter_project_workspace(int64_t M, int64_t K, int64_t rank) {
   const int64_t runs = project_runs(M, K, rank);
   return runs == 1 ? 0 : runs * M * rank * (int64_t)sizeof(float);
 }
+
+int64_t adapter_packed_bytes(int64_t M, int64_t rank) { return MxPacked::elements(M, rank) * 2; }
 
 int64_t adapter_grad_workspace(int64_t M, int64_t C, int64_t rank, int64_t adapters) {
   const GradShape s = grad_shape(M, C, rank, adapters);

@@ -50,6 +50,10 @@ bool adapter_extents(int64_t M, int64_t adapters, int64_t rank) {
 bool adapter_ld(int64_t ld, int64_t row, int64_t stride) {
   return ld >= row && ld % 8 == 0 && ld <= kMaxGemmLd && stride >= 0 && stride % 8 == 0;
 }
+// p in the order in which the product's tiles read it; a product of few rows does without.
+int64_t packed_bytes(int64_t M, int64_t N, int64_t rank) {
+  return N > 0 && (M > 16 || N > mxfp8::kFewRowsN) ? mxfp8::adapter_packed_bytes(M, rank) : 0;
+}
 bool grad_extents(int64_t M, int64_t C, int64_t rank, int64_t adapters) {
   if (!adapter_extents(M, adapters, rank) || C < 0 || C > INT32_MAX / 2 || C % 32 != 0) return false;
   // A launch takes fewer than 2^32 threads.
@@ -285,8 +289,14 @@ int mx_adapter_project(int64_t M, int64_t K, const uint8_t* a, int64_t lda, int 
   if (shared({p, work ? workspace : nullptr}, {a, a_scales, ids, down, alpha})) return MXFP8_ERR_ALIAS;
   (void)hipGetLastError();
   mxfp8::launch_mx_adapter_project(M, K, a, lda, a_fmt, a_scales, ids, adapters, rank, down, ldd, down_stride, alpha, p,
-                                   static_cast<float*>(workspace), (hipStream_t)stream);
+                                   nullptr, static_cast<float*>(workspace), (hipStream_t)stream);
   return launch_status();
+}
+
+int64_t mxfp4_gemm_adapted_workspace(int64_t M, int64_t N, int64_t K, int64_t rank) {
+  if (N < 0 || N > INT32_MAX / 2 || !adapter_extents(M, 0, rank) || M == 0) return 0;
+  if (K < 0 || K > INT32_MAX / 2 || K % 128 != 0) return 0;
+  return packed_bytes(M, N, rank) + mxfp8::adapter_project_workspace(M, K, rank);
 }
 
 int mxfp4_gemm_adapted(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, int a_fmt,
@@ -300,7 +310,7 @@ int mxfp4_gemm_adapted(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_
   if (M == 0) return MXFP8_OK;
   if (!p || !ids || (N > 0 && !c)) return MXFP8_ERR_NULL;
   if (K > 0 && (!a || !a_scales || (adapters > 0 && !down) || (N > 0 && (!b || !b_scales)))) return MXFP8_ERR_NULL;
-  const bool work = mxfp8::adapter_project_workspace(M, K, rank) > 0;
+  const bool work = mxfp4_gemm_adapted_workspace(M, N, K, rank) > 0;
   if ((N > 0 && adapters > 0 && !up) || (work && !workspace)) return MXFP8_ERR_NULL;
   if (N > 0 && !ld_ok(ldc, N)) return MXFP8_ERR_LD;
   if (K > 0) {
@@ -316,11 +326,14 @@ int mxfp4_gemm_adapted(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_
   if (shared({c, p, work ? workspace : nullptr}, {a, b, a_scales, b_scales, ids, down, up, alpha}))
     return MXFP8_ERR_ALIAS;
   (void)hipGetLastError();
+  // The packed p first (a whole number of kilobytes), then the projection's runs.
+  uint16_t* packed = packed_bytes(M, N, rank) > 0 ? static_cast<uint16_t*>(workspace) : nullptr;
+  float* runs = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + packed_bytes(M, N, rank));
   mxfp8::launch_mx_adapter_project(M, K, a, lda, a_fmt, a_scales, ids, adapters, rank, down, ldd, down_stride, alpha, p,
-                                   static_cast<float*>(workspace), (hipStream_t)stream);
+                                   packed, runs, (hipStream_t)stream);
   if (N > 0)
-    mxfp8::launch_mxfp4_gemm_adapted(M, N, K, a, lda, a_fmt, a_scales, b, ldb, b_scales, ids, adapters, rank, p, up, ldu,
-                                     up_stride, c, ldc, c_dtype, (hipStream_t)stream);
+    mxfp8::launch_mxfp4_gemm_adapted(M, N, K, a, lda, a_fmt, a_scales, b, ldb, b_scales, ids, adapters, rank, p, packed,
+                                     up, ldu, up_stride, c, ldc, c_dtype, (hipStream_t)stream);
   return launch_status();
 }
 

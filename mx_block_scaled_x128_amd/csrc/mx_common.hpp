@@ -208,6 +208,22 @@ __device__ __forceinline__ MxParts mx_parts(const float (&f)[8]) {
   return o;
 }
 
+// p of the adapters as the product's tiles read it: for each 32 rows and 16
+// ranks three parts (as MxParts) of 512 bf16, in the order in which the lanes of
+// a v_mfma_f32_32x32x16_bf16 take them, so that a load is 1 KB without a gap.
+// Rows without an adapter and ranks past the last one are never written.
+struct MxPacked {
+  uint16_t* at;  // null: not wanted
+  int steps;     // of 16 ranks
+  __host__ __device__ static int64_t elements(int64_t rows, int64_t rank) {
+    return (rows + 31) / 32 * ((rank + 15) / 16) * (3 * 512);
+  }
+  // The first part of row t, ranks j (a multiple of 4) .. j + 3.
+  __device__ __forceinline__ uint16_t* place(int64_t t, int j) const {
+    return at + ((t >> 5) * steps + (j >> 4)) * (3 * 512) + ((t & 31) + 32 * (j >> 3 & 1)) * 8 + (j & 7);
+  }
+};
+
 // Eight codes of one lane from memory: 8 bytes of FP8, 4 of E2M1.
 template <int FMT>
 __device__ __forceinline__ uint2 mx_load_codes8(const uint8_t* p) {

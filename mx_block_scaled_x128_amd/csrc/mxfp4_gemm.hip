@@ -38,6 +38,7 @@ struct NoAdapters {};
 struct Adapters {
   const int32_t* ids;
   const float* p;       // [M][rank]
+  const uint16_t* packed;  // p as MxPacked
   const uint16_t* up;   // [adapters] at `stride`, each [N][ldu] bf16
   int64_t ldu, stride;
   int adapters, rank;
@@ -489,89 +490,114 @@ __device__ __forceinline__ uint32_t opaque(uint32_t x) {
 // up p as a tile's first accumulators (v_mfma_f32_32x32x16_bf16, whose results
 // lie as the scaled instruction's do): 16 ranks at a time of each adapter that
 // the wave's rows name, zeros for p in the rows of others.  m0, n0: the wave's
-// first row and column.
+// first row and column.  What does not depend on the rows' ids is asked for
+// before the tile's own first loads (`ask`).
 //
 // Zeros times an infinity or a NaN would not be zero.  So such values of up are
 // taken out, and `spoilt` keeps, for each of a lane's rows, the columns that
-// they leave without a result; true if there are any.  (Choosing row by row what
-// to add would take the accumulators through the vector registers.)
+// they leave without a result; add() says whether there are any.  (Choosing row
+// by row what to add would take the accumulators through the vector registers.)
 template <int PARTS, int MT, int NT>
-__device__ __forceinline__ bool first_adapters(const Adapters& ad, int M, int N, int m0, int n0, int lane,
-                                               v16f (&acc)[MT][NT], uint32_t (&spoilt)[MT][NT]) {
-  const int r = lane & 31, g = lane >> 5;
-  int id[MT];
-  bool any = false;
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    id[i] = m0 + 32 * i + r < M ? ad.ids[m0 + 32 * i + r] : -1;
-    if (id[i] >= ad.adapters) id[i] = -1;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) spoilt[i][j] = 0;
-  }
-  const __amdgpu_buffer_rsrc_t rp = descriptor(reinterpret_cast<const uint8_t*>(ad.p + (int64_t)m0 * ad.rank));
+struct FirstAdapters {
   struct In {
-    u32x4 u[NT];
-    MxRaw<float> p[MT];
+    v4i u[NT], p[MT][PARTS];
   };
-  for (int a = next_adapter(id); a >= 0; a = next_adapter(id)) {
-    const __amdgpu_buffer_rsrc_t ru =
-        descriptor(reinterpret_cast<const uint8_t*>(ad.up + a * ad.stride + (int64_t)n0 * ad.ldu));
-    auto load = [&](int k0, In& v) __attribute__((always_inline)) {
-      const int k = k0 + 8 * g;
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        v.u[j] = __builtin_bit_cast(u32x4, load16(ru, n0 + 32 * j + r < N && k < ad.rank
-                                                          ? (uint32_t)((32 * j + r) * ad.ldu + k) * 2 : kOutside, 0));
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-        mx_get(rp, id[i] == a && k < ad.rank ? (uint32_t)((32 * i + r) * ad.rank + k) * 4 : kOutside, 0, v.p[i]);
-    };
-    In v;
-    load(0, v);
-#pragma nounroll
-    for (int k0 = 0; k0 < ad.rank; k0 += 16) {
-      In next;
-      load(k0 + 16, next);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        bool bad = false;
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-          bad |= (v.u[j][w] & 0x7F80u) == 0x7F80u || (v.u[j][w] & 0x7F800000u) == 0x7F800000u;
-        const uint64_t where = __ballot(bad);
-        if (where) {
-          any = true;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            if ((v.u[j][w] & 0x7F80u) == 0x7F80u) v.u[j][w] &= 0xFFFF0000u;
-            if ((v.u[j][w] & 0x7F800000u) == 0x7F800000u) v.u[j][w] &= 0x0000FFFFu;
-          }
-#pragma unroll
-          for (int i = 0; i < MT; ++i)
-            if (id[i] == a) spoilt[i][j] |= (uint32_t)where | (uint32_t)(where >> 32);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        if (!__ballot(id[i] == a)) continue;
-        float f[8];
-        mx_unpack(v.p[i], f);
-        const MxParts p = mx_parts(f);
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int part = PARTS - 1; part >= 0; --part)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(mx_bf8, v.u[j]), p.part[part],
-                                                                acc[i][j], 0, 0, 0);
-      }
-      v = next;
-    }
+  int id[MT];
+  In first;
+  __amdgpu_buffer_rsrc_t rp;
+  uint32_t po;  // a lane's place in 1 KB
+  int steps;
+
+  // Past the last row's strip: nothing is read, no row is anybody's.
+  __device__ __forceinline__ void get_p(int m0, int M, int step, In& v) const {
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-      if (id[i] == a) id[i] = -1;
+#pragma unroll
+      for (int part = 0; part < PARTS; ++part)
+        v.p[i][part] = load16(rp, m0 + 32 * i < M && step < steps ? po : kOutside, ((i * steps + step) * 3 + part) * 1024);
   }
-  return any;
-}
+  __device__ __forceinline__ void ask(const Adapters& ad, int M, int m0, int lane) {
+    steps = (ad.rank + 15) >> 4;
+    po = lane * 16;
+    // m0 is a multiple of 32
+    rp = descriptor(reinterpret_cast<const uint8_t*>(ad.packed) + (int64_t)(m0 >> 5) * steps * 3072);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) id[i] = m0 + 32 * i + (lane & 31) < M ? ad.ids[m0 + 32 * i + (lane & 31)] : -1;
+    get_p(m0, M, 0, first);
+  }
+  __device__ __forceinline__ bool add(const Adapters& ad, int M, int N, int m0, int n0, int lane, v16f (&acc)[MT][NT],
+                                      uint32_t (&spoilt)[MT][NT]) {
+    const int r = lane & 31, g = lane >> 5;
+    bool any = false, once = true;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      if (id[i] >= ad.adapters) id[i] = -1;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) spoilt[i][j] = 0;
+    }
+    for (int a = next_adapter(id); a >= 0; a = next_adapter(id)) {
+      const __amdgpu_buffer_rsrc_t ru =
+          descriptor(reinterpret_cast<const uint8_t*>(ad.up + a * ad.stride + (int64_t)n0 * ad.ldu));
+      auto get_u = [&](int step, In& v) __attribute__((always_inline)) {
+        const int k = step * 16 + 8 * g;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          v.u[j] = load16(ru, n0 + 32 * j + r < N && k < ad.rank ? (uint32_t)((32 * j + r) * ad.ldu + k) * 2 : kOutside, 0);
+      };
+      In v = first;
+      get_u(0, v);
+      if (!once) get_p(m0, M, 0, v);
+      once = false;
+#pragma nounroll
+      for (int step = 0; step < steps; ++step) {
+        In next;
+        get_u(step + 1, next);
+        get_p(m0, M, step + 1, next);
+        const bool in = step * 16 + 8 * g < ad.rank;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          // an exponent of all ones carries into the bit above it
+          uint32_t over = 0;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) over |= ((uint32_t)v.u[j][w] & 0x7F807F80u) + 0x00800080u;
+          const uint64_t where = __ballot((over & 0x80008000u) != 0);
+          if (where) {
+            any = true;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t x = (uint32_t)v.u[j][w];
+              v.u[j][w] = (int)(((x & 0x7F80u) == 0x7F80u ? 0 : x & 0xFFFFu) |
+                                ((x & 0x7F800000u) == 0x7F800000u ? 0 : x & 0xFFFF0000u));
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+              if (id[i] == a) spoilt[i][j] |= (uint32_t)where | (uint32_t)(where >> 32);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const bool mine = id[i] == a;
+          if (!__ballot(mine)) continue;
+#pragma unroll
+          for (int part = PARTS - 1; part >= 0; --part) {
+            v4i p;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) p[w] = mine && in ? v.p[i][part][w] : 0;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(mx_bf8, v.u[j]),
+                                                                  __builtin_bit_cast(mx_bf8, p), acc[i][j], 0, 0, 0);
+          }
+        }
+        v = next;
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        if (id[i] == a) id[i] = -1;
+    }
+    return any;
+  }
+};
 #endif
 
 // SW: scale rows that start on 16-byte boundaries are loaded 16 bytes a lane,
@@ -589,6 +615,7 @@ __device__ __forceinline__ void gemm_tile(int M, int N, int K, const uint8_t* __
   constexpr int WM = BM / 2, WN = BN / 2, MT = WM / 32, NT = WN / 32;
   constexpr int A_LOADS = T::A_ST / (kTileThreads * 16), B_LOADS = T::B_ST / (kTileThreads * 16);
   constexpr int STEPS = A4 ? 2 : 1;  // 64-wide matrix steps per stage
+  constexpr bool ADAPT = std::is_same_v<AD, Adapters>;
 
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -829,7 +856,7 @@ __device__ __forceinline__ void gemm_tile(int M, int N, int K, const uint8_t* __
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           v4f v = v4f{acc[mt][nt][4 * q], acc[mt][nt][4 * q + 1], acc[mt][nt][4 * q + 2], acc[mt][nt][4 * q + 3]};
-          if constexpr (std::is_same_v<AD, Adapters>) {
+          if constexpr (ADAPT) {
             if (spoils) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
@@ -864,15 +891,20 @@ __device__ __forceinline__ void gemm_tile(int M, int N, int K, const uint8_t* __
     }
   };
 
+  // p's leading 16 bits are 2^-16 of it off, 24 none; bf16 results round by 2^-8.
+  [[maybe_unused]] std::conditional_t<ADAPT, FirstAdapters<sizeof(OutT) == 2 ? 2 : 3, MT, NT>, NoAdapters> lead;
+  if constexpr (ADAPT) {
+    lead.ask(ad, M, m0 + wm * WM, lane);
+    __builtin_amdgcn_sched_barrier(0);
+  }
   // The first RING K blocks in flight.
   scale_loads(0);
 #pragma unroll
   for (int q = 0; q < RING; ++q)
 #pragma unroll
     for (int item = 0; item < DMA_ITEMS; ++item) dma_item(q, q, item);
-  if constexpr (std::is_same_v<AD, Adapters>) {
-    // p's leading 16 bits are 2^-16 of it off, 24 none; bf16 results round by 2^-8.
-    spoils = first_adapters<sizeof(OutT) == 2 ? 2 : 3, MT, NT>(ad, M, N, m0 + wm * WM, n0 + wn * WN, lane, acc, spoilt);
+  if constexpr (ADAPT) {
+    spoils = lead.add(ad, M, N, m0 + wm * WM, n0 + wn * WN, lane, acc, spoilt);
     mfma_retire_pad();
   }
   wait_loads_and_meet<(RING - 1) * DMA_ITEMS>();
@@ -1030,7 +1062,7 @@ void gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const 
   const int chunks = (int)(K / 128);
   const int64_t n16 = (N + 15) / 16, pairs = ((N + 31) / 32) * ((M + 31) / 32);
   const int64_t wide = ((N + 63) / 64) * ((M + 31) / 32), cus = device_cus();
-  const bool few = (M <= 16 ? N <= (int64_t(1) << 26) : wide <= cus) &&
+  const bool few = (M <= 16 ? N <= kFewRowsN : wide <= cus) &&
                    (M <= 16 || pairs <= cus ? few_rows_lds<AFMT, 2, 2, 4, false>(0, (int)K)
                                             : few_rows_lds<AFMT, 2, 4, 4, false>(0, (int)K)) <= kFewRowsLds;
 #define MXFP4_FEW(MT, NT, WAVES, U)                                                                           \
@@ -1121,9 +1153,9 @@ void launch_mxfp4_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_
 
 void launch_mxfp4_gemm_adapted(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, int a_fmt,
                                const uint8_t* sa, const uint8_t* b, int64_t ldb, const uint8_t* sb, const int32_t* ids,
-                               int64_t adapters, int64_t rank, const float* p, const uint16_t* up, int64_t ldu,
-                               int64_t stride, void* c, int64_t ldc, int c_dtype, hipStream_t stream) {
-  const mxfp4_detail::Adapters ad{ids, p, up, ldu, stride, (int)adapters, (int)rank};
+                               int64_t adapters, int64_t rank, const float* p, const uint16_t* packed, const uint16_t* up,
+                               int64_t ldu, int64_t stride, void* c, int64_t ldc, int c_dtype, hipStream_t stream) {
+  const mxfp4_detail::Adapters ad{ids, p, packed, up, ldu, stride, (int)adapters, (int)rank};
   any_gemm(M, N, K, a, lda, a_fmt, sa, b, ldb, sb, c, ldc, c_dtype, ad, stream);
 }
 

@@ -34,6 +34,7 @@ struct Library {
   decltype(&::mx_adapter_project) mx_adapter_project;
   decltype(&::mx_adapter_project_workspace) mx_adapter_project_workspace;
   decltype(&::mxfp4_gemm_adapted) mxfp4_gemm_adapted;
+  decltype(&::mxfp4_gemm_adapted_workspace) mxfp4_gemm_adapted_workspace;
   decltype(&::mx_adapter_grad) mx_adapter_grad;
   decltype(&::mx_adapter_grad_workspace) mx_adapter_grad_workspace;
 } lib;
@@ -66,6 +67,7 @@ void bind(const std::string& path) {
   MXFP8_FIND(mx_adapter_project);
   MXFP8_FIND(mx_adapter_project_workspace);
   MXFP8_FIND(mxfp4_gemm_adapted);
+  MXFP8_FIND(mxfp4_gemm_adapted_workspace);
   MXFP8_FIND(mx_adapter_grad);
   MXFP8_FIND(mx_adapter_grad_workspace);
 #undef MXFP8_FIND
@@ -490,7 +492,7 @@ py::tuple mxfp4_adapted_gemm(const at::Tensor& a, const at::Tensor& sa, int a_fm
           "out_dtype must be float32 or bfloat16, got ", type);
   const Place on(stream, device_of({&a, &sa, &b, &sb, &down, &up, &ids, given(alpha), given(out)}));
   at::Tensor c = out.has_value() ? *out : on.pitched(M, N, type), p = on.fresh({M, rank}, at::kFloat);
-  at::Tensor work = on.scratch({lib.mx_adapter_project_workspace(M, K, rank)}, at::kByte);
+  at::Tensor work = on.scratch({lib.mxfp4_gemm_adapted_workspace(M, N, K, rank)}, at::kByte);
   status(lib.mxfp4_gemm_adapted(M, N, K, bytes(a), ld(a), a_fmt, bytes(sa), bytes(b), ld(b), bytes(sb), ints(ids),
                                 down.size(0), rank, bf16(down), adapter_ld(down), adapter_stride(down), bf16(up),
                                 adapter_ld(up), adapter_stride(up), floats(given(alpha)), floats(&p), ptr(c), ld(c),
