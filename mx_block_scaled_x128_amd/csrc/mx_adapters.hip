@@ -335,7 +335,7 @@ __global__ __launch_bounds__(256) void project_join_kernel(const nt_f32x4* __res
 // ---------------------------------------------------------------------------
 // Gradients: out[a][j][c] = sum over the rows t of a of p[t][j] z[t][c].
 // A workgroup takes 16 NF columns, 16 JT ranks, one adapter and one run of the
-// rows.  It lists its adapter's rows among the next 512 in LDS, in order, and
+// rows.  It lists its adapter's rows among the next 2048 in LDS, in order, and
 // its four waves take 32 of the list in turn; rows of other adapters are not
 // read.  v_mfma_f32_16x16x32_bf16 with z first: lane l = (m, g) loads NF columns
 // from column NF m of the rows 8 g .. 8 g + 7 of the 32, and column i of each
@@ -348,7 +348,8 @@ __global__ __launch_bounds__(256) void project_join_kernel(const nt_f32x4* __res
 // The runs' sums go to `part` and are joined in order; with one run they are
 // the result.
 // ---------------------------------------------------------------------------
-[[maybe_unused]] constexpr int kWindow = 512;
+// Rows listed at once: 2048, or 512 where as many rows would pass 32-bit offsets.
+[[maybe_unused]] constexpr int kWindow = 2048, kSmallWindow = 512;
 constexpr int kGradThreads = 256;
 template <int FMT>
 __device__ __forceinline__ mx_f2 two_codes(uint32_t w, float scale, int pair) {
@@ -385,7 +386,8 @@ __device__ __forceinline__ uint32_t load_scales(mx_rsrc r, uint32_t off, int lef
 
 struct GradArgs {
   int M, C, rank, adapters, runs, jgroups, ctiles;
-  int per;  // rows of a run
+  int per;     // rows of a run
+  int window;  // kWindow or kSmallWindow
   int transposed;
   int64_t ldz;
   float* out;    // one run: the gradients; else [runs] of them
@@ -398,8 +400,9 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(GradArgs q, const
                                                                const float* __restrict__ p,
                                                                const int32_t* __restrict__ ids) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int WORDS = FMT == kE2M1 ? NF / 8 : NF / 4, PER = FMT == kE2M1 ? 8 : 4;  // words of a lane and row, codes of a word
-  __shared__ int list[kWindow];
+  constexpr int WORDS = FMT == kE2M1 ? NF / 8 : NF / 4, CPW = FMT == kE2M1 ? 8 : 4;  // words of a lane and row, codes of a word
+  // The list is filled up to whole steps of all waves, and one step more, which is loaded ahead.
+  __shared__ __attribute__((aligned(16))) uint32_t list[kWindow + 256];
   __shared__ int found[kWindow / 64];
   __shared__ v4f red[2][NF * JT][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -410,8 +413,8 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(GradArgs q, const
   const int run = __builtin_amdgcn_readfirstlane(b2 / q.adapters), a = b2 - run * q.adapters;
   const int first = min(run * q.per, q.M), end = min(first + q.per, q.M);
   const int c0 = ct * (16 * NF), j0 = jg * (16 * JT), sk = q.C >> 5;
-  const int col = c0 + NF * m;
-  const bool col_in = col < q.C;
+  // Columns and ranks past the last ones: the last ones again, for results that nobody stores.
+  const int col = min(c0 + NF * m, q.C - NF), rk_in = min(j0 + JT * m, q.rank - JT);
   const uint32_t zo = FMT == kE2M1 ? col >> 1 : col;
   const bool s_dword = ((uintptr_t)SZ & 3) == 0 && (sk & 3) == 0;
   v4f acc[NF][JT];
@@ -426,39 +429,58 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(GradArgs q, const
     float p[8][JT];
   };
   // Which lane has the scale of row 8 g + i, and which byte it is there.
-  const int s_from = (8 * g * LPR + m * NF / 128) * 4, s_shift = 8 * (m * NF / 32 % 4);
+  const int block = (col >> 5) - (c0 >> 5);
+  const int s_from = (8 * g * LPR + block / 4) * 4, s_shift = 8 * (block % 4);
   const uint32_t s_col = (uint32_t)(c0 >> 5) + 4 * (lane % LPR);
   int total = 0;
-  for (int w0 = first; w0 < end; w0 += kWindow) {
-    // This adapter's rows of the window, in order.
-    uint64_t mine[kWindow / kGradThreads];
+  for (int w0 = first; w0 < end; w0 += q.window) {
+    // This adapter's rows of the window, in order: each wave counts every fourth
+    // 64 rows, then places them behind those before.
+    constexpr int PER = kWindow / kGradThreads;
+    const int span = min(q.window, end - w0);
+    uint64_t mine[PER];
+    int id[PER];
 #pragma unroll
-    for (int k = 0; k < kWindow / kGradThreads; ++k) {
-      const int t = w0 + k * kGradThreads + tid;
-      mine[k] = __ballot(t < end && ids[t < end ? t : first] == a);
-      if (lane == 0) found[k * 4 + wave] = __builtin_popcountll(mine[k]);
+    for (int k = 0; k < PER; ++k) {
+      const int t = k * kGradThreads + tid;
+      id[k] = -1;
+      if (k * kGradThreads < span && t < span) id[k] = ids[w0 + t];
+    }
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      mine[k] = __ballot(id[k] == a);
+      if (k * kGradThreads < span && lane == 0) found[k * 4 + wave] = __builtin_popcountll(mine[k]);
     }
     __syncthreads();
     int n = 0;
 #pragma unroll
     for (int k = 0; k < kWindow / 64; ++k) {
-      if (k % 4 == wave && (mine[k / 4] >> lane & 1))
-        list[n + __builtin_popcountll(mine[k / 4] & ((1ull << lane) - 1))] = k * 64 + lane;
-      n += found[k];
+      if (k / 4 * kGradThreads < span) {
+        if (k % 4 == wave && (mine[k / 4] >> lane & 1))
+          list[n + __builtin_popcountll(mine[k / 4] & ((1ull << lane) - 1))] = k * 64 + lane;
+        n += found[k];
+      }
     }
     n = __builtin_amdgcn_readfirstlane(n);
     total += n;
+    if (n == 0) {
+      __syncthreads();  // `found` has been read
+      continue;
+    }
+    __syncthreads();
+    // Places past the list's end name its first row, whose p is then not read but zero.
+    for (int i = n + tid; i < ((n + 127) & ~127) + 128; i += kGradThreads) list[i] = list[0];
     __syncthreads();
     const mx_rsrc rz = mx_run(Z + (int64_t)w0 * q.ldz), rs = mx_run(SZ + (int64_t)w0 * sk);
     const mx_rsrc rp = mx_run(p + (int64_t)w0 * q.rank);
     auto load = [&](int at, In& v) __attribute__((always_inline)) {
-      const int rk = j0 + JT * m;
+      const nt_u32x4 lo = *reinterpret_cast<const nt_u32x4*>(list + at + 8 * g);
+      const nt_u32x4 hi = *reinterpret_cast<const nt_u32x4*>(list + at + 8 * g + 4);
+      const bool whole = at + 32 <= n;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int e = at + 8 * g + i;
-        const bool in = e < n;
-        const uint32_t t = in ? (uint32_t)list[e] : 0;
-        const uint32_t off = in && col_in ? __umul24(t, (uint32_t)q.ldz) + zo : kNowhere;
+        const uint32_t t = i < 4 ? lo[i % 4] : hi[i % 4];
+        const uint32_t off = __umul24(t, (uint32_t)q.ldz) + zo;
         if constexpr (WORDS == 4) {
           const nt_u32x4 w = get16(rz, off, 0);
 #pragma unroll
@@ -470,12 +492,9 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(GradArgs q, const
         } else {
           v.z[i][0] = __builtin_amdgcn_raw_buffer_load_b32(rz, off, 0, 0);
         }
-        const uint32_t po = in && rk < q.rank ? (__umul24(t, (uint32_t)q.rank) + rk) * 4 : kNowhere;
-        if constexpr (JT == 4) {
-          const nt_u32x4 w = get16(rp, po, 0);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v.p[i][j] = __uint_as_float(w[j]);
-        } else if constexpr (JT == 2) {
+        uint32_t po = __umul24(t, (uint32_t)q.rank * 4) + (uint32_t)rk_in * 4;
+        if (!whole && at + 8 * g + i >= n) po = kNowhere;
+        if constexpr (JT == 2) {
           const uint2 w = mx_get_codes(rp, po, 0);
           v.p[i][0] = __uint_as_float(w.x);
           v.p[i][1] = __uint_as_float(w.y);
@@ -484,9 +503,8 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(GradArgs q, const
         }
       }
       // Row lane / LPR of the 32; bytes past the row's end are of columns that nobody stores.
-      const int e = at + lane / LPR;
-      const bool in = lane < 32 * LPR && e < n && s_col < (uint32_t)sk;
-      const uint32_t t = in ? (uint32_t)list[e] : 0;
+      const bool in = lane < 32 * LPR && s_col < (uint32_t)sk;
+      const uint32_t t = list[at + (lane / LPR) % 32];
       v.s = load_scales(rs, in ? __umul24(t, (uint32_t)sk) + s_col : kNowhere, sk - (int)s_col, s_dword);
     };
     In v;
@@ -500,29 +518,36 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(GradArgs q, const
         const uint32_t w = (uint32_t)__builtin_amdgcn_ds_bpermute(s_from + 4 * LPR * i, (int)v.s);
         scale[i] = __uint_as_float((w >> s_shift & 255u) << 23);
       }
-      nt_u32x4 zf[NF];
-#pragma unroll
-      for (int k = 0; k < WORDS; ++k)
-#pragma unroll
-        for (int h = 0; h < PER / 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const mx_f2 x = two_codes<FMT>(v.z[2 * i][k], scale[2 * i], h);
-            const mx_f2 y = two_codes<FMT>(v.z[2 * i + 1][k], scale[2 * i + 1], h);
-            zf[k * PER + 2 * h][i] = mx_bf16x2(x.x, y.x);
-            zf[k * PER + 2 * h + 1][i] = mx_bf16x2(x.y, y.y);
-          }
+      MxParts pp[JT];
 #pragma unroll
       for (int j = 0; j < JT; ++j) {
         float f[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = v.p[i][j];
-        const MxParts pp = mx_parts(f);
+        pp[j] = mx_parts(f);
+      }
+      // A word's columns at a time: as many fragments.
 #pragma unroll
-        for (int part = 2; part >= 0; --part)
+      for (int k = 0; k < WORDS; ++k) {
+        nt_u32x4 zf[CPW];
 #pragma unroll
-          for (int k = 0; k < NF; ++k)
-            acc[k][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(mx_bf8, zf[k]), pp.part[part], acc[k][j], 0, 0, 0);
+        for (int h = 0; h < CPW / 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const mx_f2 x = two_codes<FMT>(v.z[2 * i][k], scale[2 * i], h);
+            const mx_f2 y = two_codes<FMT>(v.z[2 * i + 1][k], scale[2 * i + 1], h);
+            zf[2 * h][i] = mx_bf16x2(x.x, y.x);
+            zf[2 * h + 1][i] = mx_bf16x2(x.y, y.y);
+          }
+#pragma unroll
+        for (int j = 0; j < JT; ++j)
+#pragma unroll
+          for (int part = 2; part >= 0; --part)
+#pragma unroll
+            for (int f = 0; f < CPW; ++f)
+              acc[k * CPW + f][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(mx_bf8, zf[f]), pp[j].part[part],
+                                                                            acc[k * CPW + f][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
       }
       v = next;
     }
@@ -552,7 +577,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(GradArgs q, const
   // A lane holds ranks JT m + j and, of fragment f, the columns NF (4 g + i) + f.
   float* out = q.out + ((int64_t)run * q.adapters + a) * q.rank * q.C;
   const int rk = j0 + JT * m;
-  if (rk >= q.rank) return;
+  if (rk >= q.rank) return;  // rk_in of another lane
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int c = c0 + NF * (4 * g + i);
@@ -642,15 +667,15 @@ struct GradShape {
 };
 GradShape grad_shape(int64_t M, int64_t C, int64_t rank, int64_t adapters) {
   GradShape s;
-  s.jt = rank <= 16 ? 1 : rank <= 32 ? 2 : 4;
+  s.jt = rank <= 16 ? 1 : 2;
   s.nf = s.jt == 1 ? 16 : 8;
   s.jgroups = (int)((rank + 16 * s.jt - 1) / (16 * s.jt));
   s.ctiles = (int)((C + 16 * s.nf - 1) / (16 * s.nf));
-  // Two workgroups to each of 256 compute units, runs of 256 rows at least, and
-  // at most 256 MB of partial sums.
+  // Two workgroups to each of 256 compute units, runs of 128 rows at least to
+  // each adapter, and at most 256 MB of partial sums.
   const int64_t wgs = (int64_t)s.ctiles * s.jgroups * adapters;
   int64_t runs = 512 / wgs;
-  const int64_t most = (M + 255) / 256, bytes = adapters * rank * C * 4;
+  const int64_t most = M / (128 * adapters), bytes = adapters * rank * C * 4;
   if (runs > most) runs = most;
   if (runs * bytes > (int64_t(256) << 20)) runs = (int64_t(256) << 20) / bytes;
   s.runs = (int)(runs < 1 ? 1 : runs);  // M == 0: one run of no rows, which gives zeros
@@ -662,8 +687,7 @@ void grad(const GradShape& s, const GradArgs& q, const uint8_t* z, const uint8_t
           const int32_t* ids, hipStream_t stream) {
   const dim3 grid((uint32_t)s.ctiles * (uint32_t)s.jgroups * (uint32_t)q.adapters * (uint32_t)s.runs);
   if (s.jt == 1) hipLaunchKernelGGL((grad_kernel<FMT, 1, 16>), grid, dim3(kGradThreads), 0, stream, q, z, sz, p, ids);
-  else if (s.jt == 2) hipLaunchKernelGGL((grad_kernel<FMT, 2, 8>), grid, dim3(kGradThreads), 0, stream, q, z, sz, p, ids);
-  else hipLaunchKernelGGL((grad_kernel<FMT, 4, 8>), grid, dim3(kGradThreads), 0, stream, q, z, sz, p, ids);
+  else hipLaunchKernelGGL((grad_kernel<FMT, 2, 8>), grid, dim3(kGradThreads), 0, stream, q, z, sz, p, ids);
 }
 
 }  // namespace mx_adapters_detail
@@ -706,6 +730,7 @@ void launch_mx_adapter_grad(int64_t M, int64_t C, const uint8_t* z, int64_t ldz,
   q.M = (int)M, q.C = (int)C, q.rank = (int)rank, q.adapters = (int)adapters;
   q.per = (int)((M + s.runs - 1) / s.runs + 31) / 32 * 32;
   q.runs = s.runs, q.jgroups = s.jgroups, q.ctiles = s.ctiles, q.transposed = transposed, q.ldz = ldz;
+  q.window = ldz < (int64_t(1) << 31) / kWindow ? kWindow : kSmallWindow;
   q.out = s.runs == 1 ? out : static_cast<float*>(workspace);
   q.counts = s.runs == 1 ? nullptr : reinterpret_cast<int*>(q.out + s.runs * adapters * rank * C);
   if (z_fmt == 0) grad<0>(s, q, z, sz, p, ids, stream);

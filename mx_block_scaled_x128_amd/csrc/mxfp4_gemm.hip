@@ -183,81 +183,95 @@ __device__ __forceinline__ int next_adapter(const int (&id)[MT]) {
   }
   return a;
 }
-// up p in the few-row kernel's accumulators: pieces of 32 ranks of each adapter
-// that the workgroup's rows name, dealt to the waves in turn, DEPTH of them on
-// their way at once.  A lane's four results belong to one row, so rows of other
-// adapters keep what they had, whatever this one's values are.
+// up p of the few-row kernel's rows: pieces of 32 ranks of each adapter that
+// they name, dealt to the waves in turn.  A wave adds DEPTH of them between
+// batches of the product, with the next ones on their way, so that their loads
+// cost no waiting of their own while the product lasts.  (All of them in front of
+// it, or a row at a time with its loads in a longer run of code, took 2 to 7 us
+// more than the product alone; so does code that every workgroup fetches anew.)
+// A lane's four results belong to one row, so rows of other adapters keep what
+// they had, whatever this one's values are.
 template <int MT, int NT, int WAVES>
-__device__ __forceinline__ void add_adapters(const Adapters& ad, int m0, int n0, int rows_a, int rows_b, int wave,
-                                             int lane, v4f (&acc)[MT][NT]) {
-  constexpr int DEPTH = 2;
-  const int r = lane & 15, g = lane >> 4;
-  int id[MT], left[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    id[i] = 16 * i + r < rows_a ? ad.ids[m0 + 16 * i + r] : -1;
-    if (id[i] >= ad.adapters) id[i] = -1;
-    left[i] = id[i];
-  }
-  // Lane n of `names` holds the n-th adapter.
-  int names = -1, count = 0;
-  for (int a = next_adapter(left); a >= 0; a = next_adapter(left)) {
-    if (lane == count) names = a;
-    ++count;
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-      if (left[i] == a) left[i] = -1;
-  }
-  const int per = (ad.rank + 31) >> 5, pieces = count * per;
-  const __amdgpu_buffer_rsrc_t rp = descriptor(reinterpret_cast<const uint8_t*>(ad.p + (int64_t)m0 * ad.rank));
+struct RowAdapters {
+  static constexpr int DEPTH = 2, LOADS = DEPTH * (NT + 2 * MT);
   struct Piece {
     int a;
-    mx_bf8 u[NT];
+    v4i u[NT];
     MxRaw<float> p[MT];
   };
-  auto load = [&](int n, Piece& v) __attribute__((always_inline)) {
-    const bool in = n < pieces;
-    const int which = in ? n / per : 0;
-    v.a = __builtin_amdgcn_readlane(names, which);
-    const int k = (n - which * per) * 32 + 8 * g;
+  int id[MT], names, per, pieces, n;
+  Piece v[DEPTH];
+  v4f sum[MT][NT];
+
+  __device__ __forceinline__ void load(const Adapters& ad, int m0, int n0, int rows_b, int lane, int at, Piece& v) const {
+    const int r = lane & 15, g = lane >> 4;
+    const bool in = at < pieces;
+    const int which = in ? at / per : 0, k = (at - which * per) * 32 + 8 * g;
+    v.a = in ? __builtin_amdgcn_readlane(names, which) : -2;
+    const __amdgpu_buffer_rsrc_t rp = descriptor(reinterpret_cast<const uint8_t*>(ad.p + (int64_t)m0 * ad.rank));
     const __amdgpu_buffer_rsrc_t ru = descriptor(
         reinterpret_cast<const uint8_t*>(ad.up + (in ? v.a * ad.stride + (int64_t)n0 * ad.ldu : 0)));
 #pragma unroll
     for (int j = 0; j < NT; ++j)
-      v.u[j] = __builtin_bit_cast(mx_bf8, load16(ru, in && 16 * j + r < rows_b && k < ad.rank
-                                                         ? (uint32_t)((16 * j + r) * ad.ldu + k) * 2 : kOutside, 0));
+      v.u[j] = load16(ru, in && 16 * j + r < rows_b && k < ad.rank ? (uint32_t)((16 * j + r) * ad.ldu + k) * 2 : kOutside, 0);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-      mx_get(rp, in && id[i] == v.a && k < ad.rank ? (uint32_t)((16 * i + r) * ad.rank + k) * 4 : kOutside, 0, v.p[i]);
-  };
-  auto add = [&](const Piece& v) __attribute__((always_inline)) {
+      mx_get(rp, id[i] == v.a && k < ad.rank ? (uint32_t)((16 * i + r) * ad.rank + k) * 4 : kOutside, 0, v.p[i]);
+  }
+  // The ids, before anything else is asked for.
+  __device__ __forceinline__ void ask(const Adapters& ad, int m0, int rows_a, int lane) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) id[i] = 16 * i + (lane & 15) < rows_a ? ad.ids[m0 + 16 * i + (lane & 15)] : -1;
+  }
+  // Lane n of `names` holds the n-th adapter; the first pieces' loads.
+  __device__ __forceinline__ void start(const Adapters& ad, int m0, int n0, int rows_b, int wave, int lane) {
+    int left[MT], count = 0;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      float f[8];
-      mx_unpack(v.p[i], f);
-      const MxParts p = mx_parts(f);
-      const bool mine = id[i] == v.a;
+      if (id[i] >= ad.adapters) id[i] = -1;
+      left[i] = id[i];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        v4f s = acc[i][j];
-#pragma unroll
-        for (int part = 2; part >= 0; --part) s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v.u[j], p.part[part], s, 0, 0, 0);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = mine ? s[e] : acc[i][j][e];
-      }
+      for (int j = 0; j < NT; ++j) sum[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
-  };
-  Piece v[DEPTH];
+    names = -1;
+    for (int a = next_adapter(left); a >= 0; a = next_adapter(left)) {
+      if (lane == count) names = a;
+      ++count;
 #pragma unroll
-  for (int d = 0; d < DEPTH; ++d) load(wave + d * WAVES, v[d]);
-  for (int n = wave; n < pieces; n += DEPTH * WAVES) {
+      for (int i = 0; i < MT; ++i)
+        if (left[i] == a) left[i] = -1;
+    }
+    per = (ad.rank + 31) >> 5;
+    pieces = count * per;
+    n = wave;
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) load(ad, m0, n0, rows_b, lane, n + d * WAVES, v[d]);
+  }
+  __device__ __forceinline__ void step(const Adapters& ad, int m0, int n0, int rows_b, int lane) {
+    if (n >= pieces) return;
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
-      if (n + d * WAVES < pieces) add(v[d]);
-      load(n + (d + DEPTH) * WAVES, v[d]);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        float f[8];
+        mx_unpack(v[d].p[i], f);
+        const MxParts p = mx_parts(f);
+        const bool mine = id[i] == v[d].a;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          v4f s = sum[i][j];
+#pragma unroll
+          for (int part = 2; part >= 0; --part)
+            s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(mx_bf8, v[d].u[j]), p.part[part], s, 0, 0, 0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[i][j][e] = mine ? s[e] : sum[i][j][e];
+        }
+      }
+      load(ad, m0, n0, rows_b, lane, n + (d + DEPTH) * WAVES, v[d]);
     }
+    n += DEPTH * WAVES;
   }
-}
+};
 #endif
 
 template <int AFMT, int MT, int NT, int WAVES, int U, bool ALDS, typename OutT, typename AD>
@@ -277,8 +291,14 @@ __global__ __launch_bounds__(WAVES * 64) void few_rows_kernel(int M, int N, int 
   const int rows_a = min(16 * MT, M - m0), rows_b = min(16 * NT, N - n0);
   const int chunks = K >> 7, sk = K >> 5;
   const int c0 = (int)((int64_t)chunks * wave / WAVES), c1 = (int)((int64_t)chunks * (wave + 1) / WAVES);
+  constexpr bool ADAPT = std::is_same_v<AD, Adapters>;
   uint8_t *lsa = lds, *lsb = lsa + kilo(16 * MT * sk), *la = lsb + kilo(16 * NT * sk);
 
+  [[maybe_unused]] std::conditional_t<ADAPT, RowAdapters<MT, NT, WAVES>, NoAdapters> rows;
+  if constexpr (ADAPT) {
+    rows.ask(ad, m0, rows_a, lane);
+    __builtin_amdgcn_sched_barrier(0);
+  }
   copy_to_lds<WAVES>(SA + (int64_t)m0 * sk, rows_a * sk, lsa, wave, lane);
   copy_to_lds<WAVES>(SB + (int64_t)n0 * sk, rows_b * sk, lsb, wave, lane);
   const __amdgpu_buffer_rsrc_t ra = descriptor(A + (int64_t)m0 * lda), rb = descriptor(B + (int64_t)n0 * ldb);
@@ -364,10 +384,7 @@ __global__ __launch_bounds__(WAVES * 64) void few_rows_kernel(int M, int N, int 
   Batch x, y;
   load(c0, x);
   load(c0 + U, y);
-  if constexpr (std::is_same_v<AD, Adapters>) {
-    add_adapters<MT, NT, WAVES>(ad, m0, n0, rows_a, rows_b, wave, lane, acc);
-    mfma_retire_pad();
-  }
+  if constexpr (ADAPT) rows.start(ad, m0, n0, rows_b, wave, lane);
   auto pin = [](Batch& v) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -384,7 +401,8 @@ __global__ __launch_bounds__(WAVES * 64) void few_rows_kernel(int M, int N, int 
   };
   pin(x);
   pin(y);
-  wait_loads_and_meet<0>();
+  if constexpr (ADAPT) wait_loads_and_meet<RowAdapters<MT, NT, WAVES>::LOADS>();  // all but the pieces', the last
+  else wait_loads_and_meet<0>();
   for (int c = c0; c < c1; c += 2 * U) {
     multiply(c, x);
     __builtin_amdgcn_sched_barrier(0);  // each load is issued a batch ahead of its use
@@ -392,10 +410,19 @@ __global__ __launch_bounds__(WAVES * 64) void few_rows_kernel(int M, int N, int 
     __builtin_amdgcn_sched_barrier(0);
     multiply(c + U, y);
     __builtin_amdgcn_sched_barrier(0);
+    if constexpr (ADAPT) rows.step(ad, m0, n0, rows_b, lane);
     load(c + 3 * U, y);
     __builtin_amdgcn_sched_barrier(0);
   }
   mfma_retire_pad();
+  if constexpr (ADAPT) {
+#pragma nounroll
+    while (rows.n < rows.pieces) rows.step(ad, m0, n0, rows_b, lane);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[i][j] += rows.sum[i][j];
+  }
   auto store = [&](int i, int j, v4f v) __attribute__((always_inline)) {
     const int m = m0 + 16 * i + r, n = n0 + 16 * j + 4 * g;
     if (m < M) store4(C + (int64_t)m * ldc + n, v, N - n);
