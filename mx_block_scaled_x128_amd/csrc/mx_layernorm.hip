@@ -29,6 +29,28 @@ namespace mxfp8 {
 namespace mx_layernorm_detail {
 
 #if defined(__HIP_DEVICE_COMPILE__)
+// The largest |f|, NaN if one is: absmax8 in 4 instructions.
+__device__ __forceinline__ uint32_t largest8(const float (&f)[8]) {
+  float m;
+  asm("v_maximum3_f32 %0, |%1|, |%2|, |%3|" : "=v"(m) : "v"(f[0]), "v"(f[1]), "v"(f[2]));
+  asm("v_maximum3_f32 %0, %0, |%1|, |%2|" : "+v"(m) : "v"(f[3]), "v"(f[4]));
+  asm("v_maximum3_f32 %0, %0, |%1|, |%2|" : "+v"(m) : "v"(f[5]), "v"(f[6]));
+  asm("v_maximum3_f32 %0, %0, |%1|, |%1|" : "+v"(m) : "v"(f[7]));
+  return __float_as_uint(m);
+}
+// Sum of eight elements as read.
+__device__ __forceinline__ float sum8(const MxRaw<float>& r) {
+  return ((r.a.x + r.a.y) + (r.a.z + r.a.w)) + ((r.b.x + r.b.y) + (r.b.z + r.b.w));
+}
+__device__ __forceinline__ float sum8(const MxRaw<uint16_t>& r) {
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  const b2 one = {(__bf16)1.0f, (__bf16)1.0f};
+  float s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, r.v.x), one, 0.0f, false);
+  s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, r.v.y), one, s, false);
+  s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, r.v.z), one, s, false);
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, r.v.w), one, s, false);
+}
+
 // LDS written before is read after, by all waves; loads from memory stay in flight.
 __device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
@@ -154,11 +176,7 @@ __global__ __launch_bounds__(1024) void forward_kernel(
     for (int k = 0; k < RB; ++k) {
       s1[k] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < NU; ++i) {
-        float f[8];
-        mx_unpack(raw[k][i], f);
-        s1[k] += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
-      }
+      for (int i = 0; i < NU; ++i) s1[k] += sum8(raw[k][i]);
     }
     reduce(s1);
     float m0[RB], e[2 * RB];
@@ -248,7 +266,7 @@ __global__ __launch_bounds__(1024) void forward_kernel(
         mx_unpack(raw[k][i], f);
         if (scale == 0.0f) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = ((f[j] - m0[k]) - delta) * r;
+          for (int j = 0; j < 8; ++j) f[j] = ((f[j] - m0[k]) - delta) * r;  // zero for equal values
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) f[j] = (float)(((double)(f[j] * scale) - mean) * rr);
@@ -257,11 +275,11 @@ __global__ __launch_bounds__(1024) void forward_kernel(
         if constexpr (!KEEP_W) affine(i, wl, bl);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = __builtin_fmaf(f[j], KEEP_W ? wk[j] : wl[j], KEEP_W ? bk[j] : bl[j]);
-        const uint32_t sv = mx_scale<FMT, CEIL>(max_quad(absmax8(v)));
+        const uint32_t sv = mx_scale<FMT, CEIL>(max_quad(largest8(v)));
         mx_put_codes(ry, at(i, in, cq), i * ustep * 8, mx_codes8<FMT, CEIL>(v, sv));
         mx_put_byte(rys, at(i, in, cs), i * ustep / 4, sv);
         if (kept) {
-          const uint32_t sk = mx_scale<FMT, CEIL>(max_quad(absmax8(f)));
+          const uint32_t sk = mx_scale<FMT, CEIL>(max_quad(largest8(f)));
           mx_put_codes(rk, at(i, in, cq), i * ustep * 8, mx_codes8<FMT, CEIL>(f, sk));
           mx_put_byte(rks, at(i, in, cs), i * ustep / 4, sk);
         }
