@@ -622,8 +622,9 @@ constexpr int64_t kFewRows = 256;
 int project_runs(int64_t M, int64_t K, int64_t rank) {
   if (M <= kFewRows) return 1;
   const int64_t tiles = (M + kTileRows - 1) / kTileRows * ((rank + 63) / 64), chunks = K / 128;
-  // Two workgroups to each of 256 compute units, runs of four chunks at least.
-  int64_t runs = 512 / tiles;
+  // As many workgroups as 256 compute units hold at once (their buffers: two to a
+  // unit up to 32 ranks, else one), runs of four chunks at least.
+  int64_t runs = (rank <= 32 ? 512 : 256) / tiles;
   if (runs > chunks / 4) runs = chunks / 4;
   return (int)(runs < 1 ? 1 : runs);
 }

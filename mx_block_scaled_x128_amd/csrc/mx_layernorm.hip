@@ -167,7 +167,7 @@ __global__ __launch_bounds__(1024) void forward_kernel(
   float wk[8], bk[8];
   if constexpr (KEEP_W) affine(0, wk, bk);
   const double n = (double)(upr * 8);
-  const float inv_n = (float)(1.0 / n);
+  const float inv_n = (float)(1.0 / n), inv_n_low = (float)(1.0 / n - (double)inv_n);
   for (; row0 < rows; row0 += step) {
     MxRaw<InT> next[RB][NU];
     if constexpr (AHEAD) load(row0 + step, next);
@@ -184,8 +184,10 @@ __global__ __launch_bounds__(1024) void forward_kernel(
     for (int k = 0; k < RB; ++k) {
       words_again(raw[k]);
       // One rounded m0 for both uses: as a product, it would be contracted into
-      // each difference, which then would round differences of its own.
+      // each difference, which then would round differences of its own.  Sixteen
+      // bits of it where x has eight: so nearly all differences are exact.
       m0[k] = s1[k] * inv_n;
+      if constexpr (sizeof(InT) == 2) m0[k] = __uint_as_float((__float_as_uint(m0[k]) + 0x80u) & 0xFFFFFF00u);
       asm volatile("" : "+v"(m0[k]));
       e[2 * k] = 0.0f, e[2 * k + 1] = 0.0f;
 #pragma unroll
@@ -212,13 +214,20 @@ __global__ __launch_bounds__(1024) void forward_kernel(
       const bool in = row < rows;
       const mx_rsrc ry = mx_run(y + row * ldy), rys = mx_run(ys + row * nb);
       const mx_rsrc rk = mx_run(kept + row * ldk), rks = mx_run(ks + row * nb);
-      // One Newton step behind the hardware's root (1 ulp): r is within an ulp of
-      // what the variance gives.  (The same in 64 bits, in every wave of a row:
-      // 16384x3584 bf16 75 us in place of 60.)
-      const float delta = e[2 * k] * inv_n;
-      const float var = __builtin_fmaf(e[2 * k + 1], inv_n, __builtin_fmaf(-delta, delta, eps));
+      // 1 / n in two parts and one Newton step with its own rounding error behind
+      // the hardware's root (1 ulp): r is the nearest fp32 value or the next to
+      // what the variance gives.  What r is off by moves a whole row across the
+      // casts' ties.  (The same in 64 bits, in every wave of a row: 16384x3584
+      // bf16 75 us in place of 60.)
+      const float delta = __builtin_fmaf(e[2 * k], inv_n, e[2 * k] * inv_n_low);
+      const float var = __builtin_fmaf(e[2 * k + 1], inv_n,
+                                       __builtin_fmaf(e[2 * k + 1], inv_n_low, __builtin_fmaf(-delta, delta, eps)));
       float r = __builtin_amdgcn_rsqf(var);
-      r = __builtin_fmaf(r * 0.5f, __builtin_fmaf(-var * r, r, 1.0f), r);
+      {
+        const float t = var * r, low = __builtin_fmaf(var, r, -t);
+        r = __builtin_fmaf(r * 0.5f, __builtin_fmaf(-t, r, 1.0f) - low * r, r);
+      }
+      const float shift = -delta * r;
       // Squares that overflow in fp32, so few bits left that eps does not cover
       // the loss, or nothing left of them once m0's rounding is taken out: the
       // row scaled by a power of two, once more in 64 bits (the same branch in all
@@ -266,7 +275,7 @@ __global__ __launch_bounds__(1024) void forward_kernel(
         mx_unpack(raw[k][i], f);
         if (scale == 0.0f) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = ((f[j] - m0[k]) - delta) * r;  // zero for equal values
+          for (int j = 0; j < 8; ++j) f[j] = __builtin_fmaf(f[j] - m0[k], r, shift);
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) f[j] = (float)(((double)(f[j] * scale) - mean) * rr);
