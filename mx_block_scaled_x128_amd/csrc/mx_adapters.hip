@@ -351,32 +351,34 @@ __global__ __launch_bounds__(256) void project_join_kernel(const nt_f32x4* __res
 // Rows listed at once: 2048, or 512 where as many rows would pass 32-bit offsets.
 [[maybe_unused]] constexpr int kWindow = 2048, kSmallWindow = 512;
 constexpr int kGradThreads = 256;
+// Two codes of a word (FP8: pair 0, 1; E2M1: 0 to 3) -> two bf16 values, exactly.
 template <int FMT>
-__device__ __forceinline__ mx_f2 two_codes(uint32_t w, float scale, int pair) {
+__device__ __forceinline__ uint32_t two_codes(uint32_t w, float scale, int pair) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  // pair: which two codes of the word (FP8: 0, 1; E2M1: 0 to 3)
   if constexpr (FMT == kE2M1) {
-    return pair == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 0)
-           : pair == 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 1)
-           : pair == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 2)
-                       : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 3);
+    return __builtin_bit_cast(uint32_t, pair == 0   ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0)
+                                        : pair == 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1)
+                                        : pair == 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2)
+                                                    : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3));
   } else if constexpr (FMT == 0) {
-    return pair == 0 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, scale, false)
-                     : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, scale, true);
+    return __builtin_bit_cast(uint32_t, pair == 0 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false)
+                                                  : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true));
   } else {
-    return pair == 0 ? __builtin_amdgcn_cvt_scalef32_pk_f32_bf8(w, scale, false)
-                     : __builtin_amdgcn_cvt_scalef32_pk_f32_bf8(w, scale, true);
+    return __builtin_bit_cast(uint32_t, pair == 0 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, scale, false)
+                                                  : __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, scale, true));
   }
 #else
-  return mx_f2{};
+  return 0;
 #endif
 }
 
 #if defined(__HIP_DEVICE_COMPILE__)
-// Four scale bytes, `left` of them in the row: as a dword where rows start on
-// one, else one by one.
-__device__ __forceinline__ uint32_t load_scales(mx_rsrc r, uint32_t off, int left, bool dword) {
-  if (dword) return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+// Four scale bytes, `left` of them in the row: DWORD where rows start on one,
+// else one by one.  (A choice made here would leave the count of loads on their
+// way open, and every wait would be for all of them.)
+template <bool DWORD>
+__device__ __forceinline__ uint32_t load_scales(mx_rsrc r, uint32_t off, int left) {
+  if constexpr (DWORD) return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
   uint32_t w = 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) w |= mx_get_byte(r, k < left ? off : kNowhere, k) << (8 * k);
@@ -394,16 +396,16 @@ struct GradArgs {
   int* counts;   // [runs][adapters] rows found, with more than one run
 };
 
-template <int FMT, int JT, int NF>
+template <int FMT, int JT, int NF, bool DWORD>
 __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(GradArgs q, const uint8_t* __restrict__ Z,
                                                                const uint8_t* __restrict__ SZ,
                                                                const float* __restrict__ p,
                                                                const int32_t* __restrict__ ids) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int WORDS = FMT == kE2M1 ? NF / 8 : NF / 4, CPW = FMT == kE2M1 ? 8 : 4;  // words of a lane and row, codes of a word
-  // The list is filled up to whole steps of all waves, and one step more, which is loaded ahead.
-  __shared__ __attribute__((aligned(16))) uint32_t list[kWindow + 256];
-  __shared__ int found[kWindow / 64];
+  // The list is filled up to whole steps of all waves, and two steps more, which are loaded ahead.
+  __shared__ __attribute__((aligned(16))) uint32_t list[kWindow + 384];
+  __shared__ int found[4];
   __shared__ v4f red[2][NF * JT][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m = lane & 15, g = lane >> 4;
@@ -416,7 +418,6 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(GradArgs q, const
   // Columns and ranks past the last ones: the last ones again, for results that nobody stores.
   const int col = min(c0 + NF * m, q.C - NF), rk_in = min(j0 + JT * m, q.rank - JT);
   const uint32_t zo = FMT == kE2M1 ? col >> 1 : col;
-  const bool s_dword = ((uintptr_t)SZ & 3) == 0 && (sk & 3) == 0;
   v4f acc[NF][JT];
 #pragma unroll
   for (int f = 0; f < NF; ++f)
@@ -434,31 +435,40 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(GradArgs q, const
   const uint32_t s_col = (uint32_t)(c0 >> 5) + 4 * (lane % LPR);
   int total = 0;
   for (int w0 = first; w0 < end; w0 += q.window) {
-    // This adapter's rows of the window, in order: each wave counts every fourth
-    // 64 rows, then places them behind those before.
-    constexpr int PER = kWindow / kGradThreads;
-    const int span = min(q.window, end - w0);
-    uint64_t mine[PER];
-    int id[PER];
+    // This adapter's rows of the window, in order: each wave counts those in a
+    // quarter of it, then places them behind those of the waves before.
+    const int span = min(q.window, end - w0), share = (span + 255) / 256;  // of 64 rows
+    int own = lane;
+    asm volatile("" : "+v"(own));  // what follows from it is not kept in registers from window to window
+    constexpr int MOST = kWindow / 256;
+    uint64_t mine[MOST];
+    int n = 0, id[MOST];
+    const mx_rsrc ri = mx_run(ids + w0);
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      const int t = k * kGradThreads + tid;
-      id[k] = -1;
-      if (k * kGradThreads < span && t < span) id[k] = ids[w0 + t];
+    for (int k = 0; k < MOST; ++k) {  // all on their way at once
+      const int t = (wave * share + k) * 64 + own;
+      id[k] = __builtin_amdgcn_raw_buffer_load_b32(ri, k < share && t < span ? t * 4 : kNowhere, 0, 0);
     }
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      mine[k] = __ballot(id[k] == a);
-      if (k * kGradThreads < span && lane == 0) found[k * 4 + wave] = __builtin_popcountll(mine[k]);
-    }
+    for (int k = 0; k < MOST; ++k)
+      mine[k] = __ballot(k < share && (wave * share + k) * 64 + own < span && id[k] == a);
+#pragma unroll
+    for (int k = 0; k < MOST; ++k) n += __builtin_popcountll(mine[k]);
+    if (lane == 0) found[wave] = n;
     __syncthreads();
-    int n = 0;
+    int at_row = 0;
+    n = 0;
 #pragma unroll
-    for (int k = 0; k < kWindow / 64; ++k) {
-      if (k / 4 * kGradThreads < span) {
-        if (k % 4 == wave && (mine[k / 4] >> lane & 1))
-          list[n + __builtin_popcountll(mine[k / 4] & ((1ull << lane) - 1))] = k * 64 + lane;
-        n += found[k];
+    for (int k = 0; k < 4; ++k) {
+      if (k < wave) at_row += found[k];
+      n += found[k];
+    }
+#pragma unroll
+    for (int k = 0; k < MOST; ++k) {
+      if (k < share) {
+        if (mine[k] >> own & 1)
+          list[at_row + __builtin_popcountll(mine[k] & ((1ull << own) - 1))] = (wave * share + k) * 64 + own;
+        at_row += __builtin_popcountll(mine[k]);
       }
     }
     n = __builtin_amdgcn_readfirstlane(n);
@@ -469,7 +479,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(GradArgs q, const
     }
     __syncthreads();
     // Places past the list's end name its first row, whose p is then not read but zero.
-    for (int i = n + tid; i < ((n + 127) & ~127) + 128; i += kGradThreads) list[i] = list[0];
+    for (int i = n + tid; i < ((n + 127) & ~127) + 256; i += kGradThreads) list[i] = list[0];
     __syncthreads();
     const mx_rsrc rz = mx_run(Z + (int64_t)w0 * q.ldz), rs = mx_run(SZ + (int64_t)w0 * sk);
     const mx_rsrc rp = mx_run(p + (int64_t)w0 * q.rank);
@@ -503,21 +513,19 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(GradArgs q, const
         }
       }
       // Row lane / LPR of the 32; bytes past the row's end are of columns that nobody stores.
-      const bool in = lane < 32 * LPR && s_col < (uint32_t)sk;
       const uint32_t t = list[at + (lane / LPR) % 32];
-      v.s = load_scales(rs, in ? __umul24(t, (uint32_t)sk) + s_col : kNowhere, sk - (int)s_col, s_dword);
+      const bool in = lane < 32 * LPR && s_col < (uint32_t)sk;
+      v.s = load_scales<DWORD>(rs, in ? __umul24(t, (uint32_t)sk) + s_col : kNowhere, sk - (int)s_col);
     };
-    In v;
-    load(wave * 32, v);
-    for (int at = wave * 32; at < n; at += 128) {
-      In next;
-      load(at + 128, next);
+    auto multiply = [&](const In& v) __attribute__((always_inline)) {
       float scale[8];
+      int from = s_from;
+      asm volatile("" : "+v"(from));  // one register, not one to each of the eight
+      uint32_t sw[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t w = (uint32_t)__builtin_amdgcn_ds_bpermute(s_from + 4 * LPR * i, (int)v.s);
-        scale[i] = __uint_as_float((w >> s_shift & 255u) << 23);
-      }
+      for (int i = 0; i < 8; ++i) sw[i] = (uint32_t)__builtin_amdgcn_ds_bpermute(from + 4 * LPR * i, (int)v.s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) scale[i] = __uint_as_float((sw[i] >> s_shift & 255u) << 23);
       MxParts pp[JT];
 #pragma unroll
       for (int j = 0; j < JT; ++j) {
@@ -534,10 +542,10 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(GradArgs q, const
         for (int h = 0; h < CPW / 2; ++h)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const mx_f2 x = two_codes<FMT>(v.z[2 * i][k], scale[2 * i], h);
-            const mx_f2 y = two_codes<FMT>(v.z[2 * i + 1][k], scale[2 * i + 1], h);
-            zf[2 * h][i] = mx_bf16x2(x.x, y.x);
-            zf[2 * h + 1][i] = mx_bf16x2(x.y, y.y);
+            const uint32_t x = two_codes<FMT>(v.z[2 * i][k], scale[2 * i], h);
+            const uint32_t y = two_codes<FMT>(v.z[2 * i + 1][k], scale[2 * i + 1], h);
+            zf[2 * h][i] = __builtin_amdgcn_perm(y, x, 0x05040100u);
+            zf[2 * h + 1][i] = __builtin_amdgcn_perm(y, x, 0x07060302u);
           }
 #pragma unroll
         for (int j = 0; j < JT; ++j)
@@ -549,7 +557,24 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(GradArgs q, const
                                                                             acc[k * CPW + f][j], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
       }
-      v = next;
+    };
+    // Two steps' rows in registers, in turn (a copy from one to the other would
+    // cost a fifth of a step's instructions).  Loads stay where they are written:
+    // the compiler would move them behind the branch, down to their use.
+    auto ask = [&](int at, In& x) __attribute__((always_inline)) {
+      load(at, x);
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    In v, w;
+    ask(wave * 32, v);
+    ask(wave * 32 + 128, w);
+    for (int at = wave * 32; at < n; at += 256) {
+      multiply(v);
+      ask(at + 256, v);
+      if (at + 128 >= n) break;
+      multiply(w);
+      ask(at + 384, w);
     }
     __syncthreads();  // the list has been read
   }
@@ -687,8 +712,17 @@ template <int FMT>
 void grad(const GradShape& s, const GradArgs& q, const uint8_t* z, const uint8_t* sz, const float* p,
           const int32_t* ids, hipStream_t stream) {
   const dim3 grid((uint32_t)s.ctiles * (uint32_t)s.jgroups * (uint32_t)q.adapters * (uint32_t)s.runs);
-  if (s.jt == 1) hipLaunchKernelGGL((grad_kernel<FMT, 1, 16>), grid, dim3(kGradThreads), 0, stream, q, z, sz, p, ids);
-  else hipLaunchKernelGGL((grad_kernel<FMT, 2, 8>), grid, dim3(kGradThreads), 0, stream, q, z, sz, p, ids);
+  const bool dword = ((uintptr_t)sz & 3) == 0 && q.C % 128 == 0;
+#define MXFP8_G(JT, NF, DWORD) \
+  hipLaunchKernelGGL((grad_kernel<FMT, JT, NF, DWORD>), grid, dim3(kGradThreads), 0, stream, q, z, sz, p, ids)
+  if (s.jt == 1) {
+    if (dword) MXFP8_G(1, 16, true);
+    else MXFP8_G(1, 16, false);
+  } else {
+    if (dword) MXFP8_G(2, 8, true);
+    else MXFP8_G(2, 8, false);
+  }
+#undef MXFP8_G
 }
 
 }  // namespace mx_adapters_detail
