@@ -207,7 +207,7 @@ __global__ __launch_bounds__(256) void project_tile_kernel(int M, int K, int run
   // The rows whose results this lane holds.
   const int own[2] = {id_of(wave * 32 + r), id_of(wave * 32 + 16 + r)};
   float* to = part + ((int64_t)run * M + t0) * rank;
-  if (runs == 1) {
+  if (runs == 1 && blockIdx.z == 0) {
     for (int i = threadIdx.x; i < rows * 16 * JC; i += 256) {
       const int t = i / (16 * JC), j = j0 + i % (16 * JC);
       if (j < rank && (uint32_t)ids[t0 + t] >= (uint32_t)adapters) to[(int64_t)t * rank + j] = 0.0f;
@@ -235,7 +235,13 @@ __global__ __launch_bounds__(256) void project_tile_kernel(int M, int K, int run
   // Scales: waves 0 and 1 take 64 rows each, the others zeros (their loads count all the same).
   const uint32_t so = wave < 2 && wave * 64 + lane < rows ? (uint32_t)((wave * 64 + lane) * sk) : kNowhere;
   constexpr int LOADS = XI + DI + 1;
+  int turn = 0;
   for (int a = next_of(id0, id1); a >= 0; a = next_of(id0, id1)) {
+    if (id0 == a) id0 = -1;
+    if (id1 == a) id1 = -1;
+    const bool other = turn != (int)blockIdx.z;
+    turn = turn + 1 == (int)gridDim.z ? 0 : turn + 1;
+    if (other) continue;
     const mx_rsrc rd = mx_run(down + a * stride + j0 * ldd);
     auto load = [&](uint8_t* to, int c) __attribute__((always_inline)) {
       const bool in = c < c1;
@@ -306,8 +312,6 @@ __global__ __launch_bounds__(256) void project_tile_kernel(int M, int K, int run
           *reinterpret_cast<v4f*>(to + (int64_t)row * rank + rk) = v;
           if (runs == 1 && packed.at) put_packed(packed, t0 + row, rk, v);
         }
-    if (id0 == a) id0 = -1;
-    if (id1 == a) id1 = -1;
   }
 #endif
 }
@@ -644,14 +648,26 @@ __global__ __launch_bounds__(256) void grad_join_kernel(const nt_f32x4* __restri
 
 // Rows taken one by one up to this many, and the runs of K beyond.
 constexpr int64_t kFewRows = 256;
+int64_t project_tiles(int64_t M, int64_t rank) { return (M + kTileRows - 1) / kTileRows * ((rank + 63) / 64); }
+// Workgroups that 256 compute units hold at once (their buffers: two to a unit up to 32 ranks, else one).
+int64_t project_slots(int64_t rank) { return rank <= 32 ? 512 : 256; }
 int project_runs(int64_t M, int64_t K, int64_t rank) {
   if (M <= kFewRows) return 1;
-  const int64_t tiles = (M + kTileRows - 1) / kTileRows * ((rank + 63) / 64), chunks = K / 128;
-  // As many workgroups as 256 compute units hold at once (their buffers: two to a
-  // unit up to 32 ranks, else one), runs of four chunks at least.
-  int64_t runs = (rank <= 32 ? 512 : 256) / tiles;
+  const int64_t tiles = project_tiles(M, rank), chunks = K / 128;
+  // As many as there is room for, of four chunks at least.
+  int64_t runs = project_slots(rank) / tiles;
   if (runs > chunks / 4) runs = chunks / 4;
   return (int)(runs < 1 ? 1 : runs);
+}
+
+// Workgroups that share the adapters of a tile's rows, each a pass over the tile: twice those that there is room
+// for, since a tile may name few, and those without one end at once.  512 rows x 3584 of 32 adapters, mixed, rank 16
+// and 64: 17 and 27 us (one workgroup a tile and run: 66 and 120); of one adapter 9 and 11 either way.
+int project_split(int64_t M, int64_t rank, int64_t adapters, int runs) {
+  int64_t split = 2 * project_slots(rank) / (project_tiles(M, rank) * runs);
+  if (split > kTileRows) split = kTileRows;
+  if (split > adapters) split = adapters;
+  return (int)(split < 1 ? 1 : split);
 }
 
 template <int FMT>
@@ -670,10 +686,11 @@ void project(int64_t M, int64_t K, const uint8_t* a, int64_t lda, const uint8_t*
   }
   const int runs = project_runs(M, K, rank);
   float* to = runs == 1 ? p : workspace;
+  const int split = project_split(M, rank, adapters, runs);
 #define MXFP8_PT(JC)                                                                                              \
   hipLaunchKernelGGL((project_tile_kernel<FMT, JC>),                                                              \
-                     dim3((uint32_t)((M + kTileRows - 1) / kTileRows * runs), (uint32_t)((rank + 16 * JC - 1) / (16 * JC))), \
-                     dim3(256), 0, stream, (int)M, (int)K, runs, a, lda, sa, ids, (int)adapters, (int)rank, down, ldd, \
+                     dim3((uint32_t)((M + kTileRows - 1) / kTileRows * runs), (uint32_t)((rank + 16 * JC - 1) / (16 * JC)), \
+                          (uint32_t)split), dim3(256), 0, stream, (int)M, (int)K, runs, a, lda, sa, ids, (int)adapters, (int)rank, down, ldd, \
                      stride, alpha, to, packed)
   if (rank <= 16) MXFP8_PT(1);
   else if (rank <= 32) MXFP8_PT(2);

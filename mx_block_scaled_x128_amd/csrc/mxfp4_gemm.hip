@@ -526,17 +526,18 @@ __device__ __forceinline__ uint32_t opaque(uint32_t x) {
 // by row what to add would take the accumulators through the vector registers.)
 template <int PARTS, int MT, int NT>
 struct FirstAdapters {
-  struct In {
-    v4i u[NT], p[MT][PARTS];
+  static constexpr int LISTS = (MT + 1) / 2;
+  struct P {
+    v4i p[MT][PARTS];
   };
   int id[MT];
-  In first;
+  P first;
   __amdgpu_buffer_rsrc_t rp;
   uint32_t po;  // a lane's place in 1 KB
   int steps;
 
   // Past the last row's strip: nothing is read, no row is anybody's.
-  __device__ __forceinline__ void get_p(int m0, int M, int step, In& v) const {
+  __device__ __forceinline__ void get_p(int m0, int M, int step, P& v) const {
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -555,73 +556,114 @@ struct FirstAdapters {
   __device__ __forceinline__ bool add(const Adapters& ad, int M, int N, int m0, int n0, int lane, v16f (&acc)[MT][NT],
                                       uint32_t (&spoilt)[MT][NT]) {
     const int r = lane & 31, g = lane >> 5;
-    bool any = false, once = true;
+    bool any = false;
+    // Lane n & 63 of names[n >> 6] holds the n-th adapter.
+    int left[MT], names[LISTS], count = 0;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       if (id[i] >= ad.adapters) id[i] = -1;
+      left[i] = id[i];
 #pragma unroll
       for (int j = 0; j < NT; ++j) spoilt[i][j] = 0;
     }
-    for (int a = next_adapter(id); a >= 0; a = next_adapter(id)) {
-      const __amdgpu_buffer_rsrc_t ru =
-          descriptor(reinterpret_cast<const uint8_t*>(ad.up + a * ad.stride + (int64_t)n0 * ad.ldu));
-      auto get_u = [&](int step, In& v) __attribute__((always_inline)) {
-        const int k = step * 16 + 8 * g;
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-          v.u[j] = load16(ru, n0 + 32 * j + r < N && k < ad.rank ? (uint32_t)((32 * j + r) * ad.ldu + k) * 2 : kOutside, 0);
-      };
-      In v = first;
-      get_u(0, v);
-      if (!once) get_p(m0, M, 0, v);
-      once = false;
-#pragma nounroll
-      for (int step = 0; step < steps; ++step) {
-        In next;
-        get_u(step + 1, next);
-        get_p(m0, M, step + 1, next);
-        const bool in = step * 16 + 8 * g < ad.rank;
+    for (int k = 0; k < LISTS; ++k) names[k] = -1;
+    for (int a = next_adapter(left); a >= 0; a = next_adapter(left)) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          // an exponent of all ones carries into the bit above it
-          uint32_t over = 0;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) over |= ((uint32_t)v.u[j][w] & 0x7F807F80u) + 0x00800080u;
-          const uint64_t where = __ballot((over & 0x80008000u) != 0);
-          if (where) {
-            any = true;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const uint32_t x = (uint32_t)v.u[j][w];
-              v.u[j][w] = (int)(((x & 0x7F80u) == 0x7F80u ? 0 : x & 0xFFFFu) |
-                                ((x & 0x7F800000u) == 0x7F800000u ? 0 : x & 0xFFFF0000u));
-            }
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-              if (id[i] == a) spoilt[i][j] |= (uint32_t)where | (uint32_t)(where >> 32);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const bool mine = id[i] == a;
-          if (!__ballot(mine)) continue;
-#pragma unroll
-          for (int part = PARTS - 1; part >= 0; --part) {
-            v4i p;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) p[w] = mine && in ? v.p[i][part][w] : 0;
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(mx_bf8, v.u[j]),
-                                                                  __builtin_bit_cast(mx_bf8, p), acc[i][j], 0, 0, 0);
-          }
-        }
-        v = next;
-      }
+      for (int k = 0; k < LISTS; ++k)
+        if (lane + 64 * k == count) names[k] = a;
+      ++count;
 #pragma unroll
       for (int i = 0; i < MT; ++i)
-        if (id[i] == a) id[i] = -1;
+        if (left[i] == a) left[i] = -1;
     }
+    auto name = [&](int n) __attribute__((always_inline)) {
+      int a = __builtin_amdgcn_readlane(names[0], n & 63);
+      if constexpr (LISTS == 2) a = n < 64 ? a : __builtin_amdgcn_readlane(names[1], n & 63);
+      return a;
+    };
+    // Adapter by adapter 16 ranks at a time, `DEPTH` of them on their way.
+    int n = 0, step = 0, next_n = 0, next_step = 0;
+    auto ask_u = [&](v4i (&u)[NT]) __attribute__((always_inline)) {
+      const bool some = next_n < count;
+      const int k = next_step * 16 + 8 * g;
+      const __amdgpu_buffer_rsrc_t ru =
+          descriptor(reinterpret_cast<const uint8_t*>(ad.up + (some ? name(next_n) * ad.stride : 0) + (int64_t)n0 * ad.ldu));
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        u[j] = load16(ru, n0 + 32 * j + r < N && k < ad.rank && some ? (uint32_t)((32 * j + r) * ad.ldu + k) * 2 : kOutside, 0);
+    };
+    auto one = [&](v4i (&u)[NT], const P& now) __attribute__((always_inline)) {
+      const int a = name(n);
+      const bool in = step * 16 + 8 * g < ad.rank;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        // an exponent of all ones carries into the bit above it
+        uint32_t over = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) over |= ((uint32_t)u[j][w] & 0x7F807F80u) + 0x00800080u;
+        const uint64_t where = __ballot((over & 0x80008000u) != 0);
+        if (where) {
+          any = true;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t x = (uint32_t)u[j][w];
+            u[j][w] = (int)(((x & 0x7F80u) == 0x7F80u ? 0 : x & 0xFFFFu) |
+                              ((x & 0x7F800000u) == 0x7F800000u ? 0 : x & 0xFFFF0000u));
+          }
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            if (id[i] == a) spoilt[i][j] |= (uint32_t)where | (uint32_t)(where >> 32);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const bool mine = id[i] == a;
+        if (!__ballot(mine)) continue;
+#pragma unroll
+        for (int part = PARTS - 1; part >= 0; --part) {
+          v4i p;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) p[w] = mine && in ? now.p[i][part][w] : 0;
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(mx_bf8, u[j]),
+                                                                __builtin_bit_cast(mx_bf8, p), acc[i][j], 0, 0, 0);
+        }
+      }
+    };
+    auto run = [&](auto depth, auto single) __attribute__((always_inline)) {
+      constexpr int DEPTH = depth.value;
+      constexpr bool ONE = single.value;  // up to 16 ranks: p is there already
+      v4i u[DEPTH][NT];
+      P p[ONE ? 1 : DEPTH];
+      auto ask_next = [&](int d) __attribute__((always_inline)) {
+        ask_u(u[d]);
+        if constexpr (!ONE) get_p(m0, M, next_step, p[d]);
+        asm volatile("" ::: "memory");  // the loads stay here
+        if (ONE || ++next_step == steps) {
+          next_step = 0;
+          ++next_n;
+        }
+      };
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) ask_next(d);
+#pragma nounroll
+      while (n < count) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+          if (n >= count) break;
+          one(u[d], ONE ? first : p[d]);
+          ask_next(d);
+          if (ONE || ++step == steps) {
+            step = 0;
+            ++n;
+          }
+        }
+      }
+    };
+    if (steps == 1) run(std::integral_constant<int, NT >= 4 ? 3 : 6>{}, std::true_type{});
+    else run(std::integral_constant<int, 2>{}, std::false_type{});
     return any;
   }
 };

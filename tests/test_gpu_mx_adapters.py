@@ -2,8 +2,9 @@
 
 Tolerances, u = 2^-24.  p adds K exact products in fp32: a lane or matrix instruction adds at
 most K / 8 in a row, the joints 64 more, and alpha rounds once: (K / 8 + 66) u of the absolute
-sizes.  What an adapter adds to c is p times up, with the whole of p: rank + 8 additions, that
-many u of the sizes, and what p is off by.  The shared product itself is off by 2^-12 of its
+sizes.  What an adapter adds to c is p times up: rank + 8 additions, that many u of the sizes, and
+what p is off by.  (Tiles with bf16 results take p's leading 16 bits; 2^-16 of the sizes is
+inside the bf16 results' own bound, which has the products' 2^-12.)  The shared product itself is off by 2^-12 of its
 sizes, as everywhere; a row without an adapter has its bits.  A gradient adds its rows in fp32:
 rows + 16 u.  bf16 rounds once more (2^-8 of the value)."""
 import numpy as np
@@ -155,6 +156,20 @@ def test_product(M, K, N, rank, adapters, order, fmt):
     none = torch.from_numpy((c.ids < 0) | (c.ids >= adapters)).cuda()
     assert torch.equal(y[none], c.base()[none])
     assert torch.equal(half[none], c.base(out_dtype=torch.bfloat16)[none])
+
+
+# past 256 rows several workgroups share the adapters of the projection's tiles; a wave of the large tiles may name 128
+@pytest.mark.parametrize("M,K,N,rank,adapters", [(257, 640, 64, 16, 150), (300, 1280, 260, 8, 2), (700, 256, 300, 40, 90),
+                                                 (515, 2176, 130, 64, 1000), (4100, 128, 4352, 8, 400)])
+def test_rows_of_many_adapters(M, K, N, rank, adapters):
+    c = Case(M, K, N, mx.E4M3, rank, adapters, "mixed")
+    y, p = c.product()
+    p64, tol = c.exact_p()
+    close(p, p64, tol)
+    exact, tol = c.exact_c()
+    close(y, exact, tol)
+    close(c.product(out_dtype=torch.bfloat16)[0], exact, tol + 2.0 ** -8 * (np.abs(exact) + tol))
+    assert torch.equal(p, c.project()) and torch.equal(y, c.product()[0])
 
 
 @pytest.mark.parametrize("M,K,N,rank,adapters,order", [s for s in PRODUCT if s[0] * s[2] < 3e6])
