@@ -646,25 +646,28 @@ __global__ __launch_bounds__(256) void grad_join_kernel(const nt_f32x4* __restri
   }
 }
 
-// Rows taken one by one up to this many, and the runs of K beyond.
-constexpr int64_t kFewRows = 256;
+// Whether rows are taken one by one.  That costs 0.14 us a million of M rank K, whichever adapters they name; a tile
+// with its runs and their join 9 to 10 us if the rows name one adapter, and 17 to 50 if they name 32 or more, mixed.
+// 512x3584 rank 16: 7.3 row by row against 7.5 in tiles (17 mixed); 192x3584 rank 64: 9.9 against 9.5; 256x3584 rank
+// 64: 12.5 against 9.4 (23 mixed); 512x3584 rank 64: 22.8 against 9.7.  Past 512 rows of a short K the tiles' shared
+// loads count.
+bool row_by_row(int64_t M, int64_t K, int64_t rank) { return M <= 512 && M * rank * K <= 100 * 1000 * 1000; }
 int64_t project_tiles(int64_t M, int64_t rank) { return (M + kTileRows - 1) / kTileRows * ((rank + 63) / 64); }
-// Workgroups that 256 compute units hold at once (their buffers: two to a unit up to 32 ranks, else one).
-int64_t project_slots(int64_t rank) { return rank <= 32 ? 512 : 256; }
+// Runs of K: a workgroup to each of 256 compute units (two to a unit where their buffers would fit: 8192x3584 rank 16
+// 11.8 us in place of 9.7; one to two units: 4096x8960 rank 64 20.5 in place of 16.8), of four chunks at least
+// (515x8960 rank 8: 8.2 us, with eight 8.6, with two 9.5).
 int project_runs(int64_t M, int64_t K, int64_t rank) {
-  if (M <= kFewRows) return 1;
-  const int64_t tiles = project_tiles(M, rank), chunks = K / 128;
-  // As many as there is room for, of four chunks at least.
-  int64_t runs = project_slots(rank) / tiles;
+  if (row_by_row(M, K, rank)) return 1;
+  const int64_t chunks = K / 128;
+  int64_t runs = 256 / project_tiles(M, rank);
   if (runs > chunks / 4) runs = chunks / 4;
   return (int)(runs < 1 ? 1 : runs);
 }
-
 // Workgroups that share the adapters of a tile's rows, each a pass over the tile: twice those that there is room
-// for, since a tile may name few, and those without one end at once.  512 rows x 3584 of 32 adapters, mixed, rank 16
+// for (two to a compute unit up to 32 ranks, else one), since a tile may name few, and those without one end at once.  512 rows x 3584 of 32 adapters, mixed, rank 16
 // and 64: 17 and 27 us (one workgroup a tile and run: 66 and 120); of one adapter 9 and 11 either way.
 int project_split(int64_t M, int64_t rank, int64_t adapters, int runs) {
-  int64_t split = 2 * project_slots(rank) / (project_tiles(M, rank) * runs);
+  int64_t split = 2 * (rank <= 32 ? 512 : 256) / (project_tiles(M, rank) * runs);
   if (split > kTileRows) split = kTileRows;
   if (split > adapters) split = adapters;
   return (int)(split < 1 ? 1 : split);
@@ -674,8 +677,9 @@ template <int FMT>
 void project(int64_t M, int64_t K, const uint8_t* a, int64_t lda, const uint8_t* sa, const int32_t* ids,
              int64_t adapters, int64_t rank, const uint16_t* down, int64_t ldd, int64_t stride, const float* alpha,
              float* p, MxPacked packed, float* workspace, hipStream_t stream) {
-  if (M <= kFewRows) {
-    // One rank a workgroup until four fill the chip.
+  if (row_by_row(M, K, rank)) {
+    // One rank a workgroup until four fill the chip (13x8960 rank 8: 3.1 us, with four 4.2; 64x18944 rank 64: 11.5 us
+    // with four, 17.0 with one).
 #define MXFP8_PR(JT)                                                                                            \
   hipLaunchKernelGGL((project_rows_kernel<FMT, JT>), dim3((uint32_t)(M * (rank / JT))), dim3(256), 0, stream,   \
                      (int)K, a, lda, sa, ids, (int)adapters, (int)rank, down, ldd, stride, alpha, p, packed)
@@ -692,6 +696,8 @@ void project(int64_t M, int64_t K, const uint8_t* a, int64_t lda, const uint8_t*
                      dim3((uint32_t)((M + kTileRows - 1) / kTileRows * runs), (uint32_t)((rank + 16 * JC - 1) / (16 * JC)), \
                           (uint32_t)split), dim3(256), 0, stream, (int)M, (int)K, runs, a, lda, sa, ids, (int)adapters, (int)rank, down, ldd, \
                      stride, alpha, to, packed)
+  // As many ranks as there are, up to 64: past them rows are read again (8192x18944 rank 16: 30 us for 16 at a time, 37
+  // for 64; 4096x8960 rank 64: 27 and 17).
   if (rank <= 16) MXFP8_PT(1);
   else if (rank <= 32) MXFP8_PT(2);
   else MXFP8_PT(4);
@@ -704,7 +710,12 @@ void project(int64_t M, int64_t K, const uint8_t* a, int64_t lda, const uint8_t*
   }
 }
 
-// Ranks and columns of a workgroup, and the runs that the rows are split into.
+// Rows of an adapter that a run has at least: with 512, 4096x1536 rank 64 takes 15 us, 3000x1536 rank 128 17 and
+// 1024x1536 rank 16 13 with the join; with 128, 19, 20 and 10; with 1024, 15 (16384x1536 rank 64 64 in place of 49),
+// 22 and 14.
+constexpr int64_t kGradRows = 512;
+// Ranks and columns of a workgroup, and the runs that the rows are split into.  16 ranks by 256 columns, or past 16
+// ranks 32 by 128, which read z less often: 8192x18944 rank 16 42 us against 51, 4096x8960 rank 64 39 against 32.
 struct GradShape {
   int jt, nf, jgroups, ctiles, runs;
 };
@@ -714,11 +725,11 @@ GradShape grad_shape(int64_t M, int64_t C, int64_t rank, int64_t adapters) {
   s.nf = s.jt == 1 ? 16 : 8;
   s.jgroups = (int)((rank + 16 * s.jt - 1) / (16 * s.jt));
   s.ctiles = (int)((C + 16 * s.nf - 1) / (16 * s.nf));
-  // Two workgroups to each of 256 compute units, runs of 128 rows at least to
-  // each adapter, and at most 256 MB of partial sums.
+  // Two workgroups to each of 256 compute units (4096x8960 rank 64: 31 us, with one 45, with four 40), kGradRows to
+  // an adapter and run at least, and at most 256 MB of partial sums.
   const int64_t wgs = (int64_t)s.ctiles * s.jgroups * adapters;
   int64_t runs = 512 / wgs;
-  const int64_t most = M / (128 * adapters), bytes = adapters * rank * C * 4;
+  const int64_t most = M / (kGradRows * adapters), bytes = adapters * rank * C * 4;
   if (runs > most) runs = most;
   if (runs * bytes > (int64_t(256) << 20)) runs = (int64_t(256) << 20) / bytes;
   s.runs = (int)(runs < 1 ? 1 : runs);  // M == 0: one run of no rows, which gives zeros

@@ -472,16 +472,24 @@ Shape shape(int64_t cols) {
   s.waves = (upr + 64 * s.nu - 1) / (64 * s.nu);
   return s;
 }
-// Rows of a batch, as many as fit in 128 registers.
+// Rows of a batch, whose sums share the waits for them, as many as 128 registers
+// hold: forward 16384x3584 bf16 55 us with 4, 57 with 2, 63 with 1; 8192x3584 fp32
+// 32 with 2 or 1, 70 with 4 (spills).  Backward bf16 59 with 2, 62 with 1, 157
+// with 4; 8192x3584 fp32 53 with 1, 56 with 2.
 template <typename T>
-constexpr int forward_batch(int nu) {
-  return nu == 1 ? (sizeof(T) == 2 ? 4 : 2) : 1;
+constexpr int forward_batch() {
+  return sizeof(T) == 2 ? 4 : 2;
 }
-constexpr int backward_batch(int nu) { return nu == 1 ? 2 : 1; }
+template <typename T>
+constexpr int backward_batch(int nu) {
+  return nu == 1 && sizeof(T) == 2 ? 2 : 1;
+}
 // Workgroups: up to 16 waves to each of 256 compute units, whatever the device has
-// (the size of the backward pass's workspace goes by it).
+// (the size of the backward pass's workspace goes by it).  Half as many: forward
+// 16384x3584 bf16 65 us in place of 54; twice as many 56, backward 67 in place of 59.
+int64_t most_groups(int waves) { return 256 * (16 / waves > 1 ? 16 / waves : 1); }
 int64_t groups(int64_t rows, int rb, int waves) {
-  const int64_t need = (rows + rb - 1) / rb, most = 256 * (16 / waves > 1 ? 16 / waves : 1);
+  const int64_t need = (rows + rb - 1) / rb, most = most_groups(waves);
   return need < most ? need : most;
 }
 
@@ -490,14 +498,15 @@ void forward(const void* x, int64_t rows, int64_t cols, int64_t ldx, const float
              uint8_t* y, int64_t ldy, uint8_t* ys, uint8_t* kept, int64_t ldk, uint8_t* ks, float* rstd,
              hipStream_t stream) {
   const Shape s = shape(cols);
-#define MXFP8_F(NU)                                                                                               \
-  hipLaunchKernelGGL((forward_kernel<InT, FMT, CEIL, NU, forward_batch<InT>(NU)>),                                        \
-                     dim3((uint32_t)groups(rows, forward_batch<InT>(NU), s.waves)), dim3(64 * s.waves), 0, stream,        \
-                     static_cast<const InT*>(x), ldx, rows, (uint32_t)(cols / kLaneElems), w, b, eps, y, ldy, ys, \
-                     kept, ldk, ks, rstd)
-  if (s.nu == 1) MXFP8_F(1);
-  else if (s.nu == 2) MXFP8_F(2);
-  else MXFP8_F(4);
+#define MXFP8_F(NU, RB)                                                                                           \
+  hipLaunchKernelGGL((forward_kernel<InT, FMT, CEIL, NU, RB>), dim3((uint32_t)groups(rows, RB, s.waves)),         \
+                     dim3(64 * s.waves), 0, stream, static_cast<const InT*>(x), ldx, rows,                        \
+                     (uint32_t)(cols / kLaneElems), w, b, eps, y, ldy, ys, kept, ldk, ks, rstd)
+  // While each row can have a workgroup, a batch would only lengthen it: 1x3584 bf16 3.0 us, with 4 5.5.
+  if (s.nu == 1 && rows <= most_groups(s.waves)) MXFP8_F(1, 1);
+  else if (s.nu == 1) MXFP8_F(1, forward_batch<InT>());
+  else if (s.nu == 2) MXFP8_F(2, 1);
+  else MXFP8_F(4, 1);
 #undef MXFP8_F
 }
 
@@ -507,7 +516,7 @@ void backward(const uint8_t* kept, int64_t ldk, const uint8_t* ks, const float* 
               hipStream_t stream) {
   const Shape s = shape(cols);
 #define MXFP8_B(NU)                                                                                                   \
-  hipLaunchKernelGGL((backward_kernel<T, FMT, NU, backward_batch(NU)>), dim3((uint32_t)parts), dim3(64 * s.waves), 0,       \
+  hipLaunchKernelGGL((backward_kernel<T, FMT, NU, backward_batch<T>(NU)>), dim3((uint32_t)parts), dim3(64 * s.waves), 0,       \
                      stream, kept, ldk, ks, rstd, w, static_cast<const T*>(dy), lddy, rows,                           \
                      (uint32_t)(cols / kLaneElems), static_cast<T*>(dx), lddx, part)
   if (s.nu == 1) MXFP8_B(1);
@@ -533,7 +542,7 @@ void launch_mx_layernorm_forward(const void* x, int dtype, int64_t rows, int64_t
 
 int64_t layernorm_backward_parts(int64_t rows, int64_t cols) {
   const Shape s = shape(cols);
-  return groups(rows, backward_batch(s.nu), s.waves);
+  return groups(rows, backward_batch<uint16_t>(s.nu), s.waves);
 }
 
 void launch_mx_layernorm_backward(const uint8_t* kept, int64_t ldk, const uint8_t* ks, const float* rstd, int fmt,
