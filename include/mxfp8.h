@@ -3,7 +3,8 @@
  * power-of-two (E8M0) scales, and the block-scaled FP8 GEMM that consumes it,
  * for AMD Instinct MI355X (gfx950).  Next to them: the MX GEMM on 32-element
  * scales, two-orientation quantizers, an fp32-scale variant of the quantizers
- * and the GEMM, and the GaussWS weight sampler.
+ * and the GEMM, and the GaussWS weight sampler; MXFP4 weights with SwiGLU,
+ * RMSNorm and LayerNorm on MX codes, and low-rank adapters beside their product.
  *
  * Sources (web pages, cited by title and section):
  *   [FP8F] "FP8 Formats for Deep Learning", review page, "Core claim": the
@@ -520,9 +521,12 @@ int64_t mx_adapter_project_workspace(int64_t M, int64_t K, int64_t rank);
  * mxfp4_gemm_adapted -- mxfp4_gemm and each row's adapter:
  *   p[m] = alpha[a] * down[a] x[m],  C[m] = W x[m] + up[a] p[m],  a = ids[m],
  * x[m] row m of A and W = B.  p is an output too (the gradient of up needs it);
- * its 24 bits enter the second product, which is added in fp32 before C is
- * rounded.  All other arguments and requirements are those of mxfp4_gemm.
- * With N == 0 p is computed alone.
+ * all its bits enter the second product, or its leading 16 at least where C is
+ * bf16, and that is added in fp32 before C is rounded.  All other arguments and
+ * requirements are those of mxfp4_gemm.  With N == 0 p is computed alone.
+ * A row whose p is not finite gets results that are not finite (NaN, where the
+ * formula may give an infinity), and so does, in the rows of its adapter, a
+ * column of up that is not.
  */
 int mxfp4_gemm_adapted(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, int a_fmt,
                        const uint8_t* a_scales, const uint8_t* b, int64_t ldb, const uint8_t* b_scales,
@@ -540,8 +544,9 @@ int64_t mxfp4_gemm_adapted_workspace(int64_t M, int64_t N, int64_t K, int64_t ra
  *   z: [M][ldz] codes of z_fmt (E4M3, E5M2 or E2M1), z_scales [M][C / 32].
  *   grad: [adapters][rank][C] fp32, or [adapters][C][rank] if transposed; zeros
  *         for an adapter without rows.  16-byte aligned.
- * Requires C % 32 == 0 and ldz <= 2^22.  Sums are in fp32 and in a fixed order:
- * the same inputs give the same bits.
+ * Requires C % 32 == 0 and ldz <= 2^22.  Products take all bits of p, sums are
+ * in fp32 and in a fixed order: the same inputs give the same bits.  An infinity
+ * in p or z makes NaN of the sums that it enters.
  */
 int mx_adapter_grad(int64_t M, int64_t C, const uint8_t* z, int64_t ldz, int z_fmt, const uint8_t* z_scales,
                     const float* p, int64_t rank, const int32_t* ids, int64_t adapters, int transposed, float* grad,

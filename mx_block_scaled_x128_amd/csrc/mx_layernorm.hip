@@ -20,7 +20,11 @@
 // 8 elements (up to 16 waves; then 2 or 4 units to a lane), with the next RB
 // rows on their way.  A lane keeps its columns, so w, b, and the backward
 // pass's sums dw and db stay in its registers.  Each tensor is read and written
-// once: HBM bounds both passes.
+// once: HBM bounds both passes.  16384x3584 bf16, kept: forward 57 us (238 MB, 4.2
+// TB/s of the 5.1 that a copy reaches; the rest is instructions, two casts and
+// three passes over the registers), backward 59 and 4.7 for the sums (293 MB, 5.0
+// TB/s).  515x8960 fp32 backward 16 us (42 MB): 258 workgroups of two rows, the
+// latency of each row's reads and its sums.
 #include "mx_common.hpp"
 #include "mx_launch.hpp"
 
