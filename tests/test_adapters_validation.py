@@ -141,9 +141,9 @@ def test_mx_adapter_grad():
 
 
 def test_adapter_project_workspace():
-    for bad in ((-1, 256, 16), (64, 200, 16), (64, 256, 9), (0, 256, 16), (2 ** 27 + 1, 256, 16), (256, 18944, 64)):
+    for bad in ((-1, 256, 16), (64, 200, 16), (64, 256, 9), (0, 256, 16), (2 ** 27 + 1, 256, 16), (64, 18944, 64)):
         assert mx.mx_adapter_project_workspace(*bad) == 0, bad
-    for M, K, rank in ((257, 1 << 22, 256), (65536, 18944, 256), (8192, 18944, 16), (1 << 27, 128, 8)):
+    for M, K, rank in ((256, 18944, 64), (257, 1 << 22, 256), (65536, 18944, 256), (8192, 18944, 16), (1 << 27, 128, 8)):
         assert mx.mx_adapter_project_workspace(M, K, rank) <= 512 * 128 * rank * 4
 
 
