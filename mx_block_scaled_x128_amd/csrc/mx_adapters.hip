@@ -355,9 +355,10 @@ __global__ __launch_bounds__(256) void project_join_kernel(const nt_f32x4* __res
 // the JT ranks from JT m of its rows, rank i of each lane's for fragment i.  The
 // scales of the 32 rows come with one load and go to their lanes from there.
 // What bounds it: up to 16 ranks the reads, 17 load instructions for 32 rows
-// (8192x18944 rank 16 40 us, 3.9 TB/s; 8192x3584 16); past that each 32 ranks
-// read z again (4096x8960 rank 64 27 us: 94 MB fetched for 37, 3.5 TB/s, matrix
-// instructions 25 % of the time).
+// (8192x18944 rank 16 40 us, 3.9 TB/s; 8192x3584 16); past that instructions, a
+// third of them p's split into its parts (4096x8960 rank 64 27 us; matrix
+// instructions 25 % of the time; each 32 ranks read z again, but side by side on
+// one XCD, from its cache, they took as long).
 //
 // The runs' sums go to `part` and are joined in order; with one run they are
 // the result.
