@@ -530,9 +530,10 @@ __device__ __forceinline__ uint32_t opaque(uint32_t x) {
 // PARTS of p: two, 16 bits, where C is bf16 (its rounding is 2^7 times as large),
 // three, all of it, for fp32.
 //
-// It costs the ids' and up's latency and the instructions of a tile, 3 us for
-// each: 8192x18944x3584 rank 16 430 us in place of 397, 4096x8960x1536 rank 16 63
-// and rank 64 72 in place of 55, 512x3584x3584 rank 16 15 in place of 13.  Each
+// It costs the ids' and up's latency and the instructions of a tile, 2 us for
+// each, of which 1 without any adapter: 8192x18944x3584 416 us alone, 436 with
+// rank 16 and 476 with rank 64; 4096x8960x1536 55, 60 and 73; 4096x1536x8960 58,
+// 61 and 63; 512x3584x3584 rank 16 15 in place of 13.  Each
 // further adapter of a wave's rows takes 0.4 us (512 rows, 32 adapters mixed: 27
 // us; rank 64: 68), bound by its matrix instructions and the rows of up, of which
 // 16 ranks are 32 bytes.
@@ -937,13 +938,6 @@ __device__ __forceinline__ void gemm_tile(int M, int N, int K, const uint8_t* __
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           v4f v = v4f{acc[mt][nt][4 * q], acc[mt][nt][4 * q + 1], acc[mt][nt][4 * q + 2], acc[mt][nt][4 * q + 3]};
-          if constexpr (ADAPT) {
-            if (spoils) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (spoilt[mt][nt] >> (8 * q + 4 * g + i) & 1) v[i] = __builtin_nanf("");
-            }
-          }
           if constexpr (F32)
             *reinterpret_cast<v4f*>(stg + (lane & 31) * P + (((nt * 8 + 2 * q + g) ^ (lane & 15)) * 16)) = v;
           else
@@ -968,6 +962,30 @@ __device__ __forceinline__ void gemm_tile(int M, int N, int K, const uint8_t* __
               }
           }
         }
+      }
+    }
+    // Columns that a value of up leaves without a result, over what was written (a
+    // choice among the values above costs 2 us a tile, spoilt or not).
+    if constexpr (ADAPT) {
+      if (spoils) {
+        __builtin_amdgcn_s_waitcnt(0);
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int m = m0 + wm * WM + mt * 32 + (lane & 31), n = n0 + wn * WN + nt * 32;
+            if (m < M) {
+#pragma nounroll
+              for (uint32_t left = spoilt[mt][nt]; left; left &= left - 1) {
+                const int at = n + __builtin_ctz(left);
+                if (at < N) {
+                  if constexpr (F32) C[(int64_t)m * ldc + at] = __builtin_nanf("");
+                  else C[(int64_t)m * ldc + at] = 0x7FC0;
+                }
+              }
+            }
+          }
       }
     }
   };
