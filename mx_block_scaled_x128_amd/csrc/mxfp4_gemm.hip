@@ -561,7 +561,7 @@ struct FirstAdapters {
     steps = (ad.rank + 15) >> 4;
     po = lane * 16;
     // m0 is a multiple of 32
-    rp = descriptor(reinterpret_cast<const uint8_t*>(ad.packed) + (int64_t)(m0 >> 5) * steps * 3072);
+    rp = descriptor(reinterpret_cast<const uint8_t*>(ad.packed) + (int64_t)(m0 >> 5) * steps * (3 * 1024));
 #pragma unroll
     for (int i = 0; i < MT; ++i) id[i] = m0 + 32 * i + (lane & 31) < M ? ad.ids[m0 + 32 * i + (lane & 31)] : -1;
     get_p(m0, M, 0, first);
