@@ -50,9 +50,10 @@ bool adapter_extents(int64_t M, int64_t adapters, int64_t rank) {
 bool adapter_ld(int64_t ld, int64_t row, int64_t stride) {
   return ld >= row && ld % 8 == 0 && ld <= kMaxGemmLd && stride >= 0 && stride % 8 == 0;
 }
-// p in the order in which the product's tiles read it; a product of few rows does without.
-int64_t packed_bytes(int64_t M, int64_t N, int64_t rank) {
-  return N > 0 && (M > 16 || N > mxfp8::kFewRowsN) ? mxfp8::adapter_packed_bytes(M, rank) : 0;
+// p in the order in which the product's tiles read it; none where the few-row kernel takes the product on every device
+// (one without compute units stands for that), since the device of the workspace's query need not be the call's.
+int64_t packed_bytes(int64_t M, int64_t N, int64_t K, int64_t rank) {
+  return N > 0 && !mxfp8::mxfp4_few_rows(M, N, K, 0) ? mxfp8::adapter_packed_bytes(M, rank) : 0;
 }
 bool grad_extents(int64_t M, int64_t C, int64_t rank, int64_t adapters) {
   if (!adapter_extents(M, adapters, rank) || C < 0 || C > INT32_MAX / 2 || C % 32 != 0) return false;
@@ -296,7 +297,7 @@ int mx_adapter_project(int64_t M, int64_t K, const uint8_t* a, int64_t lda, int 
 int64_t mxfp4_gemm_adapted_workspace(int64_t M, int64_t N, int64_t K, int64_t rank) {
   if (N < 0 || N > INT32_MAX / 2 || !adapter_extents(M, 0, rank) || M == 0) return 0;
   if (K < 0 || K > INT32_MAX / 2 || K % 128 != 0) return 0;
-  return packed_bytes(M, N, rank) + mxfp8::adapter_project_workspace(M, K, rank);
+  return packed_bytes(M, N, K, rank) + mxfp8::adapter_project_workspace(M, K, rank);
 }
 
 int mxfp4_gemm_adapted(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, int a_fmt,
@@ -327,8 +328,8 @@ int mxfp4_gemm_adapted(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_
     return MXFP8_ERR_ALIAS;
   (void)hipGetLastError();
   // The packed p first (a whole number of kilobytes), then the projection's runs.
-  uint16_t* packed = packed_bytes(M, N, rank) > 0 ? static_cast<uint16_t*>(workspace) : nullptr;
-  float* runs = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + packed_bytes(M, N, rank));
+  uint16_t* packed = packed_bytes(M, N, K, rank) > 0 ? static_cast<uint16_t*>(workspace) : nullptr;
+  float* runs = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + packed_bytes(M, N, K, rank));
   mxfp8::launch_mx_adapter_project(M, K, a, lda, a_fmt, a_scales, ids, adapters, rank, down, ldd, down_stride, alpha, p,
                                    packed, runs, (hipStream_t)stream);
   if (N > 0)

@@ -50,10 +50,13 @@ void launch_mx_layernorm_backward(const uint8_t* kept, int64_t ldk, const uint8_
 void launch_mxfp4_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, int a_fmt, const uint8_t* sa,
                        const uint8_t* b, int64_t ldb, const uint8_t* sb, void* c, int64_t ldc, int c_dtype,
                        hipStream_t stream);
-// The same and, for row m with a = ids[m] in 0 .. adapters - 1, up[a] p[m] added: p [M][rank], and packed, adapter
-// a's [N][ldu] bf16 from up + a stride.  rank, ldu and stride are multiples of 8, ldu <= 2^22.  With up to 16 rows
-// and kFewRowsN columns packed is not read.
+// Whether the few-row kernel takes that product on a device of `cus` compute units; tiles do otherwise.  Up to 16 rows
+// it is the same on every device, so what a caller's workspace holds can go by it.
 constexpr int64_t kFewRowsN = int64_t(1) << 26;
+bool mxfp4_few_rows(int64_t M, int64_t N, int64_t K, int64_t cus);
+// The same and, for row m with a = ids[m] in 0 .. adapters - 1, up[a] p[m] added: p [M][rank], and packed, adapter
+// a's [N][ldu] bf16 from up + a stride.  rank, ldu and stride are multiples of 8, ldu <= 2^22.  The few-row kernel
+// does not read packed.
 void launch_mxfp4_gemm_adapted(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, int a_fmt,
                                const uint8_t* sa, const uint8_t* b, int64_t ldb, const uint8_t* sb, const int32_t* ids,
                                int64_t adapters, int64_t rank, const float* p, const uint16_t* packed,
@@ -67,7 +70,7 @@ void launch_mx_adapter_project(int64_t M, int64_t K, const uint8_t* a, int64_t l
                                int64_t stride, const float* alpha, float* p, uint16_t* packed, float* workspace,
                                hipStream_t stream);
 int64_t adapter_project_workspace(int64_t M, int64_t K, int64_t rank);
-// p as the product's tiles read it (packed above; may be null where only few rows follow).
+// p as the product's tiles read it (packed above; may be null where the few-row kernel follows).
 int64_t adapter_packed_bytes(int64_t M, int64_t rank);
 // out[a] = the sum over the rows m of adapter a of p[m] (x) z[m], [rank][C], or [C][rank] if transposed.  C % 32 ==
 // 0, all extents >= 1.  Bytes of workspace, and workgroups (fewer than 2^24).

@@ -48,6 +48,22 @@ template <int AFMT, typename AD>
 void gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const uint8_t* sa, const uint8_t* b,
           int64_t ldb, const uint8_t* sb, void* c, int64_t ldc, int c_dtype, AD ad, hipStream_t stream);
 
+// LDS of the few-row kernel, in bytes: A's scales, B's scales, A, each in
+// whole kilobytes (a copy fills whole ones); the partial sums of the waves
+// take their place at the end.
+template <typename I>
+__host__ __device__ constexpr I kilo(I n) {
+  return (n + 1023) & ~I(1023);
+}
+template <int AFMT, int MT, int NT, int WAVES, bool ALDS>
+constexpr int64_t few_rows_lds(int64_t rows, int64_t K) {
+  const int64_t a = AFMT == kE2M1 ? K / 2 : K;
+  const int64_t in = kilo(16 * MT * (K / 32)) + kilo(16 * NT * (K / 32)) + (ALDS ? kilo(rows * a) : 0);
+  const int64_t out = WAVES > 1 ? WAVES * MT * NT * 1024 : 0;
+  return in > out ? in : out;
+}
+constexpr int64_t kFewRowsLds = 150 * 1024;
+
 #if MXFP4_GEMM_FMT >= 0
 
 typedef int v4i __attribute__((ext_vector_type(4)));
@@ -157,18 +173,6 @@ __device__ __forceinline__ void copy_to_lds(const uint8_t* p, int n, uint8_t* to
   }
 }
 #endif
-
-// LDS of the few-row kernel, in bytes: A's scales, B's scales, A, each in
-// whole kilobytes (a copy fills whole ones); the partial sums of the waves
-// take their place at the end.
-__host__ __device__ constexpr int kilo(int n) { return (n + 1023) & ~1023; }
-template <int AFMT, int MT, int NT, int WAVES, bool ALDS>
-__host__ __device__ inline int few_rows_lds(int rows, int K) {
-  const int a = AFMT == kE2M1 ? K / 2 : K;
-  const int in = kilo(16 * MT * (K / 32)) + kilo(16 * NT * (K / 32)) + (ALDS ? kilo(rows * a) : 0);
-  const int out = WAVES > 1 ? WAVES * MT * NT * 1024 : 0;
-  return in > out ? in : out;
-}
 
 #if defined(__HIP_DEVICE_COMPILE__)
 // The next adapter that any lane's rows name, or -1; its rows are crossed off
@@ -452,13 +456,11 @@ __global__ __launch_bounds__(WAVES * 64) void few_rows_kernel(int M, int N, int 
 #endif
 }
 
-constexpr int kFewRowsLds = 150 * 1024;
-
 template <int AFMT, int MT, int NT, int WAVES, int U, bool ALDS, typename AD>
 void few_rows(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const uint8_t* sa, const uint8_t* b,
               int64_t ldb, const uint8_t* sb, void* c, int64_t ldc, int c_dtype, AD ad, hipStream_t stream) {
   const dim3 grid((uint32_t)(((N + 16 * NT - 1) / (16 * NT)) * ((M + 16 * MT - 1) / (16 * MT))));
-  const int lds = few_rows_lds<AFMT, MT, NT, WAVES, ALDS>((int)(M < 16 * MT ? M : 16 * MT), (int)K);
+  const uint32_t lds = (uint32_t)few_rows_lds<AFMT, MT, NT, WAVES, ALDS>(M < 16 * MT ? M : 16 * MT, K);
   if (c_dtype == 0)
     hipLaunchKernelGGL((few_rows_kernel<AFMT, MT, NT, WAVES, U, ALDS, float, AD>), grid, dim3(WAVES * 64), lds, stream,
                        (int)M, (int)N, (int)K, a, lda, sa, b, ldb, sb, static_cast<float*>(c), ldc, ad);
@@ -1148,27 +1150,13 @@ void tiles(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const
 template <int AFMT, typename AD>
 void gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const uint8_t* sa, const uint8_t* b,
           int64_t ldb, const uint8_t* sb, void* c, int64_t ldc, int c_dtype, AD ad, hipStream_t stream) {
-  // Few rows or tiles.  Up to 16 rows B crosses a CU's load path once however
-  // wide it is.  Beyond, the few-row kernel is the faster one while its
-  // workgroups all fit on the chip, one to a CU, since it has four times or
-  // more as many of them as there are tiles; with a second round of them the
-  // tiles win (us, few rows / tiles, E4M3 x E2M1 and E2M1 pairs, one round:
-  // 64x3584x8960 17.2 / 26.7, 12.6 / 18.8; 128x3584x3584 8.8 / 13.4, 7.8 / 9.5;
-  // 512x1024x1024 5.5 / 6.1, 4.9 / 5.2; 32x14336x4096 12.2 / 14.1, 10.0 / 10.4;
-  // more: 40x16384x3584 17 / 13, 12.1 / 10.0; 256x3584x3584 19.2 / 14.2,
-  // 15.7 / 10.3; 1024x1024x1024 9.1 / 6.2, 8.4 / 5.3).  The few-row kernel
-  // takes as many scales as fit in LDS and 2^26 rows of B (its grid).
   const int chunks = (int)(K / 128);
-  const int64_t n16 = (N + 15) / 16, pairs = ((N + 31) / 32) * ((M + 31) / 32);
-  const int64_t wide = ((N + 63) / 64) * ((M + 31) / 32), cus = device_cus();
-  const bool few = (M <= 16 ? N <= kFewRowsN : wide <= cus) &&
-                   (M <= 16 || pairs <= cus ? few_rows_lds<AFMT, 2, 2, 4, false>(0, (int)K)
-                                            : few_rows_lds<AFMT, 2, 4, 4, false>(0, (int)K)) <= kFewRowsLds;
+  const int64_t n16 = (N + 15) / 16, pairs = ((N + 31) / 32) * ((M + 31) / 32), cus = device_cus();
 #define MXFP4_FEW(MT, NT, WAVES, U)                                                                           \
-  (few_rows_lds<AFMT, MT, NT, WAVES, true>((int)(M < 16 * MT ? M : 16 * MT), (int)K) <= kFewRowsLds           \
+  (few_rows_lds<AFMT, MT, NT, WAVES, true>(M < 16 * MT ? M : 16 * MT, K) <= kFewRowsLds                       \
        ? few_rows<AFMT, MT, NT, WAVES, U, true>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, ad, stream) \
        : few_rows<AFMT, MT, NT, WAVES, U, false>(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, c_dtype, ad, stream))
-  if (few) {
+  if (mxfp4_few_rows(M, N, K, cus)) {
     if (M <= 16) {
       // Two waves a workgroup where a run of K is short or the workgroups are
       // many (E4M3, two / four waves: 1x8960x1536 3.8 / 4.2 us, 1x18944x3584
@@ -1232,6 +1220,25 @@ MXFP4_GEMM(MXFP4_GEMM_FMT, NoAdapters)
 }  // namespace mxfp4_detail
 
 #if MXFP4_GEMM_FMT == 3 || MXFP4_GEMM_FMT < 0
+// Few rows or tiles.  Up to 16 rows B crosses a CU's load path once however
+// wide it is.  Beyond, the few-row kernel is the faster one while its
+// workgroups all fit on the chip, one to a CU, since it has four times or
+// more as many of them as there are tiles; with a second round of them the
+// tiles win (us, few rows / tiles, E4M3 x E2M1 and E2M1 pairs, one round:
+// 64x3584x8960 17.2 / 26.7, 12.6 / 18.8; 128x3584x3584 8.8 / 13.4, 7.8 / 9.5;
+// 512x1024x1024 5.5 / 6.1, 4.9 / 5.2; 32x14336x4096 12.2 / 14.1, 10.0 / 10.4;
+// more: 40x16384x3584 17 / 13, 12.1 / 10.0; 256x3584x3584 19.2 / 14.2,
+// 15.7 / 10.3; 1024x1024x1024 9.1 / 6.2, 8.4 / 5.3).  The few-row kernel
+// takes as many scales as fit in LDS and 2^26 rows of B (its grid).
+bool mxfp4_few_rows(int64_t M, int64_t N, int64_t K, int64_t cus) {
+  using namespace mxfp4_detail;
+  const int64_t pairs = ((N + 31) / 32) * ((M + 31) / 32), wide = ((N + 63) / 64) * ((M + 31) / 32);
+  // A's own place in LDS is not counted: rows that do not fit stay in memory.
+  return (M <= 16 ? N <= kFewRowsN : wide <= cus) &&
+         (M <= 16 || pairs <= cus ? few_rows_lds<0, 2, 2, 4, false>(0, K)
+                                  : few_rows_lds<0, 2, 4, 4, false>(0, K)) <= kFewRowsLds;
+}
+
 namespace {
 template <typename AD>
 void any_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, int a_fmt, const uint8_t* sa,
