@@ -327,9 +327,11 @@ int mxfp4_gemm_adapted(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_
   if (shared({c, p, work ? workspace : nullptr}, {a, b, a_scales, b_scales, ids, down, up, alpha}))
     return MXFP8_ERR_ALIAS;
   (void)hipGetLastError();
-  // The packed p first (a whole number of kilobytes), then the projection's runs.
-  uint16_t* packed = packed_bytes(M, N, K, rank) > 0 ? static_cast<uint16_t*>(workspace) : nullptr;
-  float* runs = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + packed_bytes(M, N, K, rank));
+  // The packed p first (a whole number of kilobytes), then the projection's runs.  It is written where the tiles read it.
+  const int64_t before = packed_bytes(M, N, K, rank);
+  const bool tiles = before > 0 && !mxfp8::mxfp4_few_rows(M, N, K, mxfp8::device_cus());
+  uint16_t* packed = tiles ? static_cast<uint16_t*>(workspace) : nullptr;
+  float* runs = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + before);
   mxfp8::launch_mx_adapter_project(M, K, a, lda, a_fmt, a_scales, ids, adapters, rank, down, ldd, down_stride, alpha, p,
                                    packed, runs, (hipStream_t)stream);
   if (N > 0)
