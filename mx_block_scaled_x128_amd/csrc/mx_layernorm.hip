@@ -232,14 +232,15 @@ __global__ __launch_bounds__(1024) void forward_kernel(
         r = __builtin_fmaf(r * 0.5f, __builtin_fmaf(-t, r, 1.0f) - low * r, r);
       }
       const float shift = -delta * r;
-      // Squares that overflow in fp32 or vanish there, or a row so nearly of equal
+      // Squares that overflow in fp32 or vanish there, an eps that takes the
+      // variance out of its range, or a row so nearly of equal
       // values that m0's rounding is a good part of them, a sixteenth and more, and
       // eps does not cover that: what is left when delta^2 is taken out would have
       // lost the bits that cancel.  The row scaled by a power of two, once more in
       // 64 bits (the same branch in all waves).
       double mean = 0.0, rr = 0.0;
       float scale = 0.0f;
-      if (in && (!(var > 0.9375f * e[2 * k + 1] * inv_n) || e[2 * k + 1] + eps * (float)(upr * 8) < 0x1p-100f)) {
+      if (in && (!(var > 0.9375f * e[2 * k + 1] * inv_n && var < 0x1p127f) || e[2 * k + 1] + eps * (float)(upr * 8) < 0x1p-100f)) {
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < NU; ++i) {

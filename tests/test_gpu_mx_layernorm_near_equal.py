@@ -1,10 +1,10 @@
-"""LayerNorm of rows whose values are nearly equal and far from zero: what m0's rounding leaves is then as large as the
-deviation itself, or larger.  Tolerances as in test_gpu_mx_layernorm."""
+"""LayerNorm of rows whose values are nearly equal and far from zero, where what m0's rounding leaves is as large as the
+deviation itself, or larger; and of the largest eps.  Tolerances as in test_gpu_mx_layernorm."""
 import numpy as np
 import pytest
 
 import mx_block_scaled_x128_amd as mx
-from test_gpu_mx_layernorm import T, U, check_codes, close, normalised, tensor, xh_error
+from test_gpu_mx_layernorm import T, U, check_codes, close, given, normalised, tensor, xh_error
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +45,14 @@ def test_equal_but_for_a_few_steps_of_bf16(rows, cols):
         y, ys, kept = mx.layernorm_mx(x, None, None, eps)
         close(kept.rstd, r, (T / 2 + 4) * U * r)
         check_codes(y, ys, xh, xh_error(xh), mx.E4M3, mx.RULE_CEIL)
+
+
+@pytest.mark.parametrize("rows,cols", [(5, 64), (1100, 3584), (5, 9216)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_the_largest_eps(rows, cols, dtype):
+    """eps = 3.4e38, the largest that is taken: the variance of some rows takes the sum past fp32's range."""
+    x = given((rows, cols), 2.0 ** np.array([0, 40, 58, 59, 60] * rows)[:rows, None], 7, dtype)
+    xh, r = normalised(x.astype(np.float64), float(np.float32(3.4e38)))
+    y, ys, kept = mx.layernorm_mx(tensor(x, dtype), None, None, 3.4e38)
+    close(kept.rstd, r, (T / 2 + 4) * U * r)
+    check_codes(y, ys, xh, xh_error(xh), mx.E4M3, mx.RULE_CEIL)
