@@ -521,9 +521,9 @@ int64_t mx_adapter_project_workspace(int64_t M, int64_t K, int64_t rank);
  * mxfp4_gemm_adapted -- mxfp4_gemm and each row's adapter:
  *   p[m] = alpha[a] * down[a] x[m],  C[m] = W x[m] + up[a] p[m],  a = ids[m],
  * x[m] row m of A and W = B.  p is an output too (the gradient of up needs it);
- * all its bits enter the second product, or its leading 16 at least where C is
- * bf16, and that is added in fp32 before C is rounded.  All other arguments and
- * requirements are those of mxfp4_gemm.  With N == 0 p is computed alone.
+ * all its bits enter the second product, which is added in fp32 before C is
+ * rounded.  All other arguments and requirements are those of mxfp4_gemm.  With
+ * N == 0 p is computed alone.
  * A row whose p is not finite gets results that are not finite (NaN, where the
  * formula may give an infinity), and so does, in the rows of its adapter, a
  * column of up that is not.

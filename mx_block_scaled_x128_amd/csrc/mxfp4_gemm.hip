@@ -14,7 +14,7 @@
 // half the rate at most.  E2M1 pairs lose nothing.
 //
 // With adapters, row m of C starts from up[a] p[m], a = ids[m], in place of zero:
-// a few bf16 matrix instructions per tile (p in two or three parts) while
+// a few bf16 matrix instructions per tile (p in three parts, all its bits) while
 // the first operands are on their way.
 #include "mx_common.hpp"
 #include "mx_launch.hpp"
@@ -529,19 +529,21 @@ __device__ __forceinline__ uint32_t opaque(uint32_t x) {
 // they leave without a result; add() says whether there are any.  (Choosing row
 // by row what to add would take the accumulators through the vector registers.)
 //
-// PARTS of p: two, 16 bits, where C is bf16 (its rounding is 2^7 times as large),
-// three, all of it, for fp32.
+// All three parts of p, also where C is bf16: ranks that cancel can leave less of
+// each than C's rounding, and a row's bits of p must not go by its batch.  (With
+// the leading two, 16 bits: 8192x18944x3584 rank 64 469 us in place of 483, 4096
+// rows x 3584 x 3584 of 32 adapters, mixed, rank 64 154 in place of 176.)
 //
 // It costs the ids' and up's latency and the instructions of a tile, 2 us for
-// each, of which 1 without any adapter: 8192x18944x3584 416 us alone, 436 with
-// rank 16 and 476 with rank 64; 4096x8960x1536 55, 60 and 73; 4096x1536x8960 58,
-// 61 and 63; 512x3584x3584 rank 16 15 in place of 13.  Each
-// further adapter of a wave's rows takes 0.4 us (512 rows, 32 adapters mixed: 27
-// us; rank 64: 68), bound by its matrix instructions and the rows of up, of which
-// 16 ranks are 32 bytes.
-template <int PARTS, int MT, int NT>
+// each, of which 1 without any adapter: 8192x18944x3584 408 us alone, 432 with
+// rank 16 and 483 with rank 64; 4096x8960x1536 50, 57 and 70; 4096x1536x8960 55,
+// 60 and 60; 512x3584x3584 rank 16 13.6 in place of 12.5.  Each further adapter of
+// a wave's rows takes 0.4 us (512 rows, 32 adapters mixed: 29 us; rank 64: 73),
+// bound by its matrix instructions and the rows of up, of which 16 ranks are 32
+// bytes.
+template <int MT, int NT>
 struct FirstAdapters {
-  static constexpr int LISTS = (MT + 1) / 2;
+  static constexpr int PARTS = 3, LISTS = (MT + 1) / 2;
   struct P {
     v4i p[MT][PARTS];
   };
@@ -992,8 +994,7 @@ __device__ __forceinline__ void gemm_tile(int M, int N, int K, const uint8_t* __
     }
   };
 
-  // p's leading 16 bits are 2^-16 of it off, 24 none; bf16 results round by 2^-8.
-  [[maybe_unused]] std::conditional_t<ADAPT, FirstAdapters<sizeof(OutT) == 2 ? 2 : 3, MT, NT>, NoAdapters> lead;
+  [[maybe_unused]] std::conditional_t<ADAPT, FirstAdapters<MT, NT>, NoAdapters> lead;
   if constexpr (ADAPT) {
     lead.ask(ad, M, m0 + wm * WM, lane);
     __builtin_amdgcn_sched_barrier(0);
