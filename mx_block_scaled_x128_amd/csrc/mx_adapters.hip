@@ -740,9 +740,12 @@ GradShape grad_shape(int64_t M, int64_t C, int64_t rank, int64_t adapters) {
   // an adapter and run at least, and at most 256 MB of partial sums.
   const int64_t wgs = (int64_t)s.ctiles * s.jgroups * adapters;
   int64_t runs = 512 / wgs;
-  const int64_t most = M / (kGradRows * adapters), bytes = adapters * rank * C * 4;
+  const int64_t most = M / (kGradRows * adapters);
   if (runs > most) runs = most;
-  if (runs * bytes > (int64_t(256) << 20)) runs = (int64_t(256) << 20) / bytes;
+  if (runs > 1) {  // then there are at most 256 workgroups to a run, whose sums' bytes fit in 64 bits
+    const int64_t bytes = adapters * rank * C * 4;
+    if (runs * bytes > (int64_t(256) << 20)) runs = (int64_t(256) << 20) / bytes;
+  }
   s.runs = (int)(runs < 1 ? 1 : runs);  // M == 0: one run of no rows, which gives zeros
   return s;
 }
