@@ -25,7 +25,8 @@ weight from fp32 master weights), mxstress (MX quantization with clamp counts of
 the GEMM alone over N and K; vendorgemm times the GEMM beside the FP8 products
 of the ROCm BLAS library (torch._scaled_mm) on the same shapes; mxops times the MX
 operators (MXFP4 quantizer and product, transposed quantizers, SwiGLU, RMSNorm)
-case by case; copy times a plain 256 MiB device copy.
+case by case, and mxadapters LayerNorm and the low-rank adapters beside that product;
+copy times a plain 256 MiB device copy.
 
 Usage: python bench.py [--gpus 1] [--steps K] [--warmup W] [--workload NAME] [--no-cpu]
                        [--cpu-rows R]
@@ -46,7 +47,7 @@ FP8_PEAK_TFLOPS = 5000.0   # MI355X dense FP8 MFMA, TFLOP/s
 METRIC = "FP8 quantize GB/s + block-scaled FP8 GEMM TFLOP/s, % of MI355X peak"
 HERE = os.path.dirname(os.path.abspath(__file__))
 WORKLOADS = ["dgrad7b", "fprop1p5b", "wgrad", "mxfprop1p5b", "f32sfprop1p5b", "dualq", "gaussws7b", "mxstress",
-             "copy", "gemmsweep", "vendorgemm", "mxops"]
+             "copy", "gemmsweep", "vendorgemm", "mxops", "mxadapters"]
 
 
 def parse():
@@ -1056,21 +1057,21 @@ MX_CASES = [{"name": "gemm-%dx%dx%d-%s" % (m, n, k, a), "op": "gemm", "m": m, "n
     {"name": "rmsnorm-8192x3584-f32", "op": "rmsnorm", "rows": 8192, "cols": 3584, "dtype": "f32", "pass": "train"}]
 
 
-def bench_mx_ops(args):
-    """The MX operators through their tensor functions, case by case: `warmup` passes and then
-    `steps` passes back to back between one event pair, over three sets of inputs in turn, in
-    three rounds (median; least and largest beside it).  A pass of the quantizers and of the
-    operators with 8-bit outputs holds the call that turns the codes back into values, as in
-    perf/operators.py, whose inputs and byte and operation counts these are.  `value` is the
-    listed cases' sum."""
+def bench_mx_ops(args, name, more):
+    """The MX operators of perf/<name>.py through their tensor functions, case by case: `warmup`
+    passes and then `steps` passes back to back between one event pair, over three sets of inputs
+    in turn, in three rounds (median; least and largest beside it).  A pass of the quantizers and
+    of the operators with 8-bit outputs holds the call that turns the codes back into values, as
+    in that file, whose inputs and byte and operation counts these are.  `value` is the listed
+    cases' sum; the cases `more` are timed beside them."""
     import importlib.util
     import torch
-    spec = importlib.util.spec_from_file_location("operators", os.path.join(HERE, "perf", "operators.py"))
+    spec = importlib.util.spec_from_file_location(name, os.path.join(HERE, "perf", name + ".py"))
     ops = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(ops)
     ops.own = True
     listed, res = ops.listed(), []
-    for case in listed + MX_CASES:
+    for case in listed + more:
         states = [ops.prepare(case, 100 + k) for k in range(3)]
         times = []
         for _ in range(3):
@@ -1093,7 +1094,7 @@ def bench_mx_ops(args):
     return {"metric": "MX operators, sum over the listed cases", "value": round(total, 1), "unit": "us", "n_gpus": 1,
             "steps": args.steps, "warmup": args.warmup, "ms_per_step": round(total / 1e3, 4),
             "higher_is_better": False, "scaling": "weak", "vs_baseline": None, "dtype": "mxfp4/mxfp8",
-            "data": "synthetic", "config": {"workload": "mxops: the listed cases of perf/operators.py"},
+            "data": "synthetic", "config": {"workload": "%s: the listed cases of perf/%s.py" % (args.workload, name)},
             "cases": res, "roofline": None, "cpu_baseline": None}
 
 
@@ -1132,7 +1133,9 @@ def main():
     elif args.workload == "vendorgemm":
         line = bench_vendor_gemm(args)
     elif args.workload == "mxops":
-        line = bench_mx_ops(args)
+        line = bench_mx_ops(args, "operators", MX_CASES)
+    elif args.workload == "mxadapters":
+        line = bench_mx_ops(args, "more_operators", [])
     else:
         line = bench_workload(args)
     print(json.dumps(line), flush=True)
