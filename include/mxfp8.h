@@ -446,9 +446,10 @@ int64_t mx_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
 
 /*
  * mx_layernorm_forward -- y = xh * w + b, xh = (x - mu) * r, mu the row's mean,
- * r = 1 / sqrt(mean over the row of (x - mu)^2 + eps), computed in fp32 (the
- * root in 64 bits; rows whose squares leave fp32's range throughout) and
- * written as MX codes along rows.  x - mu is taken of the values as they are: a
+ * r = 1 / sqrt(mean over the row of (x - mu)^2 + eps), computed in fp32 (in 64
+ * bits for rows whose squares leave fp32's range, or whose values are so nearly
+ * equal that fp32 would lose bits of their deviation) and written as MX codes
+ * along rows.  x - mu is taken of the values as they are: a
  * row far from zero loses nothing more.  r is an fp32 value: infinite for a row
  * of equal values with eps = 0, which makes the row's blocks NaN.
  *   x: [rows][ldx >= cols] fp32 or bf16;  w, b: [cols] fp32, 16-byte aligned;

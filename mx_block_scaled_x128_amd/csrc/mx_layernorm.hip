@@ -12,9 +12,9 @@
 // The mean is taken twice: m0 from the sum of x, and the mean of x - m0, which
 // is what m0's rounding left; the squares are of x - m0, exact where x lies
 // near m0.  So a row far from zero loses nothing but what its own type lost.
-// Arithmetic is in fp32, the root and the joints of the means in 64 bits; rows
-// whose squares leave fp32's range are scaled by a power of two and summed in
-// 64 bits.
+// Arithmetic is in fp32, the root the hardware's and one Newton step; rows whose
+// squares leave fp32's range, or of whose variance m0's rounding is a sixteenth or
+// more, are scaled by a power of two and taken in 64 bits.
 //
 // A workgroup works on RB rows at a time, as many waves as a row has units of
 // 8 elements (up to 16 waves; then 2 or 4 units to a lane), with the next RB
@@ -23,8 +23,8 @@
 // once: HBM bounds both passes.  16384x3584 bf16, kept: forward 57 us (238 MB, 4.2
 // TB/s of the 5.1 that a copy reaches; the rest is instructions, two casts and
 // three passes over the registers), backward 59 and 4.7 for the sums (293 MB, 5.0
-// TB/s).  515x8960 fp32 backward 16 us (42 MB): 258 workgroups of two rows, the
-// latency of each row's reads and its sums.
+// TB/s).  515x8960 fp32 backward 16 us (42 MB): 256 workgroups that take two or
+// three rows one after the other, the latency of each row's reads and its sums.
 #include "mx_common.hpp"
 #include "mx_launch.hpp"
 
